@@ -52,8 +52,9 @@ typedef int32_t kronq_status;
 #define KRONQ_ENUMERIC 6       /* input holds a NaN or an infinity (found on the device) */
 #define KRONQ_ENOMEM 7         /* request larger than a fixed device buffer of the library */
 
-#define KRONQ_F32 0            /* element type codes for kronq_gram */
+#define KRONQ_F32 0            /* element type codes (kronq_gram: F32 and BF16) */
 #define KRONQ_BF16 1
+#define KRONQ_F16 2
 
 /* One side of a randomized (block) Hadamard transform T = (I_b (x) H_block)
  * diag(signs) / sqrt(block) on a dimension dim = b * block; block is a power of
@@ -477,6 +478,140 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
                                          const float* zeros, const int32_t* perm,
                                          const kronq_had* in_side, const kronq_had* out_side,
                                          const float* sg, const float* x, float* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit paged key/value cache: what a decoded token needs between its packed
+ * q, k, v products and its output product (GitHub README: packed deploy path,
+ * single-token decode).  The grid is the column loop's: asymmetric, 16 levels,
+ * one group for each token's head, low bits first as kronq_pack_codes writes
+ * them.
+ *
+ * Cache of one layer (device memory of the caller, any initial content):
+ *   codes : pages x heads x page x dim/2 bytes, keys and values each.  Value d
+ *           of a token's head is in bits 4 (d mod 2) and up of byte d / 2.
+ *   grid  : pages x heads x page 32-bit words, keys and values each.  A word
+ *           with its low four bits cleared is the fp32 scale s; those four bits
+ *           are the zero point z.  Code c stands for s (c - z), which is exact
+ *           in fp32 (s has 20 significant bits).
+ *   A page's heads x page x dim/2 bytes (heads x page words) are contiguous;
+ *   the distance between pages is *_stride (bytes for codes, words for grids),
+ *   so the pages of several layers may share one buffer.
+ * dim is 64, 128 or 256, page a power of two in 16..1024 (KRONQ_EUNSUPPORTED
+ * otherwise).  Codes and grids are 16-byte aligned, their strides multiples of
+ * 16 bytes.
+ *
+ * Batch (device arrays, read by the kernels when they run):
+ *   cu    : int32[seqs + 1], not decreasing: rows cu[i] .. cu[i + 1] - 1 of the
+ *           calls' q, k, v and outputs belong to sequence i (none is allowed).
+ *   ctx   : int32[seqs]: tokens of sequence i in the cache, its rows of this
+ *           call included, so that its last row has position ctx[i] - 1.
+ *   table : int32, seqs rows of `columns` entries (leading dimension
+ *           ld_table): the page that holds positions column * page and up.
+ *           columns * page is at most 2^30 (KRONQ_EUNSUPPORTED otherwise).
+ *   Entries of columns that no visible position needs are not followed and may
+ *   hold anything.  A row outside cu[0] .. cu[seqs] - 1 (padding) belongs to no
+ *   sequence: it is not read, and its outputs are left as they were.
+ *   Nothing outside the caller's buffers is touched whatever these arrays
+ *   hold: a position with no column, or a page outside 0 .. pages - 1, is not
+ *   written by kronq_kv_append, reads back as NaN, and makes the attention of
+ *   the rows that see it NaN.
+ *
+ * Position rotation (NULL: none): cos and sin are positions x dim/2 fp32 device
+ * tables (leading dimension ld).  Of a head's values the first `dim` are turned
+ * in pairs, a' = a cos - b sin and b' = b cos + a sin; pair i is (i, i + dim/2),
+ * or (2i, 2i + 1) when `neighbours` is set.  dim is a multiple of 16 up to the
+ * head's.  A token whose position has no row in the tables is not written, and
+ * a query there gives NaN.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint32_t* k_grid;
+  uint32_t* v_grid;
+  int64_t k_codes_stride, v_codes_stride; /* bytes between pages */
+  int64_t k_grid_stride, v_grid_stride;   /* words between pages */
+  int64_t pages;
+  int32_t heads, page, dim;
+} kronq_kv_cache;
+
+typedef struct {
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* cu;
+  int64_t ld_table;
+  int32_t seqs, columns;
+} kronq_kv_batch;
+
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int64_t ld;
+  int64_t positions;
+  int32_t dim, neighbours;
+} kronq_rope;
+
+/* One operand of the calls below: `rows` rows of heads of dim contiguous
+ * elements, row and head strides in elements.  data and both strides are
+ * multiples of 16 bytes (KRONQ_EINVAL otherwise). */
+typedef struct {
+  void* data;
+  int64_t row_stride, head_stride;
+} kronq_heads;
+
+/* kronq_kv_append: the rows' keys (rotated, when rope is given) and values go
+ *   into the cache at their positions.  For each token's head, in fp64: with
+ *   lo = min(0, x), hi = max(0, x) over its dim values (lo, hi = -1, 1 when both
+ *   are 0), s = (hi - lo) / 15 rounded to fp32 and then to 20 significant bits
+ *   (at least 2^-126), z = round(-lo / s), c = clamp(round(x / s + z), 0, 15),
+ *   ties to even: the column loop's quantizer.  A head with a NaN or an
+ *   infinity gets codes 0 and a NaN scale, so all of it reads as NaN.  Other
+ *   slots of the pages are left as they were.  Two rows with one slot in a call
+ *   race.  k and v must not overlap the cache.
+ * kronq_kv_read: the inverse, as kronq_unpack_codes is of kronq_pack_codes:
+ *   the values held for the last cu[i + 1] - cu[i] positions of each sequence,
+ *   rounded once to dtype.  (Rows read back are those that an append with the
+ *   same batch wrote; a whole prefix is read with ctx as the lengths.)
+ * dtype: KRONQ_F32, KRONQ_BF16 or KRONQ_F16.  At most 2^22 rows, and 2^26 rows x
+ * heads; with rows or seqs 0 nothing is launched (the same for the attention).
+ * One launch each, no host synchronization, no memset: they may be captured in
+ * a HIP graph, and a replay reads cu, ctx and table anew.
+ */
+kronq_status kronq_kv_append(const kronq_heads* k, const kronq_heads* v, int32_t dtype, int64_t rows,
+                             const kronq_kv_cache* cache, const kronq_kv_batch* batch,
+                             const kronq_rope* rope, void* stream);
+kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t dtype, int64_t rows,
+                           const kronq_kv_cache* cache, const kronq_kv_batch* batch, void* stream);
+
+/* kronq_kv_attention: causal attention of the rows' queries over the cache.
+ *   Query head h reads key head h / (q_heads / heads).  A row at position p
+ *   sees position j when j <= p and (window == 0 or j > p - window or
+ *   j < sinks); window 0 is no window, sinks (first tokens that stay visible)
+ *   count only beside one.
+ *     out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max)
+ *     lse = max + log(sum_j w_j)        (natural logarithm; NULL: not wanted)
+ *   with q rotated first when rope is given.  A row that sees nothing gives
+ *   out = 0 and lse = -inf.  Positions that a row does not see cannot change
+ *   its output, whatever the cache holds there.
+ * q, out  : rows x q_heads heads of dtype (KRONQ_F32, KRONQ_BF16, KRONQ_F16);
+ *           they must not overlap each other, the cache or ws.
+ * lse     : rows x q_heads fp32, contiguous, or NULL.
+ * q_heads : a multiple of the cache's heads; at most 2^22 rows and 2^26 rows x
+ *           q_heads, at most 2^20 sequences.
+ * scale   : > 0 and finite, 1 / sqrt(dim) as a rule.
+ * Scores, the running maximum and sum and the outputs are fp32; queries and
+ * weights enter the matrix cores as fp16 scaled by powers of two, in two parts
+ * (22 bits) unless dtype is KRONQ_BF16; codes minus zero points are exact there.
+ * ws      : kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim) bytes,
+ *           written before it is read; calls that overlap in time need one each.
+ * No host synchronization, no memset, no atomics: may be captured in a HIP
+ * graph, replays read cu, ctx and table anew, and equal calls give equal bits.
+ */
+size_t kronq_kv_attention_ws(int64_t rows, int64_t seqs, int32_t q_heads, int32_t heads, int32_t dim);
+kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t rows, int32_t q_heads,
+                                const kronq_kv_cache* cache, const kronq_kv_batch* batch,
+                                const kronq_rope* rope, float scale, int64_t window, int64_t sinks,
+                                const kronq_heads* out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream);
 
 /* ---------------------------------------------------------------------------
  * Sensitivity (hyper.ai summary, Method, Eq. 14: s = tr(H_G) tr(H_X) computed

@@ -10,6 +10,7 @@ it raises, there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -19,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libkronq.so")
 
 (KRONQ_OK, KRONQ_EINVAL, KRONQ_ENOTPD, KRONQ_EHIP, KRONQ_EWORKSPACE, KRONQ_EUNSUPPORTED,
  KRONQ_ENUMERIC, KRONQ_ENOMEM) = range(8)
-KRONQ_F32, KRONQ_BF16 = 0, 1
+KRONQ_F32, KRONQ_BF16, KRONQ_F16 = 0, 1, 2
 
 # every entry point declared in include/kronq.h
 EXPORTS = ("kronq_status_string", "kronq_last_error", "kronq_version", "kronq_gram_ws",
@@ -34,7 +35,8 @@ EXPORTS = ("kronq_status_string", "kronq_last_error", "kronq_version", "kronq_gr
            "kronq_gptaq_correction_ws",
            "kronq_gptaq_correction", "kronq_gptaq_ws", "kronq_gptaq_quantize", "kronq_biip_sx_ws",
            "kronq_biip_rotate_sx", "kronq_biip_unrotate_sx_ws", "kronq_biip_unrotate_sx",
-           "kronq_incoherence_ws", "kronq_incoherence")
+           "kronq_incoherence_ws", "kronq_incoherence", "kronq_kv_append", "kronq_kv_read",
+           "kronq_kv_attention_ws", "kronq_kv_attention")
 
 
 class KronqError(RuntimeError):
@@ -49,6 +51,27 @@ class Had(ctypes.Structure):
 
 class QCfg(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_grid", "v_grid")] + \
+               [(n, ctypes.c_int64) for n in ("k_codes_stride", "v_codes_stride", "k_grid_stride",
+                                              "v_grid_stride", "pages")] + \
+               [(n, ctypes.c_int32) for n in ("heads", "page", "dim")]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("ctx", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int64), ("seqs", ctypes.c_int32), ("columns", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("positions", ctypes.c_int64), ("dim", ctypes.c_int32), ("neighbours", ctypes.c_int32)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -158,6 +181,15 @@ def load(path: str = LIB_PATH):
     lib.kronq_incoherence.argtypes = [vp, i64, i64, ctypes.c_double, i32, ctypes.POINTER(ctypes.c_double),
                                       vp, vp, i64, ctypes.POINTER(i32), vp, sz, vp]
     lib.kronq_incoherence.restype = i32
+    kvh, kvc, kvb, kvr = (ctypes.POINTER(s) for s in (_Heads, _Cache, _Batch, _Rope))
+    lib.kronq_kv_append.argtypes = [kvh, kvh, i32, i64, kvc, kvb, kvr, vp]
+    lib.kronq_kv_append.restype = i32
+    lib.kronq_kv_read.argtypes = [kvh, kvh, i32, i64, kvc, kvb, vp]
+    lib.kronq_kv_read.restype = i32
+    lib.kronq_kv_attention_ws.argtypes = [i64, i64, i32, i32, i32]
+    lib.kronq_kv_attention_ws.restype = sz
+    lib.kronq_kv_attention.argtypes = [kvh, i32, i64, i32, kvc, kvb, kvr, f32, i64, i64, kvh, vp, vp, sz, vp]
+    lib.kronq_kv_attention.restype = i32
     _lib = lib
     return lib
 
@@ -691,3 +723,196 @@ def kronq_gptaq_quantize(W: torch.Tensor, R: torch.Tensor, perm: torch.Tensor | 
                                     _ptr(pre), _ptr(row_loss), _ptr(ws), need, _stream(stream)),
            "kronq_gptaq_quantize")
     return dict(codes=codes, scales=scales, zeros=zeros, What=What, pre=pre, row_loss=row_loss)
+
+
+# ------------------------------------------- 4-bit paged key/value cache
+
+_KV_DTYPES = {torch.float32: KRONQ_F32, torch.bfloat16: KRONQ_BF16, torch.float16: KRONQ_F16}
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t.device != device:
+            raise ValueError("all tensors must be on one device (%s and %s)" % (device, t.device))
+
+
+class KVCache:
+    """One layer's cache: codes uint8 (pages, heads, page, dim / 2) and grid
+    words int32 (pages, heads, page), keys and values each (layouts in
+    include/kronq.h).  Holds the tensors; a page's last three (two) dimensions
+    are contiguous, the distance between pages is free."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_grid: torch.Tensor,
+                 v_grid: torch.Tensor):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be (pages, heads, page, dim / 2)")
+        pages, heads, page, half = k_codes.shape
+        self.device = k_codes.device
+        for t, nm, dt, shape in ((k_codes, "k_codes", torch.uint8, (pages, heads, page, half)),
+                                 (v_codes, "v_codes", torch.uint8, (pages, heads, page, half)),
+                                 (k_grid, "k_grid", torch.int32, (pages, heads, page)),
+                                 (v_grid, "v_grid", torch.int32, (pages, heads, page))):
+            _dev(t, nm, dt)
+            if tuple(t.shape) != shape:
+                raise ValueError("%s must have shape %s" % (nm, shape))
+            inner = tuple(math.prod(shape[i + 1:]) for i in range(1, len(shape)))
+            if t.stride()[1:] != inner:
+                raise ValueError("%s: a page must be contiguous" % nm)
+        _same_device(self.device, v_codes, k_grid, v_grid)
+        self.k_codes, self.v_codes, self.k_grid, self.v_grid = k_codes, v_codes, k_grid, v_grid
+        self.pages, self.heads, self.page, self.dim = pages, heads, page, 2 * half
+        self._c = _Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_grid.data_ptr(), v_grid.data_ptr(),
+                         k_codes.stride(0), v_codes.stride(0), k_grid.stride(0), v_grid.stride(0), pages,
+                         heads, page, 2 * half)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page: int, dim: int, device="cuda:0") -> "KVCache":
+        """A cache of `pages` pages with no content yet."""
+        codes = [torch.zeros((pages, heads, page, dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        grids = [torch.zeros((pages, heads, page), dtype=torch.int32, device=device) for _ in "kv"]
+        return cls(*codes, *grids)
+
+
+class KVBatch:
+    """Which rows belong to which sequence, and where its positions are: table
+    int32 (seqs, columns), ctx int32 (seqs), cu int32 (seqs + 1), on the device
+    (include/kronq.h).  Holds the tensors; their content may change between
+    calls (and between replays of a graph)."""
+
+    def __init__(self, table: torch.Tensor, ctx: torch.Tensor, cu: torch.Tensor):
+        self.device = table.device
+        for t, nm, d in ((table, "table", 2), (ctx, "ctx", 1), (cu, "cu", 1)):
+            _dev(t, nm, torch.int32)
+            if t.dim() != d or (d == 1 and not t.is_contiguous()):
+                raise ValueError("%s must be a contiguous %d-D tensor" % (nm, d))
+        _same_device(self.device, ctx, cu)
+        seqs, columns = table.shape
+        if ctx.shape[0] != seqs or cu.shape[0] != seqs + 1:
+            raise ValueError("table, ctx and cu must be of seqs, seqs and seqs + 1 rows")
+        self.table, self.ctx, self.cu, self.seqs = table, ctx, cu, seqs
+        self._c = _Batch(table.data_ptr(), ctx.data_ptr(), cu.data_ptr(),
+                         table.stride(0) if seqs > 1 else columns, seqs, columns)
+
+
+class Rope:
+    """Position rotation: cos and sin fp32 (positions, rotated dim / 2) on the
+    device; pairs (i, i + rotated dim / 2), or (2 i, 2 i + 1) with `neighbours`."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, neighbours: bool = False):
+        self.device = cos.device
+        _dev(cos, "cos", torch.float32)
+        _dev(sin, "sin", torch.float32)
+        _same_device(self.device, sin)
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.stride() != sin.stride():
+            raise ValueError("cos and sin must be 2-D with one shape and layout")
+        self.cos, self.sin = cos, sin
+        positions, half = cos.shape
+        self._c = _Rope(cos.data_ptr(), sin.data_ptr(), cos.stride(0) if positions > 1 else half, positions,
+                        2 * half, 1 if neighbours else 0)
+
+
+def _heads3(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype, device) -> _Heads:
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s on %s" % (name, dtype, device))
+    if t.shape != (rows, heads, dim):
+        raise ValueError("%s must have shape (%d, %d, %d)" % (name, rows, heads, dim))
+    sr, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("%s must have unit stride in its last dimension" % name)
+    # a dimension of one entry has no distance to speak of
+    return _Heads(t.data_ptr(), sr if rows > 1 else heads * dim, sh if heads > 1 else dim)
+
+
+class _OnStream:
+    """The device of the call's tensors is current, and torch allocates for the
+    stream that the call runs on."""
+
+    def __init__(self, device, stream):
+        cur = torch.cuda.current_stream(device)
+        self.handle = cur.cuda_stream if stream is None else _stream(stream)
+        self.ctx = None
+        if self.handle != cur.cuda_stream:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(self.handle, device=device)
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _kv_check(dtype, cache: KVCache, batch: KVBatch, rope: Rope | None):
+    if dtype not in _KV_DTYPES:
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    _same_device(cache.device, batch, *(() if rope is None else (rope,)))
+
+
+def kronq_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch,
+                    rope: Rope | None = None, stream=None) -> None:
+    """k and v (rows, heads, dim) join the cache at the batch's positions, the
+    keys rotated first when `rope` is given."""
+    _kv_check(k.dtype, cache, batch, rope)
+    rows = k.shape[0]
+    kh = _heads3(k, "k", rows, cache.heads, cache.dim, k.dtype, cache.device)
+    vh = _heads3(v, "v", rows, cache.heads, cache.dim, k.dtype, cache.device)
+    with _OnStream(cache.device, stream) as st:
+        _check(load().kronq_kv_append(kh, vh, _KV_DTYPES[k.dtype], rows, cache._c, batch._c,
+                                      None if rope is None else rope._c, st), "kronq_kv_append")
+
+
+def kronq_kv_read(cache: KVCache, batch: KVBatch, rows: int, dtype=torch.float32,
+                  k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """(k, v): the values held for the last cu[i + 1] - cu[i] positions of each
+    sequence, (rows, heads, dim).  Rows of no sequence are left as they were
+    (undefined when k or v is allocated here)."""
+    _kv_check(dtype, cache, batch, None)
+    shape = (rows, cache.heads, cache.dim)
+    with _OnStream(cache.device, stream) as st:
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=cache.device)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=cache.device)
+        kh = _heads3(k, "k", *shape, dtype, cache.device)
+        vh = _heads3(v, "v", *shape, dtype, cache.device)
+        _check(load().kronq_kv_read(kh, vh, _KV_DTYPES[dtype], rows, cache._c, batch._c, st), "kronq_kv_read")
+    return k, v
+
+
+def kronq_kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None,
+                       window: int = 0, sinks: int = 0, rope: Rope | None = None,
+                       out: torch.Tensor | None = None, want_lse: bool = False,
+                       lse: torch.Tensor | None = None, stream=None, ws: torch.Tensor | None = None):
+    """Causal attention of q (rows, q_heads, dim) over the cache: out in q's
+    dtype, or (out, lse) when lse is asked for.  Rows of no sequence are left as
+    they were (undefined when out is allocated here)."""
+    _kv_check(q.dtype, cache, batch, rope)
+    if q.dim() != 3:
+        raise ValueError("q must be (rows, q_heads, dim)")
+    rows, qheads, _ = q.shape
+    shape = (rows, qheads, cache.dim)
+    qh = _heads3(q, "q", *shape, q.dtype, cache.device)
+    lib = load()
+    with _OnStream(cache.device, stream) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=cache.device)
+        oh = _heads3(out, "out", *shape, q.dtype, cache.device)
+        if lse is None and want_lse:
+            lse = torch.empty((rows, qheads), dtype=torch.float32, device=cache.device)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, qheads) or
+                                not lse.is_contiguous() or lse.device != cache.device):
+            raise ValueError("lse must be a contiguous float32 (rows, q_heads) tensor on %s" % cache.device)
+        need = lib.kronq_kv_attention_ws(rows, batch.seqs, qheads, cache.heads, cache.dim)
+        if ws is None or ws.numel() < need:
+            ws = _ws(need, cache.device)
+        _check(lib.kronq_kv_attention(qh, _KV_DTYPES[q.dtype], rows, qheads, cache._c, batch._c,
+                                      None if rope is None else rope._c,
+                                      cache.dim ** -0.5 if scale is None else scale, window, sinks, oh,
+                                      _ptr(lse), _ptr(ws), need, st), "kronq_kv_attention")
+    return out if lse is None else (out, lse)

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "kronq_internal.h"
+#include "kv.h"
 
 namespace kronq {
 
@@ -117,6 +118,80 @@ static kronq_status check_gptq(const float* W, int64_t m, int64_t n, int64_t ldw
     return fail(KRONQ_EINVAL, "kronq_gptq_quantize: group %d does not divide n", (int)q->group);
   if (What == W && ldw != n)
     return fail(KRONQ_EINVAL, "kronq_gptq_quantize: What may alias W only when ldw == n");
+  return KRONQ_OK;
+}
+
+// ---- key/value cache: checks of the structures, and their kernels' views
+
+static int64_t kv_elem(int32_t dtype) { return dtype == KRONQ_F32 ? 4 : 2; }
+
+static kronq_status kv_rows(const char* fn, int32_t dtype, int64_t rows, int64_t heads) {
+  if (dtype != KRONQ_F32 && dtype != KRONQ_BF16 && dtype != KRONQ_F16)
+    return fail(KRONQ_EINVAL, "%s: dtype %d", fn, (int)dtype);
+  if (rows < 0) return fail(KRONQ_EINVAL, "%s: rows %lld", fn, (long long)rows);
+  if (heads < 1) return fail(KRONQ_EINVAL, "%s: %lld heads", fn, (long long)heads);
+  if (rows > (int64_t(1) << 22) || heads > 65535 || rows * heads > (int64_t(1) << 26))
+    return fail(KRONQ_EUNSUPPORTED, "%s: %lld rows of %lld heads (at most 2^22 rows, 2^26 in all)", fn,
+                (long long)rows, (long long)heads);
+  return KRONQ_OK;
+}
+
+static kronq_status kv_heads(const char* fn, const char* what, const kronq_heads* h, int32_t dtype, int32_t dim,
+                             HeadsView* out) {
+  if (!h || !h->data) return fail(KRONQ_EINVAL, "%s: %s is NULL", fn, what);
+  const int64_t per = 16 / kv_elem(dtype);
+  if (!aligned(h->data, 16) || h->row_stride % per || h->head_stride % per)
+    return fail(KRONQ_EINVAL, "%s: %s must be 16-byte aligned with strides of whole 16 bytes", fn, what);
+  if (h->row_stride < dim || h->head_stride < dim)
+    return fail(KRONQ_EINVAL, "%s: %s has a stride below dim", fn, what);
+  *out = HeadsView{h->data, h->row_stride, h->head_stride};
+  return KRONQ_OK;
+}
+
+static kronq_status kv_view(const char* fn, const kronq_kv_cache* c, const kronq_kv_batch* b, int64_t rows,
+                            KvView* out) {
+  if (!c || !b || !c->k_codes || !c->v_codes || !c->k_grid || !c->v_grid)
+    return fail(KRONQ_EINVAL, "%s: NULL pointer", fn);
+  if (b->seqs > 0 && (!b->ctx || !b->cu || (b->columns > 0 && !b->table)))
+    return fail(KRONQ_EINVAL, "%s: NULL batch pointer", fn);
+  if (c->heads < 1 || c->page < 1 || c->dim < 1 || c->pages < 1 || c->pages > INT32_MAX)
+    return fail(KRONQ_EINVAL, "%s: bad cache shape", fn);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(KRONQ_EUNSUPPORTED, "%s: dim %d (64, 128 and 256 are supported)", fn, (int)c->dim);
+  if (!pow2(c->page) || c->page < 16 || c->page > 1024)
+    return fail(KRONQ_EUNSUPPORTED, "%s: page %d is not a power of two in 16..1024", fn, (int)c->page);
+  const int64_t words = (int64_t)c->heads * c->page, bytes = words * (c->dim / 2);
+  if (c->k_codes_stride < bytes || c->v_codes_stride < bytes || c->k_grid_stride < words ||
+      c->v_grid_stride < words)
+    return fail(KRONQ_EINVAL, "%s: a page stride is below the page", fn);
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_grid, 16) ||
+      !aligned(c->v_grid, 16) || c->k_codes_stride % 16 || c->v_codes_stride % 16 || c->k_grid_stride % 4 ||
+      c->v_grid_stride % 4)
+    return fail(KRONQ_EINVAL, "%s: codes and grids must be 16-byte aligned with strides of whole 16 bytes", fn);
+  if (b->seqs < 0 || b->columns < 0 || b->ld_table < b->columns)
+    return fail(KRONQ_EINVAL, "%s: bad batch shape", fn);
+  if (b->seqs > (1 << 20)) return fail(KRONQ_EUNSUPPORTED, "%s: %d sequences (at most 2^20)", fn, (int)b->seqs);
+  if ((int64_t)b->columns * c->page > (1 << 30))
+    return fail(KRONQ_EUNSUPPORTED, "%s: a table of %d pages of %d positions (at most 2^30 positions)", fn,
+                (int)b->columns, (int)c->page);
+  int lgp = 0;
+  while ((1 << lgp) < c->page) ++lgp;
+  *out = KvView{c->k_codes, c->v_codes, c->k_grid, c->v_grid, c->k_codes_stride, c->v_codes_stride,
+                c->k_grid_stride, c->v_grid_stride, b->table, b->ctx, b->cu, b->ld_table, (int)c->pages, lgp,
+                c->heads, b->seqs, b->columns, (int)rows};
+  return KRONQ_OK;
+}
+
+static kronq_status kv_rope(const char* fn, const kronq_rope* r, int32_t dim, RopeView* out) {
+  *out = RopeView{};
+  if (!r) return KRONQ_OK;
+  if (!r->cos || !r->sin) return fail(KRONQ_EINVAL, "%s: rotation table is NULL", fn);
+  if (r->dim < 1 || r->dim > dim || r->positions < 1 || r->positions > INT32_MAX || r->ld < r->dim / 2)
+    return fail(KRONQ_EINVAL, "%s: bad rotation table shape", fn);
+  if (r->dim % 16) return fail(KRONQ_EUNSUPPORTED, "%s: rotated dim %d is not a multiple of 16", fn, (int)r->dim);
+  if (!aligned(r->cos, 16) || !aligned(r->sin, 16) || r->ld % 4)
+    return fail(KRONQ_EINVAL, "%s: rotation tables must be 16-byte aligned with ld a multiple of 4", fn);
+  *out = RopeView{r->cos, r->sin, r->ld, (int)r->positions, r->dim / 2, r->neighbours};
   return KRONQ_OK;
 }
 
@@ -528,6 +603,71 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
 }
 
 size_t kronq_decode_noalloc_max_bytes(void) { return decode_scratch_bytes(); }
+
+kronq_status kronq_kv_append(const kronq_heads* k, const kronq_heads* v, int32_t dtype, int64_t rows,
+                             const kronq_kv_cache* cache, const kronq_kv_batch* batch,
+                             const kronq_rope* rope, void* stream) {
+  const char* fn = "kronq_kv_append";
+  KvView c;
+  HeadsView kv, vv;
+  RopeView r;
+  kronq_status st = kv_view(fn, cache, batch, rows, &c);
+  if (st) return st;
+  if ((st = kv_rows(fn, dtype, rows, cache->heads))) return st;
+  if ((st = kv_rope(fn, rope, cache->dim, &r))) return st;
+  if (rows == 0 || batch->seqs == 0) return KRONQ_OK;
+  if ((st = kv_heads(fn, "k", k, dtype, cache->dim, &kv))) return st;
+  if ((st = kv_heads(fn, "v", v, dtype, cache->dim, &vv))) return st;
+  return kv_append_launch(c, cache->dim, dtype, kv, vv, r, (hipStream_t)stream);
+}
+
+kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t dtype, int64_t rows,
+                           const kronq_kv_cache* cache, const kronq_kv_batch* batch, void* stream) {
+  const char* fn = "kronq_kv_read";
+  KvView c;
+  HeadsView kv, vv;
+  kronq_status st = kv_view(fn, cache, batch, rows, &c);
+  if (st) return st;
+  if ((st = kv_rows(fn, dtype, rows, cache->heads))) return st;
+  if (rows == 0 || batch->seqs == 0) return KRONQ_OK;
+  if ((st = kv_heads(fn, "k", k, dtype, cache->dim, &kv))) return st;
+  if ((st = kv_heads(fn, "v", v, dtype, cache->dim, &vv))) return st;
+  return kv_read_launch(c, cache->dim, dtype, kv, vv, (hipStream_t)stream);
+}
+
+size_t kronq_kv_attention_ws(int64_t rows, int64_t seqs, int32_t q_heads, int32_t heads, int32_t dim) {
+  if (rows < 1 || seqs < 1 || heads < 1 || q_heads < heads || q_heads % heads || dim < 1) return 0;
+  if (rows > (int64_t(1) << 22) || q_heads > 65535 || rows * q_heads > (int64_t(1) << 26) || dim > 256) return 0;
+  return kv_attention_ws_bytes(rows, seqs, q_heads, heads, dim);
+}
+
+kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t rows, int32_t q_heads,
+                                const kronq_kv_cache* cache, const kronq_kv_batch* batch,
+                                const kronq_rope* rope, float scale, int64_t window, int64_t sinks,
+                                const kronq_heads* out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream) {
+  const char* fn = "kronq_kv_attention";
+  KvView c;
+  HeadsView qv, ov;
+  RopeView r;
+  kronq_status st = kv_view(fn, cache, batch, rows, &c);
+  if (st) return st;
+  if ((st = kv_rows(fn, dtype, rows, q_heads))) return st;
+  if (q_heads % cache->heads)
+    return fail(KRONQ_EINVAL, "%s: %d query heads on %d key heads", fn, (int)q_heads, (int)cache->heads);
+  if ((st = kv_rope(fn, rope, cache->dim, &r))) return st;
+  if (!(scale > 0.0f) || !std::isfinite(scale))
+    return fail(KRONQ_EINVAL, "%s: scale must be finite and > 0", fn);
+  if (window < 0 || sinks < 0) return fail(KRONQ_EINVAL, "%s: window or sinks below 0", fn);
+  if (rows == 0 || batch->seqs == 0) return KRONQ_OK;
+  if ((st = kv_heads(fn, "q", q, dtype, cache->dim, &qv))) return st;
+  if ((st = kv_heads(fn, "out", out, dtype, cache->dim, &ov))) return st;
+  const size_t need = kv_attention_ws_bytes(rows, batch->seqs, q_heads, cache->heads, cache->dim);
+  if ((st = check_ws(fn, ws, ws_bytes, need, true))) return st;
+  const int64_t room = room_of(c);      // a window of all positions is none
+  return kv_attention_launch(c, cache->dim, dtype, qv, q_heads, r, scale, window < room ? (int)window : 0,
+                             (int)std::min(sinks, room), ov, lse, ws, (hipStream_t)stream);
+}
 
 kronq_status kronq_sensitivity(const float* HX, int64_t n, int64_t ldhx, const float* HG,
                                int64_t m, int64_t ldhg, double* out3, void* stream) {

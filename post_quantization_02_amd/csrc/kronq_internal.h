@@ -125,4 +125,17 @@ kronq_status decode_launch_noalloc(const uint8_t* codes, int64_t m, int64_t n, i
                                    const int32_t* perm, const kronq_had& in, const kronq_had& out,
                                    const float* sg, const float* x, float* y, hipStream_t s);
 
+// kvcache.hip, kvattn.hip (the views are in kv.h)
+struct KvView;
+struct HeadsView;
+struct RopeView;
+kronq_status kv_append_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& k, const HeadsView& v,
+                              const RopeView& r, hipStream_t s);
+kronq_status kv_read_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& k, const HeadsView& v,
+                            hipStream_t s);
+size_t kv_attention_ws_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int dim);
+kronq_status kv_attention_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& q, int q_heads,
+                                 const RopeView& rope, float scale, int window, int sinks, const HeadsView& out,
+                                 float* lse, void* ws, hipStream_t s);
+
 }  // namespace kronq

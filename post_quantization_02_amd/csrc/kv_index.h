@@ -1,0 +1,147 @@
+// Which memory a call on the 4-bit paged key/value cache touches: rows to
+// sequences, positions to pages, and how the attention's work is cut.  Plain
+// functions of the batch arrays (whose content no host check sees), so that
+// what they may return is tested on the host.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace kronq {
+
+struct KvView {
+  uint8_t *kc, *vc;        // codes
+  uint32_t *kg, *vg;       // grids
+  int64_t kcs, vcs;        // bytes between pages
+  int64_t kgs, vgs;        // words between pages
+  const int32_t *table, *ctx, *cu;
+  int64_t ldt;
+  int pages, lgp, heads;   // page = 1 << lgp
+  int seqs, columns;
+  int rows;
+};
+
+// The sequence of a row: the last one that starts at or before it and ends
+// behind it; -1 if there is none.  `cu` are the sequences' starts and the end.
+__host__ __device__ inline int seq_of(const int32_t* cu, int seqs, int row) {
+  int lo = 0, hi = seqs;   // cu[lo] <= row < cu[hi]
+  if (row < cu[0] || row >= cu[seqs]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= row) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+struct PageAt { int page; bool bad; };
+
+// The page of a position >= 0 of the sequence whose table row is given; page 0
+// where there is none in range, so that reading is safe.
+__host__ __device__ inline PageAt page_at(const KvView& c, const int32_t* table, int pos) {
+  const int col = pos >> c.lgp;
+  const int page = col < c.columns ? table[col] : -1;
+  const bool bad = page < 0 || page >= c.pages;
+  return {bad ? 0 : page, bad};
+}
+
+// Where a row's token lives.  pos < 0: nowhere.  bad: no page in range.
+struct Place { int pos, page, slot; bool bad; };
+
+__host__ __device__ inline Place place_of(const KvView& c, int seq, int row, int end) {
+  const int64_t pos = (int64_t)c.ctx[seq] - end + row;   // end: the sequence's, cu[seq + 1] > row
+  if (pos < 0) return {-1, 0, 0, true};
+  const PageAt p = page_at(c, c.table + seq * c.ldt, (int)pos);
+  return {(int)pos, p.page, (int)(pos & ((1 << c.lgp) - 1)), p.bad};
+}
+
+// ---- attention: the work of a sequence
+//
+// Rows x share query heads of a key head in tiles of BM, keys in tiles of KT.
+
+struct AttnShape { int share, window, sinks; };   // window 0: none
+
+struct Seq { int row0, len, ctx, tiles, qtiles; };
+
+__host__ __device__ inline int tiles_of(int n, int kt) { return n / kt + (n % kt != 0); }
+
+// Positions that have a column.
+__host__ __device__ inline int64_t room_of(const KvView& c) { return (int64_t)c.columns << c.lgp; }
+
+__host__ __device__ inline int cut_to_room(const KvView& c, int n) {
+  const int64_t room = room_of(c);
+  return n < 0 ? 0 : (int64_t)n < room ? n : (int)room;
+}
+
+// The key tiles that rows at pos_lo .. pos_hi see: `sink` first ones, then
+// from .. upto - 1.
+struct Span { int sink, from, upto; };
+
+__host__ __device__ inline Span span_between(const KvView& c, const AttnShape& a, int pos_lo, int pos_hi, int kt) {
+  const int end = cut_to_room(c, pos_hi < 0 ? 0 : pos_hi == INT32_MAX ? pos_hi : pos_hi + 1);
+  Span s{0, 0, tiles_of(end, kt)};
+  if (a.window) {
+    const int first = pos_lo - a.window + 1;
+    s.from = first > 0 ? first / kt : 0;
+    if (s.from > s.upto) s.from = s.upto;
+    s.sink = tiles_of(a.sinks < end ? a.sinks : end, kt);
+    if (s.sink > s.from) s.sink = s.from;
+  }
+  return s;
+}
+
+__host__ __device__ inline Seq seq_at(const KvView& c, const AttnShape& a, int b, int bm, int kt) {
+  Seq s{0, 0, 0, 0, 0};
+  if (b >= c.seqs) return s;
+  const int lo = c.cu[b] > 0 ? c.cu[b] : 0, hi = c.cu[b + 1] < c.rows ? c.cu[b + 1] : c.rows;
+  if (hi <= lo) return s;
+  s.row0 = lo;
+  s.len = hi - lo;
+  s.ctx = c.ctx[b] > 0 ? c.ctx[b] : 0;
+  const Span all = span_between(c, a, s.ctx > s.len ? s.ctx - s.len : 0, s.ctx - 1, kt);
+  s.tiles = all.sink + all.upto - all.from;
+  s.qtiles = (int)(((int64_t)s.len * a.share + bm - 1) / bm);
+  return s;
+}
+
+// The launch has a fixed number of units; a unit is (sequence, tile of rows,
+// chunk of the keys).  The chunk length is the smallest at which all chunks fit:
+// sum of qtiles * ceil(tiles / per) <= work / per + rows <= units, with
+// work = sum of qtiles * tiles and rows = sum of qtiles.
+__host__ __device__ inline int chunk_tiles(double work, double rows, int units, int least) {
+  const double room = units - rows > 1.0 ? units - rows : 1.0;
+  const int per = (int)ceil(work / room);
+  return per > least ? per : least;
+}
+
+__host__ __device__ inline int chunks_of(const Seq& s, int per) {
+  const int n = tiles_of(s.tiles, per);
+  return n > 1 ? n : 1;
+}
+
+struct Unit {
+  int b, qtile, chunk, chunks, base;   // base: the sequence's first unit
+  int row0, len, ctx;
+};
+
+__host__ __device__ inline Span span_of(const KvView& c, const AttnShape& a, const Unit& u, int bm, int kt, int& pos_lo,
+                                        int& pos_hi) {
+  const int last = (u.qtile * bm + bm - 1) / a.share;
+  pos_lo = u.ctx - u.len + u.qtile * bm / a.share;
+  pos_hi = u.ctx - u.len + (last < u.len ? last : u.len - 1);
+  return span_between(c, a, pos_lo, pos_hi, kt);
+}
+
+// The tiles v0 .. v1 - 1 of a span's (counted over both its parts) that are the
+// unit's: equal parts of what the unit's rows see.
+__host__ __device__ inline void chunk_of(const Span& s, const Unit& u, int& v0, int& v1) {
+  const int tiles = s.sink + s.upto - s.from, per = tiles / u.chunks + (tiles % u.chunks != 0);
+  v0 = (int64_t)u.chunk * per < tiles ? u.chunk * per : tiles;
+  v1 = v0 + per < tiles ? v0 + per : tiles;
+}
+
+__host__ __device__ inline int key_of(const Span& s, int v, int kt) {
+  return (v < s.sink ? v : v - s.sink + s.from) * kt;
+}
+
+}  // namespace kronq
