@@ -590,17 +590,19 @@ kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t d
  *     out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max)
  *     lse = max + log(sum_j w_j)        (natural logarithm; NULL: not wanted)
  *   with q rotated first when rope is given.  A row that sees nothing gives
- *   out = 0 and lse = -inf.  Positions that a row does not see cannot change
- *   its output, whatever the cache holds there.
+ *   out = 0 and lse = -inf.  What the cache holds at positions that a row does
+ *   not see is no part of its output.  Where out is NaN, lse is not defined.
  * q, out  : rows x q_heads heads of dtype (KRONQ_F32, KRONQ_BF16, KRONQ_F16);
  *           they must not overlap each other, the cache or ws.
  * lse     : rows x q_heads fp32, contiguous, or NULL.
  * q_heads : a multiple of the cache's heads; at most 2^22 rows and 2^26 rows x
  *           q_heads, at most 2^20 sequences.
  * scale   : > 0 and finite, 1 / sqrt(dim) as a rule.
- * Scores, the running maximum and sum and the outputs are fp32; queries and
- * weights enter the matrix cores as fp16 scaled by powers of two, in two parts
- * (22 bits) unless dtype is KRONQ_BF16; codes minus zero points are exact there.
+ * Scores, the running maximum and sum and the outputs are fp32.  Queries and
+ * weights enter the matrix cores as fp16 scaled by powers of two: for KRONQ_F32
+ * in two parts (22 bits); for KRONQ_F16 queries in two parts, weights in one or
+ * two; for KRONQ_BF16 in one.  Codes minus zero points are exact there; for
+ * KRONQ_BF16 and many rows they carry the scales, rounded to fp16.
  * ws      : kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim) bytes,
  *           written before it is read; calls that overlap in time need one each.
  * No host synchronization, no memset, no atomics: may be captured in a HIP

@@ -69,4 +69,17 @@ __device__ inline void store8(_Float16* p, const float* x) {
   *reinterpret_cast<half8_t*>(p) = a;
 }
 
+// four consecutive values, aligned to four
+__device__ inline void store4(float* p, const float* x) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+}
+__device__ inline void store4(bf16_t* p, const float* x) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{to_bf16(x[0]) | ((uint32_t)to_bf16(x[1]) << 16),
+                                       to_bf16(x[2]) | ((uint32_t)to_bf16(x[3]) << 16)};
+}
+__device__ inline void store4(_Float16* p, const float* x) {
+  typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<half4*>(p) = half4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
+}
+
 }  // namespace kronq

@@ -58,8 +58,9 @@ __host__ __device__ inline Place place_of(const KvView& c, int seq, int row, int
 // ---- attention: the work of a sequence
 //
 // Rows x share query heads of a key head in tiles of BM, keys in tiles of KT.
+// A kernel takes the sequences whose rows x share are least .. most.
 
-struct AttnShape { int share, window, sinks; };   // window 0: none
+struct AttnShape { int share, window, sinks, least, most; };   // window 0: none
 
 struct Seq { int row0, len, ctx, tiles, qtiles; };
 
@@ -95,12 +96,14 @@ __host__ __device__ inline Seq seq_at(const KvView& c, const AttnShape& a, int b
   if (b >= c.seqs) return s;
   const int lo = c.cu[b] > 0 ? c.cu[b] : 0, hi = c.cu[b + 1] < c.rows ? c.cu[b + 1] : c.rows;
   if (hi <= lo) return s;
+  const int64_t n = (int64_t)(hi - lo) * a.share;
+  if (n < a.least || n > a.most) return s;
   s.row0 = lo;
   s.len = hi - lo;
   s.ctx = c.ctx[b] > 0 ? c.ctx[b] : 0;
   const Span all = span_between(c, a, s.ctx > s.len ? s.ctx - s.len : 0, s.ctx - 1, kt);
   s.tiles = all.sink + all.upto - all.from;
-  s.qtiles = (int)(((int64_t)s.len * a.share + bm - 1) / bm);
+  s.qtiles = (int)((n + bm - 1) / bm);
   return s;
 }
 

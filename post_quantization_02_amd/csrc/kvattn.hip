@@ -9,143 +9,10 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kv.h"
+#include "kvattn.h"
 
 namespace kronq {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
-struct AttnView {
-  KvView c;
-  HeadsView q, out;
-  RopeView rope;
-  float* lse;
-  int qheads;              // query heads
-  float scale;
-  AttnShape shape;
-  int units;               // work units of a key head
-  int min_tiles;           // tiles of a chunk at least
-  float* part;             // [units][heads][BM][dim] unnormalized outputs
-  float* stat;             // [units][heads][BM][2]   maximum (of f S), sum
-};
-
-// ---- work units
-//
-// The host knows neither the lengths nor the contexts, only how many rows and
-// sequences there are, so the launch has a fixed number of units and the kernels
-// cut the keys.  Every wave works its unit out from cu and ctx by itself, 64
-// sequences at a time.
-
-__device__ inline int wave_scan(int x) {              // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if ((int)(threadIdx.x & 63) >= d) x += y;
-  }
-  return x;
-}
-
-__device__ inline double wave_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-  return x;
-}
-
-// The unit `want`; by_row: the sequence of row `want`, its first unit.  false:
-// there is none.
-template <int BM, int KT>
-__device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit& u) {
-  const int lane = threadIdx.x & 63;
-  // sums of integers below 2^53: exact
-  double rows = 0, work = 0;
-  Seq s = seq_at(a.c, a.shape, lane, BM, KT);
-  for (int b0 = 0;;) {
-    rows += s.qtiles;
-    work += (double)s.qtiles * s.tiles;
-    b0 += 64;
-    if (b0 >= a.c.seqs) break;
-    s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
-  }
-  rows = wave_sum(rows);
-  work = wave_sum(work);
-  const int per = chunk_tiles(work, rows, a.units, a.min_tiles);
-  int before = 0;
-  for (int b0 = 0; b0 < a.c.seqs; b0 += 64) {
-    if (a.c.seqs > 64) s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
-    const int chunks = chunks_of(s, per);
-    const int n = s.qtiles * chunks, upto = before + wave_scan(n);
-    const bool mine = by_row ? (want >= s.row0 && want < s.row0 + s.len) : (want < upto && want >= upto - n);
-    const uint64_t hit = __ballot(mine);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      u.b = b0 + l;
-      u.base = __shfl(upto - n, l);
-      u.chunks = __shfl(chunks, l);
-      u.row0 = __shfl(s.row0, l);
-      u.len = __shfl(s.len, l);
-      u.ctx = __shfl(s.ctx, l);
-      const int rest = by_row ? 0 : want - u.base;
-      u.qtile = rest / u.chunks;
-      u.chunk = rest % u.chunks;
-      return true;
-    }
-    before = __shfl(upto, 63);
-  }
-  return false;
-}
-
-// ---- queries
-
-// Eight values of a query head from position d on, rotated in fp32.
-template <typename T>
-__device__ inline void query8(const T* p, int d, const RopeView& rope, int64_t pos, float* x) {
-  load8(p + d, x);
-  if (d >= 2 * rope.half) return;
-  const float* ct = rope.cos + pos * rope.ld;
-  const float* st = rope.sin + pos * rope.ld;
-  if (rope.neighbours) {
-    const f32x4 c = *reinterpret_cast<const f32x4*>(ct + d / 2);
-    const f32x4 s = *reinterpret_cast<const f32x4*>(st + d / 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y = x[2 * i], z = x[2 * i + 1];
-      x[2 * i] = y * c[i] - z * s[i];
-      x[2 * i + 1] = z * c[i] + y * s[i];
-    }
-  } else {
-    const bool second = d >= rope.half;
-    const int j = second ? d - rope.half : d;
-    float o[8], c[8], s[8];
-    load8(p + (second ? j : d + rope.half), o);
-    load8(ct + j, c);
-    load8(st + j, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = second ? x[i] * c[i] + o[i] * s[i] : x[i] * c[i] - o[i] * s[i];
-  }
-}
-
-// Eight codes of a word in the order the unpacking yields them.
-__device__ constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-
-__device__ inline half2_t as_half2(uint32_t x) { return __builtin_bit_cast(half2_t, x); }
-
-// Pairs of values c - z.  1024 + c is the fp16 number 0x6400 | c, and
-// 1024 + 16 c is 0x6400 | 16 c; zero holds z in both halves (0x6400 | z, and
-// 64 + z = 0x5400 | 16 z).  All differences are exact.
-__device__ inline half2_t low_pair(uint32_t x, half2_t zero1024) {
-  return as_half2((x & 0x000F000Fu) | 0x64006400u) - zero1024;
-}
-__device__ inline half2_t high_pair(uint32_t x, half2_t zero64) {
-  return as_half2((x & 0x00F000F0u) | 0x64006400u) * half2_t{(_Float16)0.0625f, (_Float16)0.0625f} - zero64;
-}
-
-// A word's eight codes minus their zero point, in kOrder.
-__device__ inline half8_t unpack_word(uint32_t w, half2_t zero1024, half2_t zero64) {
-  const half2_t a = low_pair(w, zero1024), b = high_pair(w, zero64);
-  const half2_t c = low_pair(w >> 8, zero1024), d = high_pair(w >> 8, zero64);
-  return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
 
 // ---- one tile of 16 rows
 //
@@ -219,21 +86,7 @@ __device__ inline void load_tile(const KvView& c, const int32_t* table, int head
   }
 }
 
-// What a row keeps while its keys go by: the maximum m of f S, its lane's part
-// of l, and the factor 2^-e under which the products of weights and value scales
-// enter the matrix cores as fp16.  e follows the row's largest such product:
-// where that was last set it lies in [2^5, 2^6), and products up to 2^14 pass
-// before it is set again, so that products 2^-20 of the largest are still normal
-// numbers whatever the scales' range.  m is raised only where a score leaves it
-// behind by 2^kLazy.
-constexpr int kLazy = 8, kRoom = 6, kTop = 14, kNone = -127;
-
-struct RowState {
-  float m = -INFINITY, l = 0, limit = 0;   // limit 2^(kTop + e); 0: nothing seen yet
-  int e = kNone;
-};
-
-template <int DIM, typename T, bool TWO>
+template <int DIM, typename T, int PARTS>
 __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
   constexpr int BM = 16, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
   __shared__ float lds_o[4][BM][PAD];
@@ -250,50 +103,9 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
   const int32_t* table = a.c.table + (int64_t)u.b * a.c.ldt;
 
   // this lane's query row
-  const int r = u.qtile * BM + i;
-  const int t = min(r / share, u.len - 1);
-  const int pos = u.ctx - u.len + t;
-  const bool real = r < u.len * share;
-  float f;
-  half8_t q1[KS], q2[TWO ? KS : 1];
-  {
-    const int qh = head * share + r % share;
-    const T* qp = static_cast<const T*>(a.q.data) + (int64_t)(u.row0 + t) * a.q.row + (int64_t)qh * a.q.head;
-    float x[KS][8], big = 0;
-    const bool turned = !a.rope.half || (pos >= 0 && pos < a.rope.positions);
-    bool fine = turned;
-    RopeView rope = a.rope;
-    if (!turned) rope.half = 0;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      query8(qp, g * (DIM / 4) + 8 * k, rope, pos, x[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        big = fmaxf(big, fabsf(x[k][e]));
-        fine = fine && (x[k][e] - x[k][e] == 0);
-      }
-    }
-    big = fmaxf(big, __shfl_xor(big, 16));
-    big = fmaxf(big, __shfl_xor(big, 32));
-    const uint64_t notfine = __ballot(!fine);
-    fine = !((notfine >> i) & 0x0001000100010001ull);
-    int e2 = 0;
-    if (fine && big > 0) {
-      frexpf(big, &e2);                               // big < 2^e2
-      e2 = 4 - e2;                                    // the row's largest value in [2^3, 2^4)
-    }
-    // a row that is not finite has no score
-    f = fine ? ldexpf(a.scale * kLog2e, -e2) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = fine ? ldexpf(x[k][kOrder[e]], e2) : 0.0f;
-        q1[k][e] = (_Float16)y;
-        if constexpr (TWO) q2[k][e] = (_Float16)(y - (float)q1[k][e]);
-      }
-    }
-  }
+  const int r = u.qtile * BM + i, pos = u.ctx - u.len + min(r / share, u.len - 1);
+  half8_t q1[KS], q2[PARTS > 1 ? KS : 1];
+  const float f = load_query<T, PARTS, KS, 4>(a, u, head, r, g * (DIM / 4), 8, q1, q2);
 
   f32x4 o[VT];
 #pragma unroll
@@ -317,7 +129,7 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
       for (int k = 0; k < KS; ++k) {
         const half8_t kv = unpack_word(cur.k[b][k], z1, z2);
         sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q1[k], sc[b], 0, 0, 0);
-        if constexpr (TWO) sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q2[k], sc[b], 0, 0, 0);
+        if constexpr (PARTS > 1) sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q2[k], sc[b], 0, 0, 0);
       }
     }
     // keys 8 g + x: which are visible?  All are, but in the tiles at the edges.
@@ -330,9 +142,8 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
     for (int x = 0; x < 8; ++x) {
       const int j = first + x;
       seen[x] = whole || (j <= pos && (!window || j > pos - window || j < sinks));
-      const float nan = __uint_as_float(0x7FC00000u);
-      const float ks = cur.bad ? nan : __uint_as_float(cur.ks[x >> 2][x & 3] & ~15u);
-      vs[x] = cur.bad ? nan : __uint_as_float(cur.vs[x >> 2][x & 3] & ~15u);
+      const float ks = cur.bad ? kNan : __uint_as_float(cur.ks[x >> 2][x & 3] & ~15u);
+      vs[x] = cur.bad ? kNan : __uint_as_float(cur.vs[x >> 2][x & 3] & ~15u);
       s[x] = seen[x] ? sc[x >> 2][x & 3] * (ks * f) : -INFINITY;
       top = fmaxf(top, s[x]);
     }
@@ -379,7 +190,7 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
     for (int x = 0; x < 8; ++x) {
       y[x] *= unit;
       p1[x] = (_Float16)y[x];
-      if constexpr (TWO) p2[x] = (_Float16)(y[x] - (float)p1[x]);
+      if constexpr (PARTS > 1) p2[x] = (_Float16)(y[x] - (float)p1[x]);
     }
     half2_t z1[4], z2[4];
 #pragma unroll
@@ -402,7 +213,7 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
       const half8_t vb{hi[0].x, hi[0].y, hi[1].x, hi[1].y, hi[2].x, hi[2].y, hi[3].x, hi[3].y};
       o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p1, o[2 * b], 0, 0, 0);
       o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p1, o[2 * b + 1], 0, 0, 0);
-      if constexpr (TWO) {
+      if constexpr (PARTS > 1) {
         o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p2, o[2 * b], 0, 0, 0);
         o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p2, o[2 * b + 1], 0, 0, 0);
       }
@@ -441,7 +252,7 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
     }
     const int tok = rg / share, qh = head * share + rg % share;
     // a position without a column: its row sees at least itself
-    if (u.ctx - u.len + tok >= room_of(a.c)) ll = __uint_as_float(0x7FC00000u);
+    if (u.ctx - u.len + tok >= room_of(a.c)) ll = kNan;
     if (u.chunks == 1) {
       const float inv = ll == 0 ? 0.0f : 1.0f / ll;
 #pragma unroll
@@ -460,15 +271,23 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
   }
 }
 
-// Joins the chunks of one row's head, in the order of the chunks.
+// Joins the chunks of one row's head, in the order of the chunks.  blockIdx.x:
+// a row; or, where few rows of each sequence are this kernel's (per > 0), a
+// sequence's row, per for each.
 template <int DIM, int BM, int KT, typename T>
-__global__ __launch_bounds__(256) void kv_attention_join(AttnView a) {
+__global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per) {
   constexpr int LANES = DIM / 8, SLOTS = 256 / LANES;
   __shared__ float lds_x[SLOTS][DIM + 4];
   __shared__ float lds_l[SLOTS];
   Unit u;
   const int share = a.shape.share;
-  const int row = blockIdx.x, qh = blockIdx.y, head = qh / share;
+  int row = blockIdx.x;
+  if (per) {
+    const Seq s = seq_at(a.c, a.shape, blockIdx.x / per, BM, KT);
+    if ((int)blockIdx.x % per >= s.len) return;
+    row = s.row0 + blockIdx.x % per;
+  }
+  const int qh = blockIdx.y, head = qh / share;
   if (!find_unit<BM, KT>(a, row, true, u) || u.chunks == 1) return;
   const int r = (row - u.row0) * share + qh % share;
   const int tid = threadIdx.x, slot = tid / LANES, d = (tid % LANES) * 8;
@@ -511,39 +330,101 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a) {
 }
 
 // ---- launch
+//
+// Sequences of up to kFewRows rows x share go to the 16-row kernel, which reads
+// the cache once for each 16 of them; longer ones to the 128-row kernel.
 
+constexpr int kFewRows = 32;
 constexpr int kMinTiles16 = 8;           // 256 keys: a chunk of 64 for each wave
 constexpr int kUnits16 = 2048;           // chunks over all key heads that a launch aims at
+constexpr int kMinTiles128 = 4;          // 256 keys
+constexpr int kUnits128 = 512;
 
-// Units of the 16-row kernel: a bound of the row tiles, and the chunks on top.
-int64_t units16(int64_t rows, int64_t seqs, int share, int heads) {
-  const int64_t tiles = (rows * share + 15 * std::min(rows, seqs)) / 16;
-  return tiles + std::max<int64_t>(kUnits16 / heads, 1);
+// How a call is cut: units of each kernel (0: not launched; a bound of its row
+// tiles, and chunks on top), and whether there can be chunks to join.
+struct Plan {
+  int units16, units128;
+  bool join16, join128;
+  size_t part16, part128;                // floats of partial results
+};
+
+Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
+  Plan p{};
+  const int64_t n = rows * share, some = std::min(rows, seqs);
+  // with one sequence the rows decide; with more, few rows for one may be many for another
+  if (seqs > 1 || n <= kFewRows) {
+    const int64_t tiles = std::min((n + 15 * some) / 16, some * ((kFewRows + 15) / 16));
+    const int64_t more = std::max<int64_t>(kUnits16 / heads - tiles / 2, 1);
+    p.units16 = (int)(tiles + more);
+    p.join16 = more > 1;
+  }
+  if (n > kFewRows) {
+    const int64_t tiles = (n + 127 * std::min<int64_t>(some, n / (kFewRows + 1))) / 128;
+    const int64_t more = tiles * heads >= kUnits128 ? 1 : std::max<int64_t>(kUnits128 / heads, 1);
+    p.units128 = (int)(tiles + more);
+    p.join128 = more > 1;
+  }
+  if (p.join16) p.part16 = (size_t)p.units16 * heads * 16 * (dim + 2);
+  if (p.join128) p.part128 = (size_t)p.units128 * heads * 128 * (dim + 2);
+  return p;
 }
 
-template <int DIM, typename T, bool TWO>
-kronq_status launch16(AttnView a, hipStream_t s) {
-  hipLaunchKernelGGL((kv_attention16<DIM, T, TWO>), dim3((unsigned)a.units, (unsigned)a.c.heads), dim3(256), 0, s, a);
-  KQ_LAUNCHED("kv_attention16");
+template <int DIM, int BM, int KT, typename T>
+kronq_status join(const AttnView& a, int64_t per, hipStream_t s) {
   // no chunk can be cut when the longest context the table has room for fits one
-  if (room_of(a.c) <= (int64_t)a.min_tiles * 32) return KRONQ_OK;
-  hipLaunchKernelGGL((kv_attention_join<DIM, 16, 32, T>), dim3((unsigned)a.c.rows, (unsigned)a.qheads), dim3(256), 0, s, a);
+  if (room_of(a.c) <= (int64_t)a.min_tiles * KT) return KRONQ_OK;
+  const bool by_seq = per > 0 && per * a.c.seqs < a.c.rows;
+  const int64_t grid = by_seq ? per * a.c.seqs : a.c.rows;
+  hipLaunchKernelGGL((kv_attention_join<DIM, BM, KT, T>), dim3((unsigned)grid, (unsigned)a.qheads), dim3(256), 0, s, a,
+                     by_seq ? (int)per : 0);
   KQ_LAUNCHED("kv_attention_join");
   return KRONQ_OK;
 }
 
+template <int DIM, typename T, int PARTS>
+kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s) {
+  const Plan p = plan_of(a.c.rows, a.c.seqs, a.shape.share, a.c.heads, DIM);
+  const bool both = p.units16 && p.units128;
+  if (p.units16) {
+    a.shape.least = 1;
+    a.shape.most = both ? kFewRows : INT32_MAX;
+    a.units = p.units16;
+    a.min_tiles = kMinTiles16;
+    a.part = ws;
+    a.stat = ws + (size_t)p.units16 * a.c.heads * 16 * DIM;
+    hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS>), dim3((unsigned)a.units, (unsigned)a.c.heads), dim3(256), 0, s, a);
+    KQ_LAUNCHED("kv_attention16");
+    if (p.join16) {
+      const kronq_status st = join<DIM, 16, 32, T>(a, std::max(kFewRows / a.shape.share, 1), s);
+      if (st) return st;
+    }
+  }
+  if (p.units128) {
+    a.shape.least = both ? kFewRows + 1 : 1;
+    a.shape.most = INT32_MAX;
+    a.units = p.units128;
+    a.min_tiles = kMinTiles128;
+    a.part = ws + p.part16;
+    a.stat = a.part + (size_t)p.units128 * a.c.heads * 128 * DIM;
+    const kronq_status st = kv_rows_launch(a, dim, dtype, s);
+    if (st) return st;
+    if (p.join128) return join<DIM, 128, 64, T>(a, 0, s);
+  }
+  return KRONQ_OK;
+}
+
 template <int DIM>
-kronq_status launch_dim(const AttnView& a, int32_t dtype, hipStream_t s) {
-  if (dtype == KRONQ_F32) return launch16<DIM, float, true>(a, s);
-  if (dtype == KRONQ_BF16) return launch16<DIM, bf16_t, false>(a, s);
-  return launch16<DIM, _Float16, true>(a, s);
+kronq_status launch_dim(const AttnView& a, int32_t dtype, float* ws, hipStream_t s) {
+  if (dtype == KRONQ_F32) return launch<DIM, float, 2>(a, DIM, dtype, ws, s);
+  if (dtype == KRONQ_BF16) return launch<DIM, bf16_t, 1>(a, DIM, dtype, ws, s);
+  return launch<DIM, _Float16, 2>(a, DIM, dtype, ws, s);
 }
 
 }  // namespace
 
 size_t kv_attention_ws_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int dim) {
-  const int64_t units = units16(rows, seqs, q_heads / heads, heads);
-  return (size_t)units * heads * 16 * (dim + 2) * sizeof(float);
+  const Plan p = plan_of(rows, seqs, q_heads / heads, heads, dim);
+  return std::max((p.part16 + p.part128) * sizeof(float), size_t(16));
 }
 
 kronq_status kv_attention_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& q, int q_heads,
@@ -556,15 +437,11 @@ kronq_status kv_attention_launch(const KvView& c, int dim, int32_t dtype, const 
   a.rope = rope;
   a.lse = lse;
   a.qheads = q_heads;
-  a.shape = AttnShape{q_heads / c.heads, window, sinks};
+  a.shape = AttnShape{q_heads / c.heads, window, sinks, 1, INT32_MAX};
   a.scale = scale;
-  a.units = (int)units16(c.rows, c.seqs, a.shape.share, c.heads);
-  a.min_tiles = kMinTiles16;
-  a.part = static_cast<float*>(ws);
-  a.stat = a.part + (int64_t)a.units * c.heads * 16 * dim;
-  if (dim == 64) return launch_dim<64>(a, dtype, s);
-  if (dim == 128) return launch_dim<128>(a, dtype, s);
-  return launch_dim<256>(a, dtype, s);
+  if (dim == 64) return launch_dim<64>(a, dtype, static_cast<float*>(ws), s);
+  if (dim == 128) return launch_dim<128>(a, dtype, static_cast<float*>(ws), s);
+  return launch_dim<256>(a, dtype, static_cast<float*>(ws), s);
 }
 
 }  // namespace kronq

@@ -32,7 +32,7 @@ extern "C" int units_cover(const int32_t* table, const int32_t* ctx, const int32
   KvView c{};
   c.table = table, c.ctx = ctx, c.cu = cu, c.ldt = columns, c.seqs = seqs, c.columns = columns;
   c.pages = pages, c.lgp = lgp, c.rows = rows;
-  const AttnShape a{share, window, sinks};
+  const AttnShape a{share, window, sinks, 1, INT32_MAX};
   double sum_rows = 0, work = 0;
   for (int b = 0; b < seqs; ++b) {
     const Seq s = seq_at(c, a, b, bm, kt);

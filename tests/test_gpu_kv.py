@@ -206,8 +206,9 @@ def test_what_is_not_seen_does_not_matter(new):
     assert torch.equal(attend(c, 24, 3), out)
 
 
-def test_values_that_are_not_numbers_reach_the_rows_that_see_them():
-    c = Case([(100, 40), (50, 2)], heads=2, share=2, dim=64, dtype=torch.float32)
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_values_that_are_not_numbers_reach_the_rows_that_see_them(dtype):
+    c = Case([(100, 40), (50, 2)], heads=2, share=2, dim=64, dtype=dtype)
     p, slot = K.place(c.cache, c.batch, 0, 80)
     c.cache["v_grid"][p, 0, slot] = K.NAN_WORD
     p, slot = K.place(c.cache, c.batch, 1, 49)
@@ -217,8 +218,9 @@ def test_values_that_are_not_numbers_reach_the_rows_that_see_them():
     attend(c)
 
 
-def test_places_out_of_range_give_nan_to_the_rows_that_see_them():
-    c = Case([(60, 40), (30, 3), (45, 1), (20, 2)], heads=2, share=2, dim=64, rot=64, columns=3)  # 48 positions
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_places_out_of_range_give_nan_to_the_rows_that_see_them(dtype):
+    c = Case([(60, 40), (30, 3), (45, 1), (20, 2)], heads=2, share=2, dim=64, dtype=dtype, rot=64, columns=3)  # 48 positions
     c.table[1, 0] = -5
     c.table[3, 1] = c.pages
     c.rope = (c.rope[0][:44], c.rope[1][:44], True)
@@ -240,6 +242,24 @@ def test_scales_far_apart(dtype):
     attend(c, scale=0.002)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("new", [2, 60])
+def test_scales_far_apart_within_a_tile(dtype, new):
+    # every few keys another magnitude; and one key that only later rows see is
+    # beyond all others, which must not cost the earlier rows their precision
+    c = Case([(250, new)], heads=2, share=2, dim=64, dtype=dtype)
+    for nm, decades in (("k", 2), ("v", 12)):
+        w = c.cache[nm + "_grid"]
+        for j in range(250):
+            p, slot = K.place(c.cache, c.batch, 0, j)
+            s = np.float32(0.1 * 10.0 ** (-decades * (j % 5) / 4))
+            if j == 248:
+                s = np.float32(0.1 if nm == "k" else 1e3)
+            w[p, :, slot] = (s.view(np.uint32) & np.uint32(0xFFFFFFF0)) | (w[p, :, slot] & 15)
+    attend(c)
+    attend(c, 30, 2)
+
+
 def test_small_and_large_queries():
     c = Case([(80, 3)], heads=2, share=2, dim=64)
     c.q[0] *= 1e-30
@@ -254,8 +274,15 @@ def test_long_context_is_cut_and_joined():
     attend(c, 2500, 5)
 
 
-def test_equal_calls_give_equal_bits():
-    c = Case([(5000, 1), (300, 2)], heads=2, share=4, dim=128, page=32, dtype=torch.bfloat16, rot=128)
+def test_many_rows_of_a_long_context_are_cut_and_joined():
+    c = Case([(3500, 30), (200, 1), (1000, 90)], heads=1, share=2, dim=64, page=64, dtype=torch.bfloat16, rot=64)
+    attend(c)
+    attend(c, 700, 5)
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_equal_calls_give_equal_bits(new):
+    c = Case([(5000, new), (300, 2)], heads=2, share=4, dim=128, page=32, dtype=torch.bfloat16, rot=128)
     cache, batch, rope = c.dev(kq)
     q = c.q.to(DEV)
     first = kq.kronq_kv_attention(q, cache, batch, rope=rope)
