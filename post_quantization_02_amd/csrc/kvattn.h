@@ -30,19 +30,35 @@ struct AttnView {
 // cut the keys.  Every wave works its unit out from cu and ctx by itself, 64
 // sequences at a time.
 
-__device__ inline int wave_scan(int x) {              // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if ((int)(threadIdx.x & 63) >= d) x += y;
-  }
+// Data-parallel moves within the wave (rows of 16 lanes, then their last lanes):
+// they wait for nothing, where exchanges through LDS cost 100 cycles a step.
+template <int CTRL, int ROWS>
+__device__ inline int moved(int x) {                  // 0 where nothing comes
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ inline double moved(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = moved<CTRL, ROWS>((int)(uint32_t)b), hi = moved<CTRL, ROWS>((int)(uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <typename V>
+__device__ inline V wave_scan(V x) {                  // inclusive
+  x += moved<0x111, 0xF>(x);                          // row_shr:1, 2, 4, 8
+  x += moved<0x112, 0xF>(x);
+  x += moved<0x114, 0xF>(x);
+  x += moved<0x118, 0xF>(x);
+  x += moved<0x142, 0xA>(x);                          // row_bcast:15 to rows 1 and 3
+  x += moved<0x143, 0xC>(x);                          // row_bcast:31 to rows 2 and 3
   return x;
 }
 
 __device__ inline double wave_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-  return x;
+  const uint64_t b = __builtin_bit_cast(uint64_t, wave_scan(x));
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 // The unit `want`; by_row: the sequence of row `want`, its first unit.  false:
@@ -72,18 +88,18 @@ __device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit&
     const uint64_t hit = __ballot(mine);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      u.b = b0 + l;
-      u.base = __shfl(upto - n, l);
-      u.chunks = __shfl(chunks, l);
-      u.row0 = __shfl(s.row0, l);
-      u.len = __shfl(s.len, l);
-      u.ctx = __shfl(s.ctx, l);
+      u.b = b0 + l;                                   // the same in all lanes, and known to be
+      u.base = __builtin_amdgcn_readlane(upto - n, l);
+      u.chunks = __builtin_amdgcn_readlane(chunks, l);
+      u.row0 = __builtin_amdgcn_readlane(s.row0, l);
+      u.len = __builtin_amdgcn_readlane(s.len, l);
+      u.ctx = __builtin_amdgcn_readlane(s.ctx, l);
       const int rest = by_row ? 0 : want - u.base;
       u.qtile = rest / u.chunks;
       u.chunk = rest % u.chunks;
       return true;
     }
-    before = __shfl(upto, 63);
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
   return false;
 }
@@ -122,7 +138,7 @@ __device__ inline void query8(const T* p, int d, const RopeView& rope, int64_t p
 __device__ constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 
 // A row's query as fp16, N runs of eight values at first + step k, times 2^e2 so
-// that its largest value is in [2^3, 2^4), in PARTS parts (the second is what the
+// that its largest value is in [2^10, 2^11), in PARTS parts (the second is what the
 // first's rounding left).  Returns f, by which products with it become scores in
 // powers of two; NaN for a row that has none (an entry that is not finite, a
 // position without angles).  LANES lanes 64 / LANES apart share the row.
@@ -154,7 +170,7 @@ __device__ inline float load_query(const AttnView& a, const Unit& u, int head, i
   int e2 = 0;
   if (!bad && big > 0) {
     frexpf(big, &e2);                                 // big < 2^e2
-    e2 = 4 - e2;
+    e2 = 11 - e2;
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -172,36 +188,51 @@ __device__ inline float load_query(const AttnView& a, const Unit& u, int head, i
 
 __device__ inline half2_t as_half2(uint32_t x) { return __builtin_bit_cast(half2_t, x); }
 
-// Pairs of values c - z.  1024 + c is the fp16 number 0x6400 | c, and
-// 1024 + 16 c is 0x6400 | 16 c; zero holds z in both halves (0x6400 | z, and
-// 64 + z = 0x5400 | 16 z).  All differences are exact.
-__device__ inline half2_t low_pair(uint32_t x, half2_t zero1024) {
-  return as_half2((x & 0x000F000Fu) | 0x64006400u) - zero1024;
-}
-__device__ inline half2_t high_pair(uint32_t x, half2_t zero64) {
-  return as_half2((x & 0x00F000F0u) | 0x64006400u) * half2_t{(_Float16)0.0625f, (_Float16)0.0625f} - zero64;
-}
-
-// A word's eight codes minus their zero point, in kOrder.
-__device__ inline half8_t unpack_word(uint32_t w, half2_t zero1024, half2_t zero64) {
-  const half2_t a = low_pair(w, zero1024), b = high_pair(w, zero64);
-  const half2_t c = low_pair(w >> 8, zero1024), d = high_pair(w >> 8, zero64);
-  return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// What a row keeps while its keys go by: the maximum m of f S, its lane's part
-// of l, and the factor 2^-e under which the products of weights and value scales
-// enter the matrix cores as fp16.  e follows the row's largest such product:
-// where that was last set it lies in [2^5, 2^6), and products up to 2^14 pass
-// before it is set again, so that products 2^-20 of the largest are still normal
-// numbers whatever the scales' range.  m is raised only where a score leaves it
-// behind by 2^kLazy.
-constexpr int kLazy = 8, kRoom = 6, kTop = 14, kNone = -127;
-
-struct RowState {
-  float m = -INFINITY, l = 0, limit = 0;   // limit 2^(kTop + e); 0: nothing seen yet
-  int e = kNone;
+// Codes as fp16 integers c - z.  1024 + c is the fp16 number 0x6400 | c, and
+// 1024 + 16 c is 0x6400 | 16 c, so a code in bits 0..3 or 4..7 of a half becomes a
+// number in one bit-field insert, and loses 1024 + z, or after a factor 1/16
+// 64 + z, in one packed addition for two: all exact.  The constants live in
+// registers that the compiler does not look into: as literals they would cost a
+// second operation each.
+struct Unpacker {
+  uint32_t low, high, bias;
+  __device__ inline Unpacker() : low(0x000F000Fu), high(0x00F000F0u), bias(0x64006400u) {
+    asm("" : "+s"(low));
+    asm("" : "+s"(high));
+    asm("" : "+v"(bias));
+  }
+  __device__ inline half2_t low_pair(uint32_t x, half2_t zero1024) const {
+    return as_half2((x & low) | (bias & ~low)) - zero1024;
+  }
+  __device__ inline half2_t high_pair(uint32_t x, half2_t zero64) const {
+    return as_half2((x & high) | (bias & ~high)) * half2_t{(_Float16)0.0625f, (_Float16)0.0625f} - zero64;
+  }
+  // A word's eight codes minus their zero point, in kOrder.
+  __device__ inline half8_t word(uint32_t w, half2_t zero1024, half2_t zero64) const {
+    const half2_t a = low_pair(w, zero1024), b = high_pair(w, zero64);
+    const half2_t c = low_pair(w >> 8, zero1024), d = high_pair(w >> 8, zero64);
+    return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+  }
 };
+
+// A zero point's constants for it: 1024 + z (0x6400 | z) and 64 + z
+// (0x5400 | 16 z), in both halves.
+__device__ inline uint32_t zero1024_of(uint32_t z) { return (z * 0x00010001u) | 0x64006400u; }
+__device__ inline uint32_t zero64_of(uint32_t z) { return (z * 0x00100010u) | 0x54005400u; }
+
+// Products of weights and value scales enter the matrix cores as fp16 under a
+// row's factor 2^-e.  e follows the row's largest such product: where that was
+// last set it lies in [2^5, 2^6), and products up to 2^14 pass before it is set
+// again, so that products 2^-20 of the largest are still normal numbers whatever
+// the scales' range.  A row's maximum m is raised only where a score leaves it
+// behind by 2^kLazy.
+constexpr int kLazy = 8, kRoom = 6, kTop = 14;
+constexpr int kLeast = -126, kMost = 120;             // of e; kLeast where nothing was seen yet
+
+// Exponent e for a row's largest product (positive).
+__device__ inline int exponent_for(float largest) {
+  return (int)(__float_as_uint(largest) >> 23) - 126 - kRoom;
+}
 
 // kvrows.hip: the kernel of many rows
 kronq_status kv_rows_launch(const AttnView& a, int dim, int32_t dtype, hipStream_t s);

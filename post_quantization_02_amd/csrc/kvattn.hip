@@ -1,11 +1,11 @@
 // Attention over the 4-bit paged key/value cache.
 //
 // For each row's head: scores S_j = s_j (q . (c_j - z_j)) over the visible
-// positions j, a running maximum m and sum l = sum_j 2^(f (S_j - m)) with
-// f = scale log2(e), and O = sum_j 2^(f (S_j - m)) s'_j (c'_j - z'_j), all in
-// one pass over the codes; out = O / l.  The matrix cores see codes minus zero
-// points as fp16 integers (exact); the scales of keys multiply scores, those of
-// values multiply weights, both in fp32.
+// positions j, a running maximum m of f S_j with f = scale log2(e), the sum
+// l = sum_j 2^(f S_j - m), and O = sum_j 2^(f S_j - m) s'_j (c'_j - z'_j), all in
+// one pass over the codes; out = O / l.  The matrix cores see codes as fp16
+// numbers (exact); the scales of keys multiply scores, those of values multiply
+// weights, both in fp32.
 #include <algorithm>
 #include <cmath>
 
@@ -29,26 +29,40 @@ namespace {
 template <int DIM>
 struct RawTile {
   uint32_t k[2][DIM / 32];
-  uint32_t kz[2];          // grid words of this lane's key rows
-  u32x4 ks[2], vs[2];      // grid words of keys 8 g .. 8 g + 7
   uint32_t v[8][(DIM + 127) / 128];
-  bool bad;                // the page of those keys is out of range
+  uint32_t word;           // lanes 0..31: the key's grid word, 32..63: the value's, of key lane % 32
 };
 
-template <int DIM>
-__device__ inline void load_tile(const KvView& c, const int32_t* table, int head, int key0, RawTile<DIM>& t) {
+// The pages of a tile's two halves (a page holds at least 16 keys).
+struct TilePages { PageAt a, b; };
+
+template <bool SMALL>
+__device__ inline TilePages tile_pages(const KvView& c, const int32_t* table, int key0) {
+  TilePages p;
+  p.a = page_at(c, table, key0);
+  p.b = SMALL ? page_at(c, table, key0 + 16) : p.a;
+  return p;
+}
+
+// A tile's data.  Key0 and pages are the same for all lanes, so with pages that
+// hold whole tiles every address is a scalar base and a lane's constant offset;
+// with pages of 16 keys (SMALL) a lane chooses between two bases.
+template <int DIM, bool SMALL>
+__device__ inline void load_tile(const KvView& c, const TilePages& p, int head, int key0, RawTile<DIM>& t) {
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int in_page = (1 << c.lgp) - 1;
-  // a page holds at least 16 keys: each half of the tile lies in one
-  const PageAt p0 = page_at(c, table, key0), p1 = page_at(c, table, key0 + 16);
-  const int64_t slot0 = ((int64_t)head << c.lgp) + (key0 & in_page);
-  const int64_t slot1 = ((int64_t)head << c.lgp) + ((key0 + 16) & in_page);
+  const int64_t first = (int64_t)head << c.lgp;
+  const int64_t slot = first + (key0 & in_page), slot2 = SMALL ? first : slot + 16;
+  auto pick = [&](bool up, const uint8_t* base, int64_t stride, int row) {
+    const uint8_t* lo = base + p.a.page * stride + slot * row;
+    const uint8_t* hi = base + p.b.page * stride + slot2 * row;
+    return up ? hi : lo;
+  };
   {
-    const bool up = (i >> 3) != 0;
-    const int64_t page = up ? p1.page : p0.page;
-    const int64_t slot = (up ? slot1 : slot0) + 8 * ((i >> 2) & 1) + (i & 3);
-    const uint8_t* k = c.kc + page * c.kcs + slot * (DIM / 2) + g * (DIM / 8);
-    const uint32_t* kg = c.kg + page * c.kgs + slot;
+    const int row = 8 * ((i >> 2) & 1) + (i & 3), up = i >> 3;
+    const uint8_t* k;
+    if constexpr (SMALL) k = pick(up, c.kc, c.kcs, DIM / 2) + (row * (DIM / 2) + g * (DIM / 8));
+    else k = c.kc + p.a.page * c.kcs + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + g * (DIM / 8));
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       if constexpr (DIM == 64) {
@@ -58,22 +72,13 @@ __device__ inline void load_tile(const KvView& c, const int32_t* table, int head
         for (int w = 0; w < DIM / 32; w += 4)
           *reinterpret_cast<u32x4*>(t.k[a] + w) = *reinterpret_cast<const u32x4*>(k + 4 * a * (DIM / 2) + 4 * w);
       }
-      t.kz[a] = kg[4 * a];
     }
   }
   {
-    const bool up = (g >> 1) != 0;
-    const int64_t page = up ? p1.page : p0.page;
-    const int64_t slot = (up ? slot1 : slot0) + 8 * (g & 1);
-    const uint32_t* kg = c.kg + page * c.kgs + slot;
-    const uint32_t* vg = c.vg + page * c.vgs + slot;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      t.ks[a] = *reinterpret_cast<const u32x4*>(kg + 4 * a);
-      t.vs[a] = *reinterpret_cast<const u32x4*>(vg + 4 * a);
-    }
-    t.bad = up ? p1.bad : p0.bad;
-    const uint8_t* v = c.vc + page * c.vcs + slot * (DIM / 2) + i * (DIM / 32);
+    const int row = 8 * (g & 1), up = g >> 1;
+    const uint8_t* v;
+    if constexpr (SMALL) v = pick(up, c.vc, c.vcs, DIM / 2) + (row * (DIM / 2) + i * (DIM / 32));
+    else v = c.vc + p.a.page * c.vcs + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + i * (DIM / 32));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (DIM == 64)
@@ -84,17 +89,29 @@ __device__ inline void load_tile(const KvView& c, const int32_t* table, int head
         *reinterpret_cast<u32x2*>(t.v[j]) = *reinterpret_cast<const u32x2*>(v + j * (DIM / 2));
     }
   }
+  {
+    const int up = (lane >> 4) & 1;
+    const uint32_t* kg = c.kg + (SMALL && up ? p.b.page * c.kgs + slot2 : p.a.page * c.kgs + slot + 16 * up);
+    const uint32_t* vg = c.vg + (SMALL && up ? p.b.page * c.vgs + slot2 : p.a.page * c.vgs + slot + 16 * up);
+    t.word = (lane < 32 ? kg : vg)[lane & 15];
+  }
 }
 
-template <int DIM, typename T, int PARTS>
-__global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
+template <int DIM, typename T, int PARTS, bool SMALL>
+__global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnView a) {
   constexpr int BM = 16, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
+  constexpr int AHEAD = 2;                            // tiles in registers; a third one gained nothing
   __shared__ float lds_o[4][BM][PAD];
   __shared__ float lds_m[4][BM], lds_l[4][BM];
+  // of a tile's grids: scales (32 keys, 32 values) and the zero points' constants
+  __shared__ __align__(16) float lds_s[4][64];
+  __shared__ __align__(16) uint32_t lds_kz[4][32][2];
+  __shared__ __align__(16) uint16_t lds_vz[4][2][32];
   Unit u;
   if (!find_unit<BM, KT>(a, blockIdx.x, false, u)) return;
   const int head = blockIdx.y;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int pos_lo, pos_hi;
   const Span span = span_of(a.c, a.shape, u, BM, KT, pos_lo, pos_hi);
   int v0, v1;
@@ -102,103 +119,142 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
   const int share = a.shape.share, window = a.shape.window, sinks = a.shape.sinks;
   const int32_t* table = a.c.table + (int64_t)u.b * a.c.ldt;
 
+  // The first tiles are on their way while the query is made ready.  Past its last
+  // tile a wave asks for that one again: a load that may not happen would have to
+  // be waited for together with those that must have.
+  RawTile<DIM> raw[AHEAD];
+  TilePages at[AHEAD]{};
+  const int w0 = v0 + wave;
+  auto tile_key = [&](int v) { return key_of(span, min(v, v1 - 1), KT); };
+  if (w0 < v1) {
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) at[n] = tile_pages<SMALL>(a.c, table, tile_key(w0 + 4 * n));
+#pragma unroll
+    for (int n = 0; n < AHEAD - 1; ++n) load_tile<DIM, SMALL>(a.c, at[n], head, tile_key(w0 + 4 * n), raw[n]);
+  }
+
   // this lane's query row
   const int r = u.qtile * BM + i, pos = u.ctx - u.len + min(r / share, u.len - 1);
   half8_t q1[KS], q2[PARTS > 1 ? KS : 1];
   const float f = load_query<T, PARTS, KS, 4>(a, u, head, r, g * (DIM / 4), 8, q1, q2);
 
+  const Unpacker un;
   f32x4 o[VT];
 #pragma unroll
   for (int k = 0; k < VT; ++k) o[k] = f32x4{0, 0, 0, 0};
-  RowState st;
-  RawTile<DIM> raw;
-  if (v0 + wave < v1) load_tile<DIM>(a.c, table, head, key_of(span, v0 + wave, KT), raw);
-  for (int v = v0 + wave; v < v1; v += 4) {
-    const RawTile<DIM> cur = raw;
-    const int key0 = key_of(span, v, KT);
-    if (v + 4 < v1) load_tile<DIM>(a.c, table, head, key_of(span, v + 4, KT), raw);
+  float m = -INFINITY, l = 0;                         // of f S; l of this lane's keys
+  int e = kLeast;
 
-    // scores
+  // Tile v, whose data and pages are given: the data of tile v + 4 (AHEAD - 1) (of
+  // pages looked up a tile before) and the pages of the tile after that are asked
+  // for on the way.
+  auto step = [&](int v, const RawTile<DIM>& cur, TilePages& pages, RawTile<DIM>& next, const TilePages& ahead) {
+    const int key0 = key_of(span, v, KT);
+    // keys 8 g + x are this lane's; all are seen, but in the tiles at the edges
+    const bool edge = key0 + KT - 1 > pos_lo || (window && key0 <= pos_hi - window && key0 + KT > sinks) ||
+                      pages.a.bad || pages.b.bad;
+    const bool bad = (g >> 1) ? pages.b.bad : pages.a.bad;
+    {
+      const uint32_t z = cur.word & 15, z1 = zero1024_of(z), z2 = zero64_of(z);
+      lds_s[wave][lane] = __uint_as_float(cur.word & ~15u);
+      if (lane < 32) {
+        *reinterpret_cast<u32x2_alias*>(lds_kz[wave][lane]) = u32x2_alias{z1, z2};
+      } else {
+        lds_vz[wave][0][lane - 32] = (uint16_t)z1;
+        lds_vz[wave][1][lane - 32] = (uint16_t)z2;
+      }
+    }
+    load_tile<DIM, SMALL>(a.c, ahead, head, tile_key(v + 4 * (AHEAD - 1)), next);
+    pages = tile_pages<SMALL>(a.c, table, tile_key(v + 4 * AHEAD));
+    __builtin_amdgcn_wave_barrier();                  // those parts of LDS are this wave's alone
     f32x4 sc[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const uint32_t z = cur.kz[b] & 15;
-      const half2_t z1 = as_half2((z * 0x00010001u) | 0x64006400u), z2 = as_half2((z * 0x00100010u) | 0x54005400u);
+      const u32x2_alias z = *reinterpret_cast<const u32x2_alias*>(lds_kz[wave][8 * (i >> 2) + 4 * b + (i & 3)]);
+      const half2_t z1 = as_half2(z.x), z2 = as_half2(z.y);
       sc[b] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const half8_t kv = unpack_word(cur.k[b][k], z1, z2);
+        const half8_t kv = un.word(cur.k[b][k], z1, z2);
         sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q1[k], sc[b], 0, 0, 0);
         if constexpr (PARTS > 1) sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q2[k], sc[b], 0, 0, 0);
       }
     }
-    // keys 8 g + x: which are visible?  All are, but in the tiles at the edges.
-    const int first = key0 + 8 * g;
-    const bool whole = key0 + KT - 1 <= pos_lo &&
-                       (!window || key0 > pos_hi - window || key0 + KT <= sinks);
-    bool seen[8];
     float s[8], vs[8], top = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const int j = first + x;
-      seen[x] = whole || (j <= pos && (!window || j > pos - window || j < sinks));
-      const float ks = cur.bad ? kNan : __uint_as_float(cur.ks[x >> 2][x & 3] & ~15u);
-      vs[x] = cur.bad ? kNan : __uint_as_float(cur.vs[x >> 2][x & 3] & ~15u);
-      s[x] = seen[x] ? sc[x >> 2][x & 3] * (ks * f) : -INFINITY;
-      top = fmaxf(top, s[x]);
+    for (int b = 0; b < 2; ++b) {
+      const f32x4_alias ks = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][8 * g + 4 * b]);
+      const f32x4_alias vv = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][32 + 8 * g + 4 * b]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        s[4 * b + x] = sc[b][x] * ks[x];
+        vs[4 * b + x] = vv[x];
+      }
     }
-    if (__any(top > st.m + kLazy || (st.m == -INFINITY && top > st.m))) {
+    if (edge) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int j = key0 + 8 * g + x;
+        const bool seen = j <= pos && (!window || j > pos - window || j < sinks);
+        s[x] = !seen ? -INFINITY : bad ? kNan : s[x];
+        vs[x] = seen ? vs[x] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) top = fmaxf(top, s[x]);
+    top *= f;
+    if (__any(top > m + kLazy || (m == -INFINITY && top > m))) {
       float nm = fmaxf(top, __shfl_xor(top, 16));
       nm = fmaxf(nm, __shfl_xor(nm, 32));
-      nm = fmaxf(nm, st.m);
-      if (st.m != -INFINITY) {
-        const float down = fminf(nm - st.m, 300.0f);
-        const int ne = st.e == kNone ? kNone : max(st.e - (int)ceilf(down), -126);
-        const float by = __builtin_amdgcn_exp2f((float)(st.e - ne) - down);
-        st.l *= __builtin_amdgcn_exp2f(-down);
+      nm = fmaxf(nm, m);
+      if (m != -INFINITY) {
+        const float down = fminf(nm - m, 300.0f);
+        const int ne = max(e - (int)ceilf(down), kLeast);
+        const float by = __builtin_amdgcn_exp2f((float)(e - ne) - down);
+        l *= __builtin_amdgcn_exp2f(-down);
 #pragma unroll
         for (int k = 0; k < VT; ++k) o[k] *= by;
-        st.e = ne;
-        st.limit = ne == kNone ? 0.0f : ldexpf(1.0f, min(ne + kTop, 127));
+        e = ne;
       }
-      st.m = nm;
+      m = nm;
     }
-    const float base = st.m == -INFINITY ? 0.0f : st.m;
-    float y[8], ytop = 0;
+    // weights times 2^-ue, the part of the row's factor that they can carry (none
+    // before the first is known)
+    const int ue = e == kLeast ? 0 : min(max(e, -60), 30);
+    const float base = (m == -INFINITY ? 0.0f : m) + (float)ue;
+    float y[8], ytop = 0, sum = 0;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const float p = __builtin_amdgcn_exp2f(s[x] - base);
-      st.l += p;
-      y[x] = seen[x] ? p * vs[x] : 0.0f;
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[x], f, -base));
+      sum += p;
+      y[x] = p * vs[x];
       ytop = fmaxf(ytop, y[x]);
     }
-    if (__any(ytop > st.limit)) {
+    l += sum * ldexpf(1.0f, ue);
+    if (__any(ytop > ldexpf(1.0f, min(kTop + e - ue, 127)))) {
       ytop = fmaxf(ytop, __shfl_xor(ytop, 16));
       ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
-      if (ytop > st.limit) {
-        const int ne = min(max((int)(__float_as_uint(ytop) >> 23) - 126 - kRoom, -126), 120);
-        const float by = ldexpf(1.0f, st.e - ne);
+      if (ytop > ldexpf(1.0f, min(kTop + e - ue, 127))) {
+        const int ne = min(max(exponent_for(ytop) + ue, kLeast), kMost);
+        const float by = ldexpf(1.0f, e - ne);
 #pragma unroll
         for (int k = 0; k < VT; ++k) o[k] *= by;
-        st.e = ne;
-        st.limit = ldexpf(1.0f, min(ne + kTop, 127));
+        e = ne;
       }
     }
-    const float unit = ldexpf(1.0f, min(-st.e, 126));
+    if (__any(e != ue)) {
+      const float by = ldexpf(1.0f, ue - e);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) y[x] *= by;
+    }
     half8_t p1, p2;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      y[x] *= unit;
       p1[x] = (_Float16)y[x];
       if constexpr (PARTS > 1) p2[x] = (_Float16)(y[x] - (float)p1[x]);
     }
-    half2_t z1[4], z2[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t z = (cur.vs[x >> 1][2 * (x & 1)] & 15) | ((cur.vs[x >> 1][2 * (x & 1) + 1] & 15) << 16);
-      z1[x] = as_half2(z | 0x64006400u);
-      z2[x] = as_half2((z << 4) | 0x54005400u);
-    }
+    const u32x4_alias z1 = *reinterpret_cast<const u32x4_alias*>(&lds_vz[wave][0][8 * g]);
+    const u32x4_alias z2 = *reinterpret_cast<const u32x4_alias*>(&lds_vz[wave][1][8 * g]);
 #pragma unroll
     for (int b = 0; b < VT / 2; ++b) {                // byte b of the words: values 2 b, 2 b + 1
       half2_t lo[4], hi[4];
@@ -206,8 +262,8 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
       for (int x = 0; x < 4; ++x) {
         const uint32_t w = __builtin_amdgcn_perm(cur.v[2 * x + 1][b >> 2], cur.v[2 * x][b >> 2],
                                                  0x0C000C00u | (uint32_t)(b & 3) | ((uint32_t)(4 + (b & 3)) << 16));
-        lo[x] = low_pair(w, z1[x]);
-        hi[x] = high_pair(w, z2[x]);
+        lo[x] = un.low_pair(w, as_half2(z1[x]));
+        hi[x] = un.high_pair(w, as_half2(z2[x]));
       }
       const half8_t va{lo[0].x, lo[0].y, lo[1].x, lo[1].y, lo[2].x, lo[2].y, lo[3].x, lo[3].y};
       const half8_t vb{hi[0].x, hi[0].y, hi[1].x, hi[1].y, hi[2].x, hi[2].y, hi[3].x, hi[3].y};
@@ -218,20 +274,29 @@ __global__ __launch_bounds__(256) void kv_attention16(AttnView a) {
         o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p2, o[2 * b + 1], 0, 0, 0);
       }
     }
+  };
+  for (int v = w0; v < v1; v += 4 * AHEAD) {
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      if (v + 4 * n >= v1) break;
+      step(v + 4 * n, raw[n], at[n], raw[(n + AHEAD - 1) % AHEAD], at[(n + AHEAD - 1) % AHEAD]);
+    }
   }
 
   // the four waves' parts
-  st.l += __shfl_xor(st.l, 16);
-  st.l += __shfl_xor(st.l, 32);
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
   if (lane < 16) {
-    lds_m[wave][i] = st.m;
-    lds_l[wave][i] = st.l;
+    lds_m[wave][i] = m;
+    lds_l[wave][i] = l;
   }
-  const float back = ldexpf(1.0f, st.e);
+  const float back = ldexpf(1.0f, e);
 #pragma unroll
   for (int rr = 0; rr < 4; ++rr) {
 #pragma unroll
-    for (int k = 0; k < VT; ++k) lds_o[wave][i][VT * (4 * g + rr) + k] = o[k][rr] * back;
+    for (int k = 0; k < VT; k += 4)
+      *reinterpret_cast<f32x4*>(&lds_o[wave][i][VT * (4 * g + rr) + k]) =
+          f32x4{o[k][rr], o[k + 1][rr], o[k + 2][rr], o[k + 3][rr]} * back;
   }
   __syncthreads();
   // thread: 8 values of one row at a time
@@ -332,11 +397,20 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per) {
 // ---- launch
 //
 // Sequences of up to kFewRows rows x share go to the 16-row kernel, which reads
-// the cache once for each 16 of them; longer ones to the 128-row kernel.
+// the cache once for each 16 of them; longer ones to the 128-row kernel.  Both
+// take any length, so a batch whose sequences have few rows on average is one
+// launch of the first (a launch that finds nothing costs 5 us).
 
 constexpr int kFewRows = 32;
-constexpr int kMinTiles16 = 8;           // 256 keys: a chunk of 64 for each wave
-constexpr int kUnits16 = 2048;           // chunks over all key heads that a launch aims at
+constexpr int kMinTiles16 = 8;           // tiles of a chunk at least: two for each wave
+// Where the table has room for no more than this, the keys are not cut: eight
+// steps of a wave cost less than a join behind two.
+constexpr int kWholeTiles16 = 32;
+// Chunks over all key heads that a launch aims at: a little under the 768
+// workgroups that are resident at once (three on a CU), because a unit's start (its
+// search, its query, the first tile) takes 8 us and all units' starts then pass
+// together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72.
+constexpr int kUnits16 = 704;
 constexpr int kMinTiles128 = 4;          // 256 keys
 constexpr int kUnits128 = 512;
 
@@ -351,14 +425,14 @@ struct Plan {
 Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
   Plan p{};
   const int64_t n = rows * share, some = std::min(rows, seqs);
-  // with one sequence the rows decide; with more, few rows for one may be many for another
-  if (seqs > 1 || n <= kFewRows) {
-    const int64_t tiles = std::min((n + 15 * some) / 16, some * ((kFewRows + 15) / 16));
+  const bool few = n <= kFewRows * some;   // on average, or for sure
+  if (few || seqs > 1) {
+    const int64_t tiles = std::min((n + 15 * some) / 16, few ? n : some * ((kFewRows + 15) / 16));
     const int64_t more = std::max<int64_t>(kUnits16 / heads - tiles / 2, 1);
     p.units16 = (int)(tiles + more);
     p.join16 = more > 1;
   }
-  if (n > kFewRows) {
+  if (!few) {
     const int64_t tiles = (n + 127 * std::min<int64_t>(some, n / (kFewRows + 1))) / 128;
     const int64_t more = tiles * heads >= kUnits128 ? 1 : std::max<int64_t>(kUnits128 / heads, 1);
     p.units128 = (int)(tiles + more);
@@ -389,10 +463,12 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
     a.shape.least = 1;
     a.shape.most = both ? kFewRows : INT32_MAX;
     a.units = p.units16;
-    a.min_tiles = kMinTiles16;
+    a.min_tiles = room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
     a.part = ws;
     a.stat = ws + (size_t)p.units16 * a.c.heads * 16 * DIM;
-    hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS>), dim3((unsigned)a.units, (unsigned)a.c.heads), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)a.units, (unsigned)a.c.heads);
+    if (a.c.lgp == 4) hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, false>), grid, dim3(256), 0, s, a);
     KQ_LAUNCHED("kv_attention16");
     if (p.join16) {
       const kronq_status st = join<DIM, 16, 32, T>(a, std::max(kFewRows / a.shape.share, 1), s);

@@ -122,7 +122,7 @@ struct Tile {
 // Unpacks a tile's keys in `left` into LDS, or (FOLD) those of them that fit a
 // pass, and takes them out of `left`.
 template <int DIM, bool FOLD>
-__device__ inline Pass unpack_tile(const Raw<DIM>& t, Tile<DIM, FOLD>& out, int key0, uint64_t& left) {
+__device__ inline Pass unpack_tile(const Unpacker& un, const Raw<DIM>& t, Tile<DIM, FOLD>& out, int key0, uint64_t& left) {
   const int tid = threadIdx.x, lane = tid & 63;
   Pass pass{key0, 0, 0, left};
   uint32_t kw = t.kw, vw = t.vw;
@@ -150,14 +150,14 @@ __device__ inline Pass unpack_tile(const Raw<DIM>& t, Tile<DIM, FOLD>& out, int 
     const int key = tid >> 2;
     const uint32_t word = __shfl(kw, key);
     const uint32_t z = word & 15;
-    const half2_t z1 = as_half2((z * 0x00010001u) | 0x64006400u), z2 = as_half2((z * 0x00100010u) | 0x54005400u);
+    const half2_t z1 = as_half2(zero1024_of(z)), z2 = as_half2(zero64_of(z));
     // bits 2 and 3 exchanged: see the scores' layout
     const int row = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
     half2_t by{};
     if constexpr (FOLD) by = scale_pair(word, pass.ke);
 #pragma unroll
     for (int w = 0; w < DIM / 32; ++w) {
-      half8_t x = unpack_word(t.k[w], z1, z2);
+      half8_t x = un.word(t.k[w], z1, z2);
       if constexpr (FOLD) x *= __builtin_shufflevector(by, by, 0, 1, 0, 1, 0, 1, 0, 1);
       const int piece = ((tid & 3) * (DIM / 32) + w) ^ (row & 7);
       *reinterpret_cast<half8_t*>(&out.k[row][8 * piece]) = x;
@@ -181,8 +181,8 @@ __device__ inline Pass unpack_tile(const Raw<DIM>& t, Tile<DIM, FOLD>& out, int 
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint32_t w = __builtin_amdgcn_perm(t.v[2 * x + 1][b >> 2], t.v[2 * x][b >> 2], sel);
-        lo[x] = low_pair(w, z1[x]);
-        hi[x] = high_pair(w, z2[x]);
+        lo[x] = un.low_pair(w, z1[x]);
+        hi[x] = un.high_pair(w, z2[x]);
         if constexpr (FOLD) lo[x] *= by[x], hi[x] *= by[x];
       }
 #pragma unroll
@@ -228,11 +228,13 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
   for (int k = 0; k < VT; ++k)
 #pragma unroll
     for (int x = 0; x < 16; ++x) o[k][x] = 0;
-  RowState st;
+  float m = -INFINITY, l = 0;                         // of f S; l of this lane's keys
+  int e = kLeast;                                     // not FOLD: O is held times 2^-e
   float ref = -INFINITY;                              // FOLD: O is held times 2^(kUp - ref)
 
   // the tile on its way to LDS, its keys that are still to go there, and the page
   // of the one after it
+  const Unpacker un;
   Raw<DIM> raw;
   uint64_t left = 0;
   PageAt next{0, true};
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
     if (at + 1 < v1) next = lane_page(a.c, table, key_of(span, at + 1, KT));
   };
   auto unpack = [&](int buf) {
-    const Pass p = unpack_tile<DIM, FOLD>(raw, lds[buf], key_of(span, at, KT), left);
+    const Pass p = unpack_tile<DIM, FOLD>(un, raw, lds[buf], key_of(span, at, KT), left);
     if (!left) ++at, fetch();
     return p;
   };
@@ -276,13 +278,13 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
         }
       }
       // entry x of sc[s] is key 32 s + 16 (x / 8) + 8 h + x % 8 of the tile
-      // FOLD: scores are ff sc (f > 0 or not a number)
-      const float ff = FOLD ? (f != f ? f : fmaxf(ldexpf(f, pass.ke), 0x1p-126f)) : 1.0f;
+      // scores are ff sc (ff > 0, or not a number)
+      const float ff = FOLD && f == f ? fmaxf(ldexpf(f, pass.ke), 0x1p-126f) : f;
       if constexpr (!FOLD) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) sc[s][x] *= tile.ks[32 * s + 16 * (x >> 3) + 8 * h + (x & 7)] * f;
+          for (int x = 0; x < 16; ++x) sc[s][x] *= tile.ks[32 * s + 16 * (x >> 3) + 8 * h + (x & 7)];
       }
       if (key0 + KT - 1 > wave_lo || (window && key0 <= wave_hi - window && key0 + KT > sinks) || ~pass.keys) {
 #pragma unroll
@@ -300,36 +302,37 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[s][x]);
-      if (FOLD) top *= ff;
+      top *= ff;
       const float vtop = FOLD ? top + (float)pass.ve : top;
-      if (__any(top > st.m + kLazy || (st.m == -INFINITY && top > st.m) || (FOLD && vtop > ref + kLazy))) {
-        const float row = fmaxf(top, __shfl_xor(top, 32)), nm = fmaxf(row, st.m);
-        if (st.m != -INFINITY) {
-          const float down = fminf(nm - st.m, 300.0f);
+      if (__any(top > m + kLazy || (m == -INFINITY && top > m) || (FOLD && vtop > ref + kLazy))) {
+        const float row = fmaxf(top, __shfl_xor(top, 32)), nm = fmaxf(row, m);
+        if (m != -INFINITY) {
+          const float down = fminf(nm - m, 300.0f);
           float by = __builtin_amdgcn_exp2f(-down);
-          st.l *= by;
+          l *= by;
           if constexpr (FOLD) {
             const float nref = fmaxf(row + (float)pass.ve, ref);
             by = __builtin_amdgcn_exp2f(fmaxf(ref - nref, -300.0f));
             ref = nref;
           } else {
-            const int ne = st.e == kNone ? kNone : max(st.e - (int)ceilf(down), -126);
-            by = __builtin_amdgcn_exp2f((float)(st.e - ne) - down);
-            st.e = ne;
-            st.limit = ne == kNone ? 0.0f : ldexpf(1.0f, min(ne + kTop, 127));
+            const int ne = max(e - (int)ceilf(down), kLeast);
+            by = __builtin_amdgcn_exp2f((float)(e - ne) - down);
+            e = ne;
           }
 #pragma unroll
           for (int k = 0; k < VT; ++k) o[k] *= by;
         } else if (FOLD && nm != -INFINITY) {
           ref = nm + (float)pass.ve;
         }
-        st.m = nm;
+        m = nm;
       }
-      const float base = st.m == -INFINITY ? 0.0f : st.m;
-      // FOLD: weights for O are 2^(ff sc + up), which times 2^(-base - up) are the
-      // sum's; where that is too far for one fp32 number to do for both, they are
-      // added up by themselves
-      const float up = FOLD ? (ref == -INFINITY ? 0.0f : (float)(pass.ve + kUp) - ref) : 0.0f;
+      const float base = m == -INFINITY ? 0.0f : m;
+      // weights are 2^(ff sc + up).  FOLD: for O; times 2^(-base - up) they are the
+      // sum's, and where that is too far for one fp32 number to do for both, they
+      // are added up by themselves.  Otherwise: times 2^-ue, the part of the row's
+      // factor that they can carry (none before the first is known).
+      const int ue = e == kLeast ? 0 : min(max(e, -60), 30);
+      const float up = !FOLD ? -base - (float)ue : ref == -INFINITY ? 0.0f : (float)(pass.ve + kUp) - ref;
       float ytop = 0, sum = 0;
       if (FOLD && __any(-base - up > 60.0f)) {
         float apart = 0;
@@ -337,13 +340,13 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int x = 0; x < 16; ++x) apart += __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, -base));
-        st.l += -base - up > 60.0f ? apart : 0.0f;
+        l += -base - up > 60.0f ? apart : 0.0f;
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          const float p = __builtin_amdgcn_exp2f(FOLD ? fmaf(sc[s][x], ff, up) : sc[s][x] - base);
+          const float p = __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, up));
           sum += p;
           if constexpr (FOLD) {
             sc[s][x] = p;
@@ -353,22 +356,23 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
             ytop = fmaxf(ytop, sc[s][x]);
           }
         }
-      st.l += !FOLD ? sum : -base - up > 60.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(-base - up);
+      l += !FOLD ? sum * ldexpf(1.0f, ue) : -base - up > 60.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(-base - up);
       if constexpr (!FOLD) {
-        if (__any(ytop > st.limit)) {
+        if (__any(ytop > ldexpf(1.0f, min(kTop + e - ue, 127)))) {
           ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
-          if (ytop > st.limit) {
-            const int ne = min(max((int)(__float_as_uint(ytop) >> 23) - 126 - kRoom, -126), 120);
-            const float by = ldexpf(1.0f, st.e - ne);
+          if (ytop > ldexpf(1.0f, min(kTop + e - ue, 127))) {
+            const int ne = min(max(exponent_for(ytop) + ue, kLeast), kMost);
+            const float by = ldexpf(1.0f, e - ne);
 #pragma unroll
             for (int k = 0; k < VT; ++k) o[k] *= by;
-            st.e = ne;
-            st.limit = ldexpf(1.0f, min(ne + kTop, 127));
+            e = ne;
           }
         }
-        const float unit = ldexpf(1.0f, min(-st.e, 126));
+        if (__any(e != ue)) {
+          const float by = ldexpf(1.0f, ue - e);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) sc[s] *= unit;
+          for (int s = 0; s < 2; ++s) sc[s] *= by;
+        }
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -393,14 +397,14 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
     __syncthreads();
   }
 
-  st.l += __shfl_xor(st.l, 32);
+  l += __shfl_xor(l, 32);
   if (r >= u.len * share) return;
-  if (pos >= room_of(a.c)) st.l = kNan;               // a position without a column
+  if (pos >= room_of(a.c)) l = kNan;               // a position without a column
   // O is held times 2^-(2 back): in two steps, each within fp32
-  const float back = __builtin_amdgcn_exp2f(!FOLD ? 0.5f * st.e : ref == -INFINITY ? 0.0f : 0.5f * (ref - st.m - (float)kUp));
+  const float back = __builtin_amdgcn_exp2f(!FOLD ? 0.5f * e : ref == -INFINITY ? 0.0f : 0.5f * (ref - m - (float)kUp));
   if (u.chunks == 1) {
     const int tok = r / share, qh = head * share + r % share;
-    const float by = st.l == 0 ? 0.0f : back / st.l;      // 0 of a row that sees nothing
+    const float by = l == 0 ? 0.0f : back / l;      // 0 of a row that sees nothing
     T* out = static_cast<T*>(a.out.data) + (int64_t)(u.row0 + tok) * a.out.row + (int64_t)qh * a.out.head;
 #pragma unroll
     for (int k = 0; k < VT; ++k)
@@ -408,11 +412,11 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
       for (int x = 0; x < 16; x += 4) {
         float y[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) y[z] = st.l == 0 ? 0.0f : o[k][x + z] * back * by;
+        for (int z = 0; z < 4; ++z) y[z] = l == 0 ? 0.0f : o[k][x + z] * back * by;
         store4(out + 32 * k + 2 * x + 4 * h, y);
       }
     if (a.lse && h == 0)
-      a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = st.l == 0 ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+      a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
   } else {
     const int64_t at = ((int64_t)unit * a.c.heads + head) * BM + 32 * wave + i;
 #pragma unroll
@@ -425,8 +429,8 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
         store4(a.part + at * DIM + 32 * k + 2 * x + 4 * h, y);
       }
     if (h == 0) {
-      a.stat[2 * at] = st.m;
-      a.stat[2 * at + 1] = st.l;
+      a.stat[2 * at] = m;
+      a.stat[2 * at + 1] = l;
     }
   }
 }
