@@ -25,6 +25,8 @@ struct HeadsView {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // for LDS that is written in other units than it is read in
+typedef uint16_t u16_alias __attribute__((may_alias));
+typedef uint32_t u32_alias __attribute__((may_alias));
 typedef uint32_t u32x2_alias __attribute__((ext_vector_type(2), may_alias));
 typedef uint32_t u32x4_alias __attribute__((ext_vector_type(4), may_alias));
 typedef float f32x4_alias __attribute__((ext_vector_type(4), may_alias));

@@ -37,12 +37,21 @@ __host__ __device__ inline int seq_of(const int32_t* cu, int seqs, int row) {
 struct PageAt { int page; bool bad; };
 
 // The page of a position >= 0 of the sequence whose table row is given; page 0
-// where there is none in range, so that reading is safe.
-__host__ __device__ inline PageAt page_at(const KvView& c, const int32_t* table, int pos) {
+// where there is none in range, so that reading is safe.  In two parts, an entry
+// (of the last column where there is no such column) and what it comes to, for
+// those who ask early and look late.
+__host__ __device__ inline int page_entry(const KvView& c, const int32_t* table, int pos) {
   const int col = pos >> c.lgp;
-  const int page = col < c.columns ? table[col] : -1;
-  const bool bad = page < 0 || page >= c.pages;
-  return {bad ? 0 : page, bad};
+  return c.columns > 0 ? table[col < c.columns ? col : c.columns - 1] : -1;
+}
+
+__host__ __device__ inline PageAt page_from(const KvView& c, int entry, int pos) {
+  const bool bad = (pos >> c.lgp) >= c.columns || entry < 0 || entry >= c.pages;
+  return {bad ? 0 : entry, bad};
+}
+
+__host__ __device__ inline PageAt page_at(const KvView& c, const int32_t* table, int pos) {
+  return page_from(c, page_entry(c, table, pos), pos);
 }
 
 // Where a row's token lives.  pos < 0: nowhere.  bad: no page in range.

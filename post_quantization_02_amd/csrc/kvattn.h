@@ -234,7 +234,7 @@ __device__ inline int exponent_for(float largest) {
   return (int)(__float_as_uint(largest) >> 23) - 126 - kRoom;
 }
 
-// kvrows.hip: the kernel of many rows
-kronq_status kv_rows_launch(const AttnView& a, int dim, int32_t dtype, hipStream_t s);
+// kvrows.hip: the kernel of many rows, 32 x waves (4 or 8; 4 for dim 256) a tile
+kronq_status kv_rows_launch(const AttnView& a, int dim, int32_t dtype, int waves, hipStream_t s);
 
 }  // namespace kronq

@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int j = key0 + 8 * g + x;
-        const bool seen = j <= pos && (!window || j > pos - window || j < sinks);
+        const bool seen = (j <= pos) & ((window == 0) | (j > pos - window) | (j < sinks));
         s[x] = !seen ? -INFINITY : bad ? kNan : s[x];
         vs[x] = seen ? vs[x] : 0.0f;
       }
@@ -411,15 +411,23 @@ constexpr int kWholeTiles16 = 32;
 // search, its query, the first tile) takes 8 us and all units' starts then pass
 // together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72.
 constexpr int kUnits16 = 704;
-constexpr int kMinTiles128 = 4;          // 256 keys
-constexpr int kUnits128 = 512;
+// The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
+// have that many on average (a tile of keys is unpacked once for all of its rows).
+#ifndef KQ_TALL
+#define KQ_TALL 256
+#endif
+constexpr int kTallRows = KQ_TALL;
+constexpr int kMinTilesRows = 4;         // 256 keys
+// Workgroups resident at once: two of four waves on a CU, or one of eight.  Row
+// tiles alone are enough at twice that; fewer are cut along the keys.
+constexpr int kResident = 512, kResidentTall = 256;
 
 // How a call is cut: units of each kernel (0: not launched; a bound of its row
 // tiles, and chunks on top), and whether there can be chunks to join.
 struct Plan {
-  int units16, units128;
-  bool join16, join128;
-  size_t part16, part128;                // floats of partial results
+  int units16, units_rows, waves;
+  bool join16, join_rows;
+  size_t part16, part_rows;              // floats of partial results
 };
 
 Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
@@ -433,13 +441,15 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
     p.join16 = more > 1;
   }
   if (!few) {
-    const int64_t tiles = (n + 127 * std::min<int64_t>(some, n / (kFewRows + 1))) / 128;
-    const int64_t more = tiles * heads >= kUnits128 ? 1 : std::max<int64_t>(kUnits128 / heads, 1);
-    p.units128 = (int)(tiles + more);
-    p.join128 = more > 1;
+    p.waves = dim < 256 && n >= kTallRows * some ? 8 : 4;
+    const int64_t bm = 32 * p.waves, aim = 2 * (p.waves == 8 ? kResidentTall : kResident) / heads;
+    const int64_t tiles = (n + (bm - 1) * std::min<int64_t>(some, n / (kFewRows + 1))) / bm;
+    const int64_t more = 2 * tiles < aim ? aim - tiles : 1;
+    p.units_rows = (int)(tiles + more);
+    p.join_rows = more > 1;
   }
   if (p.join16) p.part16 = (size_t)p.units16 * heads * 16 * (dim + 2);
-  if (p.join128) p.part128 = (size_t)p.units128 * heads * 128 * (dim + 2);
+  if (p.join_rows) p.part_rows = (size_t)p.units_rows * heads * 32 * p.waves * (dim + 2);
   return p;
 }
 
@@ -458,7 +468,7 @@ kronq_status join(const AttnView& a, int64_t per, hipStream_t s) {
 template <int DIM, typename T, int PARTS>
 kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s) {
   const Plan p = plan_of(a.c.rows, a.c.seqs, a.shape.share, a.c.heads, DIM);
-  const bool both = p.units16 && p.units128;
+  const bool both = p.units16 && p.units_rows;
   if (p.units16) {
     a.shape.least = 1;
     a.shape.most = both ? kFewRows : INT32_MAX;
@@ -475,16 +485,18 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
       if (st) return st;
     }
   }
-  if (p.units128) {
+  if (p.units_rows) {
     a.shape.least = both ? kFewRows + 1 : 1;
     a.shape.most = INT32_MAX;
-    a.units = p.units128;
-    a.min_tiles = kMinTiles128;
+    a.units = p.units_rows;
+    a.min_tiles = kMinTilesRows;
     a.part = ws + p.part16;
-    a.stat = a.part + (size_t)p.units128 * a.c.heads * 128 * DIM;
-    const kronq_status st = kv_rows_launch(a, dim, dtype, s);
-    if (st) return st;
-    if (p.join128) return join<DIM, 128, 64, T>(a, 0, s);
+    a.stat = a.part + (size_t)p.units_rows * a.c.heads * 32 * p.waves * DIM;
+    const kronq_status st = kv_rows_launch(a, dim, dtype, p.waves, s);
+    if (st || !p.join_rows) return st;
+    if constexpr (DIM < 256)
+      if (p.waves == 8) return join<DIM, 256, 64, T>(a, 0, s);
+    return join<DIM, 128, 64, T>(a, 0, s);
   }
   return KRONQ_OK;
 }
@@ -500,7 +512,7 @@ kronq_status launch_dim(const AttnView& a, int32_t dtype, float* ws, hipStream_t
 
 size_t kv_attention_ws_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int dim) {
   const Plan p = plan_of(rows, seqs, q_heads / heads, heads, dim);
-  return std::max((p.part16 + p.part128) * sizeof(float), size_t(16));
+  return std::max((p.part16 + p.part_rows) * sizeof(float), size_t(16));
 }
 
 kronq_status kv_attention_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& q, int q_heads,

@@ -1,16 +1,16 @@
 // Attention over the 4-bit paged cache for sequences with many rows (a prompt
-// that enters in pieces, a long draft): tiles of 128 rows x share of one key
-// head, four waves of 32 rows that share each tile of 64 keys.
+// that enters in pieces, a long draft): tiles of 32 WAVES rows x share of one key
+// head, waves of 32 rows that share each tile of 64 keys.
 //
 // The codes of a tile are unpacked once, into LDS, as fp16 codes minus zero
-// points, while the tile before is multiplied: keys as rows of dim values,
-// values transposed as rows of 64 keys, both read as whole 16-byte operands of
-// the 32x32x16 products:
+// points, while the tile before is multiplied: keys as rows of dim values, by one
+// half of the waves, values transposed as rows of 64 keys, by the other.  Both
+// are read as whole 16-byte operands of the 32x32x16 products:
 //   S^T = K Q^T: lane (row, h) gets, of each 16 keys, the eight keys 8 h and up
 //     (the LDS rows of the keys are ordered for that),
 //   O^T = V^T P^T: which are its k slots, so weights stay in registers.
-// 16-byte pieces of an LDS row are exchanged by an exclusive or with the row, so
-// that eight lanes that read or write at once use all banks.
+// The 16-byte pieces of an LDS row are exchanged so that eight lanes that read or
+// write at once use all banks.
 //
 // FOLD (bf16 results): the scales, too, go into the fp16 operands, as s 2^-e with
 // e of the tile's largest scale; that costs two roundings (2^-11) of each key and
@@ -22,13 +22,18 @@
 // rows.
 #include "kvattn.h"
 
+#include <utility>
+
 namespace kronq {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
-constexpr int BM = 128, KT = 64;
+#ifndef KQ_AHEAD
+#define KQ_AHEAD 1
+#endif
+constexpr int KT = 64;
 
 // FOLD.  Scales of a pass are in 2^-kKeySpread (2^-kValueSpread) to 1 of the
 // largest, which times 2^-e is in [2^(kFoldSet - 1), 2^kFoldSet): times a code of
@@ -38,58 +43,52 @@ constexpr int BM = 128, KT = 64;
 // the row's largest product.
 constexpr int kFoldSet = 10, kKeySpread = 20, kValueSpread = 8, kUp = 6;
 
-// What a thread holds of a tile on its way to LDS: a quarter of one key (key
-// tid / 4), and dim / 16 values of four keys (4 (tid / 16) and up).
-template <int DIM>
-struct Raw {
-  uint32_t k[DIM / 32];
-  uint32_t v[4][(DIM + 127) / 128];
-  uint32_t kw, vw;         // grid words of key `lane`
+// How a tile goes to LDS.  Waves 0 .. WAVES / 2 - 1 take the keys, the others the
+// values: kParts threads a key, kWords words each, as both are loaded.  Values are
+// unpacked by eight keys a thread, of them kVals values each, after an exchange
+// within the wave.
+template <int DIM, int WAVES>
+struct Split {
+  static constexpr int kThreads = 32 * WAVES, kParts = kThreads / KT, kWords = DIM / 8 / kParts;
+  static constexpr int kCols = kThreads / 8, kVals = DIM / kCols;
+  // Where a piece (eight values of a key, or of eight keys a value) stands in its row
+  __device__ static constexpr int key_piece(int piece, int row) {
+    return piece ^ (row & 7) ^ (DIM == 64 ? 0 : kParts == 4 ? (piece / kWords >> 1) * 2 : piece / kWords * 4);
+  }
+  __device__ static constexpr int value_piece(int piece, int d) { return piece ^ ((d ^ (d >> 3)) & 7); }
 };
 
-// The page of key `lane` of a tile; a tile past the table's end is not asked for.
-__device__ inline PageAt lane_page(const KvView& c, const int32_t* table, int key0) {
-  return page_at(c, table, key0 + (threadIdx.x & 63));
-}
+template <int DIM, int WAVES>
+struct Raw {
+  uint32_t w[Split<DIM, WAVES>::kWords];
+  uint32_t kw, vw;                        // grid words of key `lane`
+  bool bad;                               // its page is out of range
+};
 
-template <int DIM>
-__device__ inline void load_raw(const KvView& c, const PageAt& at, int head, int key0, Raw<DIM>& t) {
-  const int tid = threadIdx.x, lane = tid & 63, in_page = (1 << c.lgp) - 1;
-  const int packed = at.bad ? -1 : at.page;
+// Asks for a tile's data.  `at` is the page of key `lane` or, WHOLE, of the tile.
+// (The same loads in all waves: two loads into one register from two branches
+// would be joined by moves, which wait for them.)
+template <int DIM, int WAVES>
+__device__ __forceinline__ void load_raw(const KvView& c, PageAt at, bool whole, int head, int key0, bool keys,
+                                         Raw<DIM, WAVES>& t) {
+  using S = Split<DIM, WAVES>;
+  const int lane = threadIdx.x & 63, id = threadIdx.x & (S::kThreads - 1), in_page = (1 << c.lgp) - 1;
   const int64_t head0 = (int64_t)head << c.lgp;
-  {
-    const int key = tid >> 2, page = max(__shfl(packed, key), 0);
-    const uint8_t* p = c.kc + (int64_t)page * c.kcs + (head0 + ((key0 + key) & in_page)) * (DIM / 2) + (tid & 3) * (DIM / 8);
-    if constexpr (DIM == 64) {
-      *reinterpret_cast<u32x2*>(t.k) = *reinterpret_cast<const u32x2*>(p);
-    } else {
+  const int key = id / S::kParts;
+  const int64_t page = whole ? at.page : __shfl(at.page, key);
+  const uint8_t* p = (keys ? c.kc : c.vc) + page * (keys ? c.kcs : c.vcs) +
+                     (head0 + ((key0 + key) & in_page)) * (DIM / 2) + id % S::kParts * (4 * S::kWords);
+  if constexpr (S::kWords == 2) {
+    *reinterpret_cast<u32x2*>(t.w) = *reinterpret_cast<const u32x2*>(p);
+  } else {
 #pragma unroll
-      for (int w = 0; w < DIM / 32; w += 4)
-        *reinterpret_cast<u32x4*>(t.k + w) = *reinterpret_cast<const u32x4*>(p + 4 * w);
-    }
-  }
-  {
-    const int key = (tid >> 4) * 4, page = max(__shfl(packed, key), 0);   // four keys share a page
-    const uint8_t* p = c.vc + (int64_t)page * c.vcs + (head0 + ((key0 + key) & in_page)) * (DIM / 2) + (tid & 15) * (DIM / 32);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DIM == 64)
-        t.v[j][0] = *reinterpret_cast<const uint16_t*>(p + j * (DIM / 2));
-      else if constexpr (DIM == 128)
-        t.v[j][0] = *reinterpret_cast<const uint32_t*>(p + j * (DIM / 2));
-      else
-        *reinterpret_cast<u32x2*>(t.v[j]) = *reinterpret_cast<const u32x2*>(p + j * (DIM / 2));
-    }
+    for (int w = 0; w < S::kWords; w += 4)
+      *reinterpret_cast<u32x4*>(t.w + w) = *reinterpret_cast<const u32x4*>(p + 4 * w);
   }
   const int64_t slot = head0 + ((key0 + lane) & in_page);
-  t.kw = at.bad ? 0x7FC00000u : c.kg[(int64_t)at.page * c.kgs + slot];
-  t.vw = at.bad ? 0x7FC00000u : c.vg[(int64_t)at.page * c.vgs + slot];
-}
-
-// fp16 factor of a grid word's scale times 2^-e, in both halves.
-__device__ inline half2_t scale_pair(uint32_t word, int e) {
-  const _Float16 h = (_Float16)ldexpf(__uint_as_float(word & ~15u), -e);
-  return half2_t{h, h};
+  t.kw = c.kg[(int64_t)at.page * c.kgs + slot];
+  t.vw = c.vg[(int64_t)at.page * c.vgs + slot];
+  t.bad = at.bad;                         // for later: what is loaded is not waited for here
 }
 
 // Exponent of a grid word's scale (scale < 2^(x - 126)); 0 for one that is zero or
@@ -99,11 +98,18 @@ __device__ inline int exponent_of(uint32_t word) {
   return x == 255 ? 0 : x;
 }
 
-__device__ inline int wave_max(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = max(x, __shfl_xor(x, d));
-  return x;
+__device__ inline int wave_max(int x) {               // x >= 0
+  x = max(x, moved<0x111, 0xF>(x));
+  x = max(x, moved<0x112, 0xF>(x));
+  x = max(x, moved<0x114, 0xF>(x));
+  x = max(x, moved<0x118, 0xF>(x));
+  x = max(x, moved<0x142, 0xA>(x));
+  x = max(x, moved<0x143, 0xC>(x));
+  return __builtin_amdgcn_readlane(x, 63);
 }
+
+// The n lowest bits (all for n > 31, none for n < 1).
+__device__ inline uint32_t below(int n) { return n > 31 ? ~0u : n < 1 ? 0u : (1u << n) - 1; }
 
 // A pass over a tile: the keys in it (bit: key of the tile) and, for FOLD, the
 // exponents of what is in LDS.
@@ -112,103 +118,229 @@ struct Pass {
   uint64_t keys;
 };
 
+// FOLD: the largest exponents of scales that the current ke and ve were made for
+// (0: none yet).  They stay while all keys fit them.
+struct Most { int k, v; };
+
 template <int DIM, bool FOLD>
 struct Tile {
-  _Float16 k[KT][DIM];
-  _Float16 v[DIM][KT];
-  float ks[FOLD ? 1 : KT], vs[FOLD ? 1 : KT];
+  alignas(16) _Float16 k[KT][DIM];
+  alignas(16) _Float16 v[DIM][KT];
+  alignas(16) float ks[FOLD ? 4 : KT];
+  alignas(16) float vs[FOLD ? 4 : KT];
 };
 
-// Unpacks a tile's keys in `left` into LDS, or (FOLD) those of them that fit a
-// pass, and takes them out of `left`.
-template <int DIM, bool FOLD>
-__device__ inline Pass unpack_tile(const Unpacker& un, const Raw<DIM>& t, Tile<DIM, FOLD>& out, int key0, uint64_t& left) {
-  const int tid = threadIdx.x, lane = tid & 63;
+// Which keys of a tile's `left` the next pass takes (all of them unless FOLD), and
+// what unpacking wants to know of each: on `shelf`, 64 words of LDS of the wave's
+// own, its zero point, and for FOLD its scale times 2^-e as fp16 in the upper half
+// (0 for a key of another pass).  In `scales` (not FOLD) the scales themselves.
+template <int DIM, int WAVES, bool FOLD>
+__device__ __forceinline__ Pass choose(const Raw<DIM, WAVES>& t, int key0, bool keys, uint32_t* shelf, float* scales,
+                                       uint64_t& left, Most& most) {
+  using S = Split<DIM, WAVES>;
+  const int lane = threadIdx.x & 63, id = threadIdx.x & (S::kThreads - 1);
   Pass pass{key0, 0, 0, left};
-  uint32_t kw = t.kw, vw = t.vw;
+  uint32_t kw = t.bad ? 0x7FC00000u : t.kw, vw = t.bad ? 0x7FC00000u : t.vw;
   if constexpr (FOLD) {
     // a value scale that is not finite makes its key's scores not numbers, which
     // reaches the rows that see the key and no others
     if ((vw & 0x7F800000u) == 0x7F800000u) kw = 0x7FC00000u, vw = 0;
     if ((kw & 0x7F800000u) == 0x7F800000u) kw = 0x7FC00000u;
-    bool in = (left >> lane) & 1;
     const int kx = exponent_of(kw), vx = exponent_of(vw);
-    const int kmost = wave_max(in ? kx : 0);
-    in = in && (kx == 0 || kx >= kmost - kKeySpread);
-    const int vmost = wave_max(in ? vx : 0);
-    in = in && (vx == 0 || vx >= vmost - kValueSpread);
+    auto fits = [](int x, int largest, int spread) { return x == 0 || (uint32_t)(largest - x) <= (uint32_t)spread; };
+    bool in = (left >> lane) & 1;
+    if (__ballot(in && !(fits(kx, most.k, kKeySpread) && fits(vx, most.v, kValueSpread)))) {
+      most.k = wave_max(in ? kx : 0);
+      in = in && fits(kx, most.k, kKeySpread);
+      most.v = wave_max(in ? vx : 0);
+      in = in && fits(vx, most.v, kValueSpread);
+    }
     pass.keys = __ballot(in);
-    pass.ke = kmost - 126 - kFoldSet;
-    pass.ve = vmost - 126 - kFoldSet;
-    if (!in) kw = vw = 0;                             // a scale of 0
-  } else if (tid < KT) {
-    out.ks[lane] = __uint_as_float(kw & ~15u);
-    out.vs[lane] = __uint_as_float(vw & ~15u);
+    pass.ke = most.k - 126 - kFoldSet;
+    pass.ve = most.v - 126 - kFoldSet;
+    const uint32_t word = keys ? kw : vw;
+    const _Float16 s = in ? (_Float16)ldexpf(__uint_as_float(word & ~15u), -(keys ? pass.ke : pass.ve)) : (_Float16)0.0f;
+    shelf[lane] = (word & 15) | ((uint32_t)__builtin_bit_cast(uint16_t, s) << 16);
+  } else {
+    shelf[lane] = (keys ? kw : vw) & 15;
+    if (id < KT) scales[lane] = __uint_as_float((keys ? kw : vw) & ~15u);
   }
   left &= ~pass.keys;
-  {
-    const int key = tid >> 2;
-    const uint32_t word = __shfl(kw, key);
-    const uint32_t z = word & 15;
-    const half2_t z1 = as_half2(zero1024_of(z)), z2 = as_half2(zero64_of(z));
-    // bits 2 and 3 exchanged: see the scores' layout
-    const int row = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
-    half2_t by{};
-    if constexpr (FOLD) by = scale_pair(word, pass.ke);
-#pragma unroll
-    for (int w = 0; w < DIM / 32; ++w) {
-      half8_t x = un.word(t.k[w], z1, z2);
-      if constexpr (FOLD) x *= __builtin_shufflevector(by, by, 0, 1, 0, 1, 0, 1, 0, 1);
-      const int piece = ((tid & 3) * (DIM / 32) + w) ^ (row & 7);
-      *reinterpret_cast<half8_t*>(&out.k[row][8 * piece]) = x;
-    }
-  }
-  {
-    const int kg = tid >> 4, col = tid & 15;
-    half2_t z1[2], z2[2], by[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t w0 = __shfl(vw, 4 * kg + 2 * x), w1 = __shfl(vw, 4 * kg + 2 * x + 1);
-      const uint32_t z = (w0 & 15) | ((w1 & 15) << 16);
-      z1[x] = as_half2(z | 0x64006400u);
-      z2[x] = as_half2((z << 4) | 0x54005400u);
-      if constexpr (FOLD) by[x] = half2_t{scale_pair(w0, pass.ve).x, scale_pair(w1, pass.ve).x};
-    }
-#pragma unroll
-    for (int b = 0; b < DIM / 32; ++b) {              // byte b of the words: values 2 b, 2 b + 1
-      const uint32_t sel = 0x0C000C00u | (uint32_t)(b & 3) | ((uint32_t)(4 + (b & 3)) << 16);
-      half2_t lo[2], hi[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t w = __builtin_amdgcn_perm(t.v[2 * x + 1][b >> 2], t.v[2 * x][b >> 2], sel);
-        lo[x] = un.low_pair(w, z1[x]);
-        hi[x] = un.high_pair(w, z2[x]);
-        if constexpr (FOLD) lo[x] *= by[x], hi[x] *= by[x];
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int d = col * (DIM / 16) + 2 * b + n;
-        const int piece = (kg >> 1) ^ ((d ^ (d >> 3)) & 7);
-        const half4_t x = n ? half4_t{hi[0].x, hi[0].y, hi[1].x, hi[1].y} : half4_t{lo[0].x, lo[0].y, lo[1].x, lo[1].y};
-        *reinterpret_cast<half4_t*>(&out.v[d][8 * piece + 4 * (kg & 1)]) = x;
-      }
-    }
-  }
   return pass;
 }
 
-// Bound by the vector pipes (the exponentials and what surrounds them) and the
-// matrix cores together.
-template <int DIM, typename T, int QP, int PP, bool FOLD>
-__global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(AttnView a) {
-  constexpr int KS = DIM / 16, VT = DIM / 32;
+// A wave issues in order, and the compiler would put all vector work behind all
+// products (or one operand read before each product): the order that fills both
+// pipes is written out, and this keeps it.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// f(0), .., f(N - 1), each with a constant: register arrays want constant indices
+// before loops are unrolled.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Unpacking one tile, cut into pieces to go between products.  KEYS: this wave
+// unpacks keys, a word a piece; else values, two of eight keys a piece.
+template <int DIM, int WAVES, bool FOLD, bool KEYS>
+struct Unpacking {
+  using S = Split<DIM, WAVES>;
+  static constexpr int kPieces = KEYS ? S::kWords : 4 * ((S::kVals + 3) / 4);
+  half2_t z1[KEYS ? 1 : 4], z2[KEYS ? 1 : 4], by[KEYS ? 1 : 4];
+  u32x4 v0, v1, v2, v3;                               // of four values, pairs of keys
+  uint32_t raw[KEYS ? 1 : S::kVals > 8 ? 16 : 8];     // of each key, this thread's values
+
+  __device__ __forceinline__ void begin(uint32_t* __restrict__ shelf, const Raw<DIM, WAVES>& t) {
+    const int id = threadIdx.x & (S::kThreads - 1);
+    if constexpr (KEYS) {
+      const uint32_t c = shelf[id / S::kParts], z = c & 0xFFFF;
+      z1[0] = as_half2(zero1024_of(z));
+      z2[0] = as_half2(zero64_of(z));
+      by[0] = as_half2(__builtin_amdgcn_perm(c, c, 0x03020302u));
+    } else {
+      // the wave's keys, behind the shelf's first 64 words
+      uint8_t* mine = reinterpret_cast<uint8_t*>(shelf + 64);
+      const int lane = threadIdx.x & 63;
+      if constexpr (S::kWords == 2) {
+        *reinterpret_cast<u32x2_alias*>(mine + 8 * lane) = u32x2_alias{t.w[0], t.w[1]};
+      } else {
+#pragma unroll
+        for (int w = 0; w < S::kWords; w += 4)
+          *reinterpret_cast<u32x4_alias*>(mine + 4 * S::kWords * lane + 4 * w) =
+              u32x4_alias{t.w[w], t.w[w + 1], t.w[w + 2], t.w[w + 3]};
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* p = mine + (lane / S::kCols * 8 + j) * (DIM / 2) + lane % S::kCols * (S::kVals / 2);
+        if constexpr (S::kVals == 2) raw[j] = *p;
+        else if constexpr (S::kVals == 4) raw[j] = *reinterpret_cast<const u16_alias*>(p);
+        else if constexpr (S::kVals == 8) raw[j] = *reinterpret_cast<const u32_alias*>(p);
+        else raw[2 * j] = reinterpret_cast<const u32_alias*>(p)[0], raw[2 * j + 1] = reinterpret_cast<const u32_alias*>(p)[1];
+      }
+      const u32x4_alias c0 = *reinterpret_cast<const u32x4_alias*>(shelf + 8 * (id / S::kCols));
+      const u32x4_alias c1 = *reinterpret_cast<const u32x4_alias*>(shelf + 8 * (id / S::kCols) + 4);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t a = x < 2 ? c0[2 * x] : c1[2 * x - 4], b = x < 2 ? c0[2 * x + 1] : c1[2 * x - 3];
+        const uint32_t z = __builtin_amdgcn_perm(b, a, 0x0C040C00u);
+        z1[x] = as_half2(z | 0x64006400u);
+        z2[x] = as_half2((z << 4) | 0x54005400u);
+        by[x] = as_half2(__builtin_amdgcn_perm(b, a, 0x07060302u));
+      }
+    }
+  }
+
+  template <int W>
+  __device__ __forceinline__ void piece(const Unpacker& un, const Raw<DIM, WAVES>& t,
+                                        Tile<DIM, FOLD>* __restrict__ out) {
+    const int id = threadIdx.x & (S::kThreads - 1);
+    if constexpr (KEYS) {
+      const int key = id / S::kParts, part = id % S::kParts;
+      // bits 2 and 3 exchanged: see the scores' layout
+      const int row = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
+      half8_t x = un.word(t.w[W], z1[0], z2[0]);
+      if constexpr (FOLD) x *= __builtin_shufflevector(by[0], by[0], 0, 1, 0, 1, 0, 1, 0, 1);
+      *reinterpret_cast<half8_t*>(&out->k[row][8 * S::key_piece(part * S::kWords + W, row)]) = x;
+    } else {
+      // keys 2 x and 2 x + 1, values 4 n and up
+      constexpr int n = W / 4, x = W % 4;
+      const int kg = id / S::kCols, col = id % S::kCols;
+      const uint32_t wa = S::kVals > 8 ? raw[4 * x + (n >> 1)] : raw[2 * x];
+      const uint32_t wb = S::kVals > 8 ? raw[4 * x + 2 + (n >> 1)] : raw[2 * x + 1];
+      const uint32_t p = __builtin_amdgcn_perm(wb, wa, n & 1 ? 0x07060302u : 0x05040100u);
+      auto put = [&](half2_t pair) __attribute__((always_inline)) {
+        if constexpr (FOLD) pair *= by[x];
+        return __builtin_bit_cast(uint32_t, pair);
+      };
+      v0[x] = put(un.low_pair(p, z1[x]));
+      v1[x] = put(un.high_pair(p, z2[x]));
+      if constexpr (S::kVals > 2) {
+        v2[x] = put(un.low_pair(p >> 8, z1[x]));
+        v3[x] = put(un.high_pair(p >> 8, z2[x]));
+      }
+      if constexpr (x == 3) {
+        const int d = col * S::kVals + 4 * n;
+        auto store = [&](int y, u32x4 v) __attribute__((always_inline)) {
+          *reinterpret_cast<half8_t*>(&out->v[d + y][8 * S::value_piece(kg, d + y)]) = __builtin_bit_cast(half8_t, v);
+        };
+        store(0, v0);
+        store(1, v1);
+        if constexpr (S::kVals > 2) {
+          store(2, v2);
+          store(3, v3);
+        }
+      }
+    }
+  }
+};
+
+// One stage: the scores of the tile `cur`, and the next tile's codes into `out`.
+// Operands are read two steps ahead.
+template <int DIM, int WAVES, bool FOLD, int QP, bool QLDS, bool KEYS>
+__device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restrict__ cur, Tile<DIM, FOLD>* __restrict__ out,
+                                                  const Unpacker& un, const Raw<DIM, WAVES>& t,
+                                                  uint32_t* __restrict__ shelf, const half8_t (&q1)[DIM / 16],
+                                                  const half8_t (&q2)[QP > 1 ? DIM / 16 : 1],
+                                                  const half8_t (*__restrict__ lds_q)[64], f32x16 (&sc)[2]) {
+  using S = Split<DIM, WAVES>;
+  constexpr int KS = DIM / 16, AHEAD = KQ_AHEAD, RING = AHEAD + 1;
+  const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+  half8_t kv[RING][2], second[QLDS ? RING : 1];
+  auto read = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      kv[k % RING][s] = *reinterpret_cast<const half8_t*>(&cur->k[32 * s + i][8 * S::key_piece(2 * k + h, i)]);
+    if constexpr (QLDS) second[k % RING] = lds_q[k][lane];
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) read(k);
+  Unpacking<DIM, WAVES, FOLD, KEYS> work;
+  work.begin(shelf, t);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) sc[s][x] = 0;
+  in_order();
+  // half step `at`: a product (or two) and its share of the pieces
+  each<2 * KS>([&](auto at) __attribute__((always_inline)) {
+    constexpr int k = at / 2, s = at % 2, N = Unpacking<DIM, WAVES, FOLD, KEYS>::kPieces;
+    if constexpr (s == 0 && k + AHEAD < KS) read(k + AHEAD);
+    sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], q1[k], sc[s], 0, 0, 0);
+    if constexpr (QP > 1)
+      sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], QLDS ? second[QLDS ? k % RING : 0] : q2[QP > 1 ? k : 0],
+                                                     sc[s], 0, 0, 0);
+    each<N>([&](auto w) __attribute__((always_inline)) {
+      if constexpr (w * 2 * KS / N == at) work.template piece<w>(un, t, out);
+    });
+    in_order();
+  });
+}
+
+// Bound by the vector pipes (the exponentials and what surrounds them, and
+// unpacking) and the matrix cores together.
+template <int DIM, typename T, int QP, int PP, bool FOLD, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && QP > 1 && WAVES == 4) ? 1 : 2)
+void kv_attention_rows(AttnView a) {
+  using S = Split<DIM, WAVES>;
+  constexpr int BM = 32 * WAVES, KS = DIM / 16, VT = DIM / 32;
+  constexpr bool QLDS = QP > 1 && DIM == 128 && WAVES == 8;   // queries' second parts: no registers left
   __shared__ Tile<DIM, FOLD> lds[2];
+  __shared__ half8_t lds_q[QLDS ? WAVES : 1][QLDS ? KS : 1][64];
+  __shared__ __align__(16) uint32_t shelves[WAVES][64 + 64 * S::kWords];
   Unit u;
   // key heads are the faster index, so that workgroups on one XCD read few heads;
   // later row tiles see more keys: they come first
   const int head = blockIdx.x % a.c.heads, unit = a.units - 1 - (int)(blockIdx.x / a.c.heads);
   if (!find_unit<BM, KT>(a, unit, false, u)) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool keys = wave < WAVES / 2;
   int pos_lo, pos_hi;
   const Span span = span_of(a.c, a.shape, u, BM, KT, pos_lo, pos_hi);
   int v0, v1;
@@ -222,6 +354,10 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
   const int wave_lo = pos0 + min(r0 / share, u.len - 1), wave_hi = pos0 + min((r0 + 31) / share, u.len - 1);
   half8_t q1[KS], q2[QP > 1 ? KS : 1];
   const float f = load_query<T, QP, KS, 2>(a, u, head, r, 8 * h, 16, q1, q2);
+  if constexpr (QLDS) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) lds_q[wave][k][lane] = q2[k];
+  }
 
   f32x16 o[VT];
 #pragma unroll
@@ -232,51 +368,65 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
   int e = kLeast;                                     // not FOLD: O is held times 2^-e
   float ref = -INFINITY;                              // FOLD: O is held times 2^(kUp - ref)
 
-  // the tile on its way to LDS, its keys that are still to go there, and the page
-  // of the one after it
+  // The tile `at` on its way to LDS, and its keys that are still to go there.  What is asked for is asked for every time, the last
+  // tile again behind the end: see the kernel of few rows.
   const Unpacker un;
-  Raw<DIM> raw;
-  uint64_t left = 0;
-  PageAt next{0, true};
+  Raw<DIM, WAVES> raw;
+  const bool whole = a.c.lgp >= 6;                    // pages hold whole tiles
   int at = v0;
-  auto fetch = [&]() {                                // tile `at`, whose pages are in `next`
-    if (at >= v1) return;
-    const int key0 = key_of(span, at, KT), key = key0 + lane;
-    load_raw<DIM>(a.c, next, head, key0, raw);
-    left = __ballot(key <= pos_hi && (!window || key > pos_lo - window || key < sinks));
-    if (at + 1 < v1) next = lane_page(a.c, table, key_of(span, at + 1, KT));
+  auto tile_key = [&](int v) __attribute__((always_inline)) { return key_of(span, min(v, v1 - 1), KT); };
+  auto page_key = [&](int v) __attribute__((always_inline)) { return tile_key(v) + (whole ? 0 : lane); };
+  auto unseen = [&]() __attribute__((always_inline)) {      // keys of tile `at` that some row sees
+    const int key = tile_key(at) + lane;
+    return (uint64_t)__ballot(key <= pos_hi && (!window || key > pos_lo - window || key < sinks));
   };
-  auto unpack = [&](int buf) {
-    const Pass p = unpack_tile<DIM, FOLD>(un, raw, lds[buf], key_of(span, at, KT), left);
-    if (!left) ++at, fetch();
-    return p;
+  Most most{0, 0};
+  PageAt here{0, true};                               // of tile `at` (WHOLE), or of its key `lane`
+  int next = -1;                                      // the table's entry of the tile after it
+  uint64_t left = 0;
+  if (v0 < v1) {
+    here = page_at(a.c, table, page_key(v0));
+    next = page_entry(a.c, table, page_key(v0 + 1));
+    left = unseen();
+  }
+  // a pass's choice; its tile's data are gone from the registers after the stage that
+  // unpacks it, and the next tile's are asked for
+  auto take = [&](int buf) __attribute__((always_inline)) {
+    return choose<DIM, WAVES, FOLD>(raw, tile_key(at), keys, shelves[wave], keys ? lds[buf].ks : lds[buf].vs, left, most);
   };
-  if (v0 < v1) next = lane_page(a.c, table, key_of(span, v0, KT));
-  fetch();
+  f32x16 sc[2];
+  auto stage = [&](int buf) __attribute__((always_inline)) {
+    __builtin_amdgcn_wave_barrier();                  // the shelf is the wave's own
+    if (keys)
+      scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS, true>(&lds[buf], &lds[buf ^ 1], un, raw, shelves[wave], q1, q2,
+                                                          lds_q[QLDS ? wave : 0], sc);
+    else
+      scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS, false>(&lds[buf], &lds[buf ^ 1], un, raw, shelves[wave], q1, q2,
+                                                           lds_q[QLDS ? wave : 0], sc);
+    if (!left) {
+      ++at;
+      here = page_from(a.c, next, page_key(at));
+      left = unseen();
+    }
+    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), keys, raw);
+    next = page_entry(a.c, table, page_key(at + 1));
+  };
   Pass cur{};
   bool more = v0 < v1;
-  if (more) cur = unpack(0);
+  if (more) {
+    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), keys, raw);
+    cur = take(0);
+    stage(1);                                         // no scores yet
+  }
   __syncthreads();
   for (int buf = 0; more; buf ^= 1) {
     const Tile<DIM, FOLD>& tile = lds[buf];
     const Pass pass = cur;
     const int key0 = pass.key0;
     more = at < v1;
-    if (more) cur = unpack(buf ^ 1);
-    // some row of the wave sees some key
-    if (key0 <= wave_hi && (!window || key0 + KT - 1 > wave_lo - window || key0 < sinks)) {
-      f32x16 sc[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) sc[s][x] = 0;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const half8_t kv = *reinterpret_cast<const half8_t*>(&tile.k[32 * s + i][8 * ((2 * k + h) ^ (i & 7))]);
-          sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, q1[k], sc[s], 0, 0, 0);
-          if constexpr (QP > 1) sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, q2[k], sc[s], 0, 0, 0);
-        }
-      }
+    if (more) cur = take(buf ^ 1);
+    stage(buf);                                       // past the last tile: its data again, which nobody reads
+    {
       // entry x of sc[s] is key 32 s + 16 (x / 8) + 8 h + x % 8 of the tile
       // scores are ff sc (ff > 0, or not a number)
       const float ff = FOLD && f == f ? fmaxf(ldexpf(f, pass.ke), 0x1p-126f) : f;
@@ -289,12 +439,11 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
       if (key0 + KT - 1 > wave_lo || (window && key0 <= wave_hi - window && key0 + KT > sinks) || ~pass.keys) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t in = (uint32_t)(pass.keys >> (32 * s)) >> (8 * h);
+          const int first = key0 + 32 * s + 8 * h;    // bit b: key first + b
+          uint32_t seen = below(pos - first + 1) & ((uint32_t)(pass.keys >> (32 * s)) >> (8 * h));
+          if (window) seen &= ~below(pos - window + 1 - first) | below(sinks - first);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int bit = 16 * (x >> 3) + (x & 7), j = key0 + 32 * s + 8 * h + bit;
-            if (j > pos || (window && j <= pos - window && j >= sinks) || !((in >> bit) & 1)) sc[s][x] = -INFINITY;
-          }
+          for (int x = 0; x < 16; ++x) sc[s][x] = seen & (1u << (16 * (x >> 3) + (x & 7))) ? sc[s][x] : -INFINITY;
         }
       }
       float top = sc[0][0];
@@ -327,37 +476,32 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
         m = nm;
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      // weights are 2^(ff sc + up).  FOLD: for O; times 2^(-base - up) they are the
-      // sum's, and where that is too far for one fp32 number to do for both, they
-      // are added up by themselves.  Otherwise: times 2^-ue, the part of the row's
-      // factor that they can carry (none before the first is known).
+      // Weights are 2^(ff sc + up).  FOLD: as O is held; times 2^(-base - up) they
+      // are the sum's, and where that is too far for one fp32 number to do for both
+      // (`far`), they are added up by themselves.  Otherwise: times 2^-ue, the part of
+      // the row's factor that they can carry (none before the first is known).
       const int ue = e == kLeast ? 0 : min(max(e, -60), 30);
       const float up = !FOLD ? -base - (float)ue : ref == -INFINITY ? 0.0f : (float)(pass.ve + kUp) - ref;
-      float ytop = 0, sum = 0;
-      if (FOLD && __any(-base - up > 60.0f)) {
-        float apart = 0;
+      const bool far = FOLD && __any(-base - up > 60.0f);
+      float sum = 0, apart = 0;
+      if (far) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int x = 0; x < 16; ++x) apart += __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, -base));
-        l += -base - up > 60.0f ? apart : 0.0f;
       }
+      if constexpr (!FOLD) {
+        float ytop = 0;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, up));
-          sum += p;
-          if constexpr (FOLD) {
-            sc[s][x] = p;
-          } else {
+          for (int x = 0; x < 16; ++x) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, up));
+            sum += p;
             const bool seen = sc[s][x] != -INFINITY;  // not seen: whatever scale is there
             sc[s][x] = seen ? p * tile.vs[32 * s + 16 * (x >> 3) + 8 * h + (x & 7)] : 0.0f;
             ytop = fmaxf(ytop, sc[s][x]);
           }
-        }
-      l += !FOLD ? sum * ldexpf(1.0f, ue) : -base - up > 60.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(-base - up);
-      if constexpr (!FOLD) {
         if (__any(ytop > ldexpf(1.0f, min(kTop + e - ue, 127)))) {
           ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
           if (ytop > ldexpf(1.0f, min(kTop + e - ue, 127))) {
@@ -374,25 +518,41 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
           for (int s = 0; s < 2; ++s) sc[s] *= by;
         }
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          half8_t p1, p2;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float y = sc[s][8 * j + x];
-            p1[x] = (_Float16)y;
-            if constexpr (PP > 1) p2[x] = (_Float16)(y - (float)p1[x]);
-          }
-#pragma unroll
-          for (int k = 0; k < VT; ++k) {
-            const int d = 32 * k + i;
-            const half8_t vv = *reinterpret_cast<const half8_t*>(&tile.v[d][8 * ((4 * s + 2 * j + h) ^ ((d ^ (d >> 3)) & 7))]);
-            o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p1, o[k], 0, 0, 0);
-            if constexpr (PP > 1) o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p2, o[k], 0, 0, 0);
-          }
+      // Sixteen keys at a time: their products, and between them the next sixteen's
+      // weights.
+      half8_t p1[2], p2[PP > 1 ? 2 : 1], vv[2][VT];
+      auto weigh = [&](int n, int x) __attribute__((always_inline)) {
+        float y = sc[n >> 1][8 * (n & 1) + x];
+        if constexpr (FOLD) {
+          y = __builtin_amdgcn_exp2f(fmaf(y, ff, up));
+          sum += y;
         }
+        p1[n & 1][x] = (_Float16)y;
+        if constexpr (PP > 1) p2[n & 1][x] = (_Float16)(y - (float)p1[n & 1][x]);
+      };
+      auto read = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < VT; ++k) {
+          const int d = 32 * k + i;
+          vv[n & 1][k] = *reinterpret_cast<const half8_t*>(&tile.v[d][8 * S::value_piece(2 * n + h, d)]);
+        }
+      };
+      read(0);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) weigh(0, x);
+      in_order();
+      each<4 * VT>([&](auto at) __attribute__((always_inline)) {
+        constexpr int n = at / VT, k = at % VT;
+        if constexpr (n < 3 && k == 0) read(n + 1);
+        o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[n & 1][k], p1[n & 1], o[k], 0, 0, 0);
+        if constexpr (PP > 1) o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[n & 1][k], p2[PP > 1 ? n & 1 : 0], o[k], 0, 0, 0);
+        if constexpr (n < 3) {
+#pragma unroll
+          for (int x = 8 * k / VT; x < 8 * (k + 1) / VT; ++x) weigh(n + 1, x);
+        }
+        in_order();
+      });
+      l += !FOLD ? sum * ldexpf(1.0f, ue) : -base - up > 60.0f ? apart : sum * __builtin_amdgcn_exp2f(-base - up);
     }
     __syncthreads();
   }
@@ -435,23 +595,25 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 2) void kv_attention_rows(Att
   }
 }
 
-template <int DIM>
-void rows_dim(const AttnView& a, int32_t dtype, hipStream_t s) {
-  const dim3 grid((unsigned)(a.c.heads * a.units));
+template <int DIM, int WAVES>
+void rows_waves(const AttnView& a, int32_t dtype, hipStream_t s) {
+  const dim3 grid((unsigned)(a.c.heads * a.units)), block(64 * WAVES);
   if (dtype == KRONQ_F32)
-    hipLaunchKernelGGL((kv_attention_rows<DIM, float, 2, 2, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, float, 2, 2, false, WAVES>), grid, block, 0, s, a);
   else if (dtype == KRONQ_BF16)
-    hipLaunchKernelGGL((kv_attention_rows<DIM, bf16_t, 1, 1, true>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, bf16_t, 1, 1, true, WAVES>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((kv_attention_rows<DIM, _Float16, 2, 1, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, _Float16, 2, 1, false, WAVES>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
-kronq_status kv_rows_launch(const AttnView& a, int dim, int32_t dtype, hipStream_t s) {
-  if (dim == 64) rows_dim<64>(a, dtype, s);
-  else if (dim == 128) rows_dim<128>(a, dtype, s);
-  else rows_dim<256>(a, dtype, s);
+kronq_status kv_rows_launch(const AttnView& a, int dim, int32_t dtype, int waves, hipStream_t s) {
+  if (dim == 64 && waves == 8) rows_waves<64, 8>(a, dtype, s);
+  else if (dim == 64) rows_waves<64, 4>(a, dtype, s);
+  else if (dim == 128 && waves == 8) rows_waves<128, 8>(a, dtype, s);
+  else if (dim == 128) rows_waves<128, 4>(a, dtype, s);
+  else rows_waves<256, 4>(a, dtype, s);
   KQ_LAUNCHED("kv_attention_rows");
   return KRONQ_OK;
 }
