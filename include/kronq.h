@@ -495,7 +495,7 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
  *           in fp32 (s has 20 significant bits).
  *   A page's heads x page x dim/2 bytes (heads x page words) are contiguous;
  *   the distance between pages is *_stride (bytes for codes, words for grids),
- *   so the pages of several layers may share one buffer.
+ *   below 2^32, so the pages of several layers may share one buffer.
  * dim is 64, 128 or 256, page a power of two in 16..1024 (KRONQ_EUNSUPPORTED
  * otherwise).  Codes and grids are 16-byte aligned, their strides multiples of
  * 16 bytes.

@@ -176,9 +176,12 @@ static kronq_status kv_view(const char* fn, const kronq_kv_cache* c, const kronq
                 (int)b->columns, (int)c->page);
   int lgp = 0;
   while ((1 << lgp) < c->page) ++lgp;
-  *out = KvView{c->k_codes, c->v_codes, c->k_grid, c->v_grid, c->k_codes_stride, c->v_codes_stride,
-                c->k_grid_stride, c->v_grid_stride, b->table, b->ctx, b->cu, b->ld_table, (int)c->pages, lgp,
-                c->heads, b->seqs, b->columns, (int)rows};
+  const int64_t most = UINT32_MAX;
+  if (c->k_codes_stride > most || c->v_codes_stride > most || c->k_grid_stride > most || c->v_grid_stride > most)
+    return fail(KRONQ_EUNSUPPORTED, "%s: a page stride of 2^32 or more", fn);
+  *out = KvView{c->k_codes, c->v_codes, c->k_grid, c->v_grid, (uint32_t)c->k_codes_stride,
+                (uint32_t)c->v_codes_stride, (uint32_t)c->k_grid_stride, (uint32_t)c->v_grid_stride,
+                b->table, b->ctx, b->cu, b->ld_table, (int)c->pages, lgp, c->heads, b->seqs, b->columns, (int)rows};
   return KRONQ_OK;
 }
 

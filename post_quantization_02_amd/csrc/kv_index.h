@@ -13,8 +13,8 @@ namespace kronq {
 struct KvView {
   uint8_t *kc, *vc;        // codes
   uint32_t *kg, *vg;       // grids
-  int64_t kcs, vcs;        // bytes between pages
-  int64_t kgs, vgs;        // words between pages
+  uint32_t kcs, vcs;       // bytes between pages
+  uint32_t kgs, vgs;       // words between pages
   const int32_t *table, *ctx, *cu;
   int64_t ldt;
   int pages, lgp, heads;   // page = 1 << lgp
@@ -74,6 +74,10 @@ struct AttnShape { int share, window, sinks, least, most; };   // window 0: none
 struct Seq { int row0, len, ctx, tiles, qtiles; };
 
 __host__ __device__ inline int tiles_of(int n, int kt) { return n / kt + (n % kt != 0); }
+
+// Bytes (words) from the cache's start to a page: 32 x 32 bits, which is one
+// instruction.
+__host__ __device__ inline uint64_t page_offset(int page, uint32_t stride) { return (uint64_t)(uint32_t)page * stride; }
 
 // Positions that have a column.
 __host__ __device__ inline int64_t room_of(const KvView& c) { return (int64_t)c.columns << c.lgp; }

@@ -53,16 +53,16 @@ __device__ inline void load_tile(const KvView& c, const TilePages& p, int head, 
   const int in_page = (1 << c.lgp) - 1;
   const int64_t first = (int64_t)head << c.lgp;
   const int64_t slot = first + (key0 & in_page), slot2 = SMALL ? first : slot + 16;
-  auto pick = [&](bool up, const uint8_t* base, int64_t stride, int row) {
-    const uint8_t* lo = base + p.a.page * stride + slot * row;
-    const uint8_t* hi = base + p.b.page * stride + slot2 * row;
+  auto pick = [&](bool up, const uint8_t* base, uint32_t stride, int row) {
+    const uint8_t* lo = base + page_offset(p.a.page, stride) + slot * row;
+    const uint8_t* hi = base + page_offset(p.b.page, stride) + slot2 * row;
     return up ? hi : lo;
   };
   {
     const int row = 8 * ((i >> 2) & 1) + (i & 3), up = i >> 3;
     const uint8_t* k;
     if constexpr (SMALL) k = pick(up, c.kc, c.kcs, DIM / 2) + (row * (DIM / 2) + g * (DIM / 8));
-    else k = c.kc + p.a.page * c.kcs + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + g * (DIM / 8));
+    else k = c.kc + page_offset(p.a.page, c.kcs) + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + g * (DIM / 8));
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       if constexpr (DIM == 64) {
@@ -78,7 +78,7 @@ __device__ inline void load_tile(const KvView& c, const TilePages& p, int head, 
     const int row = 8 * (g & 1), up = g >> 1;
     const uint8_t* v;
     if constexpr (SMALL) v = pick(up, c.vc, c.vcs, DIM / 2) + (row * (DIM / 2) + i * (DIM / 32));
-    else v = c.vc + p.a.page * c.vcs + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + i * (DIM / 32));
+    else v = c.vc + page_offset(p.a.page, c.vcs) + slot * (DIM / 2) + (uint32_t)((16 * up + row) * (DIM / 2) + i * (DIM / 32));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (DIM == 64)
@@ -91,8 +91,8 @@ __device__ inline void load_tile(const KvView& c, const TilePages& p, int head, 
   }
   {
     const int up = (lane >> 4) & 1;
-    const uint32_t* kg = c.kg + (SMALL && up ? p.b.page * c.kgs + slot2 : p.a.page * c.kgs + slot + 16 * up);
-    const uint32_t* vg = c.vg + (SMALL && up ? p.b.page * c.vgs + slot2 : p.a.page * c.vgs + slot + 16 * up);
+    const uint32_t* kg = c.kg + (SMALL && up ? page_offset(p.b.page, c.kgs) + slot2 : page_offset(p.a.page, c.kgs) + slot + 16 * up);
+    const uint32_t* vg = c.vg + (SMALL && up ? page_offset(p.b.page, c.vgs) + slot2 : page_offset(p.a.page, c.vgs) + slot + 16 * up);
     t.word = (lane < 32 ? kg : vg)[lane & 15];
   }
 }
@@ -413,10 +413,9 @@ constexpr int kWholeTiles16 = 32;
 constexpr int kUnits16 = 704;
 // The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
 // have that many on average (a tile of keys is unpacked once for all of its rows).
-#ifndef KQ_TALL
-#define KQ_TALL 256
-#endif
-constexpr int kTallRows = KQ_TALL;
+// 2047 and 1774 rows x 4 behind 9001 and 4830 keys, dim 128: 616 us in tiles of 128
+// rows, 575 in tiles of 256.
+constexpr int kTallRows = 256;
 constexpr int kMinTilesRows = 4;         // 256 keys
 // Workgroups resident at once: two of four waves on a CU, or one of eight.  Row
 // tiles alone are enough at twice that; fewer are cut along the keys.

@@ -145,11 +145,11 @@ __global__ __launch_bounds__(NT) void kv_append(KvView c, HeadsView k, HeadsView
   if (!on) return;
   const int64_t slot = ((int64_t)head << c.lgp) + at.slot;
   if (keys) {
-    *reinterpret_cast<uint32_t*>(c.kc + (int64_t)at.page * c.kcs + slot * (LANES * 4) + d / 2) = codes;
-    if (d == 0) c.kg[(int64_t)at.page * c.kgs + slot] = word;
+    *reinterpret_cast<uint32_t*>(c.kc + page_offset(at.page, c.kcs) + slot * (LANES * 4) + d / 2) = codes;
+    if (d == 0) c.kg[page_offset(at.page, c.kgs) + slot] = word;
   } else {
-    *reinterpret_cast<uint32_t*>(c.vc + (int64_t)at.page * c.vcs + slot * (LANES * 4) + d / 2) = codes;
-    if (d == 0) c.vg[(int64_t)at.page * c.vgs + slot] = word;
+    *reinterpret_cast<uint32_t*>(c.vc + page_offset(at.page, c.vcs) + slot * (LANES * 4) + d / 2) = codes;
+    if (d == 0) c.vg[page_offset(at.page, c.vgs) + slot] = word;
   }
 }
 
@@ -173,8 +173,8 @@ __global__ __launch_bounds__(NT) void kv_read(KvView c, HeadsView k, HeadsView v
   uint32_t word = 0, w = 0;
   if (at.pos >= 0 && !at.bad) {
     const int64_t slot = ((int64_t)head << c.lgp) + at.slot;
-    word = keys ? c.kg[(int64_t)at.page * c.kgs + slot] : c.vg[(int64_t)at.page * c.vgs + slot];
-    const uint8_t* codes = keys ? c.kc + (int64_t)at.page * c.kcs : c.vc + (int64_t)at.page * c.vcs;
+    word = keys ? c.kg[page_offset(at.page, c.kgs) + slot] : c.vg[page_offset(at.page, c.vgs) + slot];
+    const uint8_t* codes = keys ? c.kc + page_offset(at.page, c.kcs) : c.vc + page_offset(at.page, c.vcs);
     w = *reinterpret_cast<const uint32_t*>(codes + slot * (LANES * 4) + d / 2);
     s = __uint_as_float(word & ~15u);
   }

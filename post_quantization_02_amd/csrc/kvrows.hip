@@ -3,9 +3,9 @@
 // head, waves of 32 rows that share each tile of 64 keys.
 //
 // The codes of a tile are unpacked once, into LDS, as fp16 codes minus zero
-// points, while the tile before is multiplied: keys as rows of dim values, by one
-// half of the waves, values transposed as rows of 64 keys, by the other.  Both
-// are read as whole 16-byte operands of the 32x32x16 products:
+// points, while the tile before is multiplied, by each wave some keys: keys as rows
+// of dim values, values transposed as rows of 64 keys.  Both are read as whole
+// 16-byte operands of the 32x32x16 products:
 //   S^T = K Q^T: lane (row, h) gets, of each 16 keys, the eight keys 8 h and up
 //     (the LDS rows of the keys are ordered for that),
 //   O^T = V^T P^T: which are its k slots, so weights stay in registers.
@@ -30,9 +30,6 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
-#ifndef KQ_AHEAD
-#define KQ_AHEAD 1
-#endif
 constexpr int KT = 64;
 
 // FOLD.  Scales of a pass are in 2^-kKeySpread (2^-kValueSpread) to 1 of the
@@ -43,51 +40,53 @@ constexpr int KT = 64;
 // the row's largest product.
 constexpr int kFoldSet = 10, kKeySpread = 20, kValueSpread = 8, kUp = 6;
 
-// How a tile goes to LDS.  Waves 0 .. WAVES / 2 - 1 take the keys, the others the
-// values: kParts threads a key, kWords words each, as both are loaded.  Values are
-// unpacked by eight keys a thread, of them kVals values each, after an exchange
-// within the wave.
+// How a tile goes to LDS.  Each wave takes kKeys keys: kParts lanes a key, kWords
+// words of it each, as codes are loaded.  Values are unpacked by eight keys a lane,
+// of them kVals values each, after an exchange within the wave.
 template <int DIM, int WAVES>
 struct Split {
-  static constexpr int kThreads = 32 * WAVES, kParts = kThreads / KT, kWords = DIM / 8 / kParts;
-  static constexpr int kCols = kThreads / 8, kVals = DIM / kCols;
+  static constexpr int kKeys = KT / WAVES, kParts = 64 / kKeys, kWords = DIM / 8 / kParts;
+  static constexpr int kCols = 64 / (kKeys / 8), kVals = DIM / kCols;
   // Where a piece (eight values of a key, or of eight keys a value) stands in its row
-  __device__ static constexpr int key_piece(int piece, int row) {
-    return piece ^ (row & 7) ^ (DIM == 64 ? 0 : kParts == 4 ? (piece / kWords >> 1) * 2 : piece / kWords * 4);
-  }
+  __device__ static constexpr int key_piece(int piece, int row) { return piece ^ (row & 7); }
   __device__ static constexpr int value_piece(int piece, int d) { return piece ^ ((d ^ (d >> 3)) & 7); }
 };
 
 template <int DIM, int WAVES>
 struct Raw {
-  uint32_t w[Split<DIM, WAVES>::kWords];
+  uint32_t k[Split<DIM, WAVES>::kWords], v[Split<DIM, WAVES>::kWords];
   uint32_t kw, vw;                        // grid words of key `lane`
   bool bad;                               // its page is out of range
 };
 
-// Asks for a tile's data.  `at` is the page of key `lane` or, WHOLE, of the tile.
-// (The same loads in all waves: two loads into one register from two branches
-// would be joined by moves, which wait for them.)
-template <int DIM, int WAVES>
-__device__ __forceinline__ void load_raw(const KvView& c, PageAt at, bool whole, int head, int key0, bool keys,
-                                         Raw<DIM, WAVES>& t) {
-  using S = Split<DIM, WAVES>;
-  const int lane = threadIdx.x & 63, id = threadIdx.x & (S::kThreads - 1), in_page = (1 << c.lgp) - 1;
-  const int64_t head0 = (int64_t)head << c.lgp;
-  const int key = id / S::kParts;
-  const int64_t page = whole ? at.page : __shfl(at.page, key);
-  const uint8_t* p = (keys ? c.kc : c.vc) + page * (keys ? c.kcs : c.vcs) +
-                     (head0 + ((key0 + key) & in_page)) * (DIM / 2) + id % S::kParts * (4 * S::kWords);
-  if constexpr (S::kWords == 2) {
-    *reinterpret_cast<u32x2*>(t.w) = *reinterpret_cast<const u32x2*>(p);
+// `n` words (a power of two) from memory that is aligned to them
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<u32x2*>(w) = *reinterpret_cast<const u32x2*>(p);
   } else {
 #pragma unroll
-    for (int w = 0; w < S::kWords; w += 4)
-      *reinterpret_cast<u32x4*>(t.w + w) = *reinterpret_cast<const u32x4*>(p + 4 * w);
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<u32x4*>(w + i) = *reinterpret_cast<const u32x4*>(p + 4 * i);
   }
+}
+
+// Asks for a tile's data.  `at` is the page of key `lane` or, WHOLE, of the tile.
+template <int DIM, int WAVES>
+__device__ __forceinline__ void load_raw(const KvView& c, PageAt at, bool whole, int head, int key0, int wave,
+                                         Raw<DIM, WAVES>& t) {
+  using S = Split<DIM, WAVES>;
+  const int lane = threadIdx.x & 63, in_page = (1 << c.lgp) - 1;
+  const int64_t head0 = (int64_t)head << c.lgp;
+  const int key = wave * S::kKeys + lane / S::kParts;
+  const int page = whole ? at.page : __shfl(at.page, key);
+  const int64_t part = (head0 + ((key0 + key) & in_page)) * (DIM / 2) + lane % S::kParts * (4 * S::kWords);
+  load_words(c.kc + page_offset(page, c.kcs) + part, t.k);
+  load_words(c.vc + page_offset(page, c.vcs) + part, t.v);
   const int64_t slot = head0 + ((key0 + lane) & in_page);
-  t.kw = c.kg[(int64_t)at.page * c.kgs + slot];
-  t.vw = c.vg[(int64_t)at.page * c.vgs + slot];
+  t.kw = c.kg[page_offset(at.page, c.kgs) + slot];
+  t.vw = c.vg[page_offset(at.page, c.vgs) + slot];
   t.bad = at.bad;                         // for later: what is loaded is not waited for here
 }
 
@@ -130,26 +129,29 @@ struct Tile {
   alignas(16) float vs[FOLD ? 4 : KT];
 };
 
-// Which keys of a tile's `left` the next pass takes (all of them unless FOLD), and
-// what unpacking wants to know of each: on `shelf`, 64 words of LDS of the wave's
-// own, its zero point, and for FOLD its scale times 2^-e as fp16 in the upper half
-// (0 for a key of another pass).  In `scales` (not FOLD) the scales themselves.
+// What unpacking wants to know of key `lane`: its zero points, and for FOLD its
+// scales times 2^-e as fp16 in the upper halves (0 for a key of another pass).
+struct KeyInfo { uint32_t k, v; };
+
+// Which keys of a tile's `left` the next pass takes: all of them unless FOLD.
 template <int DIM, int WAVES, bool FOLD>
-__device__ __forceinline__ Pass choose(const Raw<DIM, WAVES>& t, int key0, bool keys, uint32_t* shelf, float* scales,
-                                       uint64_t& left, Most& most) {
-  using S = Split<DIM, WAVES>;
-  const int lane = threadIdx.x & 63, id = threadIdx.x & (S::kThreads - 1);
+__device__ __forceinline__ Pass choose(const Raw<DIM, WAVES>& t, int key0, uint64_t& left, Most& most, KeyInfo& info) {
+  const int lane = threadIdx.x & 63;
   Pass pass{key0, 0, 0, left};
   uint32_t kw = t.bad ? 0x7FC00000u : t.kw, vw = t.bad ? 0x7FC00000u : t.vw;
+  info = {kw & 15, vw & 15};
   if constexpr (FOLD) {
     // a value scale that is not finite makes its key's scores not numbers, which
     // reaches the rows that see the key and no others
-    if ((vw & 0x7F800000u) == 0x7F800000u) kw = 0x7FC00000u, vw = 0;
-    if ((kw & 0x7F800000u) == 0x7F800000u) kw = 0x7FC00000u;
+    const bool odd = (vw & 0x7F800000u) == 0x7F800000u;
+    kw = odd || (kw & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : kw;
+    vw = odd ? 0 : vw;
     const int kx = exponent_of(kw), vx = exponent_of(vw);
-    auto fits = [](int x, int largest, int spread) { return x == 0 || (uint32_t)(largest - x) <= (uint32_t)spread; };
+    auto fits = [](int x, int largest, int spread) __attribute__((always_inline)) {
+      return (x == 0) | ((uint32_t)(largest - x) <= (uint32_t)spread);
+    };
     bool in = (left >> lane) & 1;
-    if (__ballot(in && !(fits(kx, most.k, kKeySpread) && fits(vx, most.v, kValueSpread)))) {
+    if (__ballot(in & !(fits(kx, most.k, kKeySpread) & fits(vx, most.v, kValueSpread)))) {
       most.k = wave_max(in ? kx : 0);
       in = in && fits(kx, most.k, kKeySpread);
       most.v = wave_max(in ? vx : 0);
@@ -158,12 +160,12 @@ __device__ __forceinline__ Pass choose(const Raw<DIM, WAVES>& t, int key0, bool 
     pass.keys = __ballot(in);
     pass.ke = most.k - 126 - kFoldSet;
     pass.ve = most.v - 126 - kFoldSet;
-    const uint32_t word = keys ? kw : vw;
-    const _Float16 s = in ? (_Float16)ldexpf(__uint_as_float(word & ~15u), -(keys ? pass.ke : pass.ve)) : (_Float16)0.0f;
-    shelf[lane] = (word & 15) | ((uint32_t)__builtin_bit_cast(uint16_t, s) << 16);
-  } else {
-    shelf[lane] = (keys ? kw : vw) & 15;
-    if (id < KT) scales[lane] = __uint_as_float((keys ? kw : vw) & ~15u);
+    auto half = [&](uint32_t word, int e) __attribute__((always_inline)) {
+      const _Float16 s = (_Float16)ldexpf(__uint_as_float(word & ~15u), -e);
+      return in ? (uint32_t)__builtin_bit_cast(uint16_t, s) << 16 : 0u;
+    };
+    info.k |= half(kw, pass.ke);
+    info.v |= half(vw, pass.ve);
   }
   left &= ~pass.keys;
   return pass;
@@ -185,72 +187,74 @@ __device__ __forceinline__ void each(F f) {
   each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// Unpacking one tile, cut into pieces to go between products.  KEYS: this wave
-// unpacks keys, a word a piece; else values, two of eight keys a piece.
-template <int DIM, int WAVES, bool FOLD, bool KEYS>
+// Unpacking a wave's keys of one tile, cut into pieces to go between products: a
+// word of a key each, then a pair of keys' kVals (at most four) values each.
+template <int DIM, int WAVES, bool FOLD>
 struct Unpacking {
   using S = Split<DIM, WAVES>;
-  static constexpr int kPieces = KEYS ? S::kWords : 4 * ((S::kVals + 3) / 4);
-  half2_t z1[KEYS ? 1 : 4], z2[KEYS ? 1 : 4], by[KEYS ? 1 : 4];
+  static constexpr int kRuns = (S::kVals + 3) / 4;    // of up to four values
+  static constexpr int kPieces = S::kWords + 4 * kRuns;
+  half2_t kz1, kz2, kby;
+  half2_t z1[4], z2[4], by[4];
   u32x4 v0, v1, v2, v3;                               // of four values, pairs of keys
-  uint32_t raw[KEYS ? 1 : S::kVals > 8 ? 16 : 8];     // of each key, this thread's values
+  uint32_t raw[8 * ((S::kVals + 7) / 8)];             // of each of eight keys, this lane's values
 
-  __device__ __forceinline__ void begin(uint32_t* __restrict__ shelf, const Raw<DIM, WAVES>& t) {
-    const int id = threadIdx.x & (S::kThreads - 1);
-    if constexpr (KEYS) {
-      const uint32_t c = shelf[id / S::kParts], z = c & 0xFFFF;
-      z1[0] = as_half2(zero1024_of(z));
-      z2[0] = as_half2(zero64_of(z));
-      by[0] = as_half2(__builtin_amdgcn_perm(c, c, 0x03020302u));
-    } else {
-      // the wave's keys, behind the shelf's first 64 words
-      uint8_t* mine = reinterpret_cast<uint8_t*>(shelf + 64);
-      const int lane = threadIdx.x & 63;
-      if constexpr (S::kWords == 2) {
-        *reinterpret_cast<u32x2_alias*>(mine + 8 * lane) = u32x2_alias{t.w[0], t.w[1]};
+  // `mine`: LDS of the wave's own, for its keys' values
+  __device__ __forceinline__ void begin(const KeyInfo& info, int wave, uint8_t* __restrict__ mine, const Raw<DIM, WAVES>& t) {
+    const int lane = threadIdx.x & 63, group = lane / S::kCols;
+#pragma unroll
+    for (int w = 0; w < S::kWords; w += S::kWords < 4 ? S::kWords : 4) {
+      uint8_t* p = mine + 4 * S::kWords * lane + 4 * w;
+      if constexpr (S::kWords == 1) *reinterpret_cast<u32_alias*>(p) = t.v[0];
+      else if constexpr (S::kWords == 2) *reinterpret_cast<u32x2_alias*>(p) = u32x2_alias{t.v[0], t.v[1]};
+      else *reinterpret_cast<u32x4_alias*>(p) = u32x4_alias{t.v[w], t.v[w + 1], t.v[w + 2], t.v[w + 3]};
+    }
+    const uint32_t c = __shfl(info.k, wave * S::kKeys + lane / S::kParts), z = c & 0xFFFF;
+    kz1 = as_half2(zero1024_of(z));
+    kz2 = as_half2(zero64_of(z));
+    kby = as_half2(__builtin_amdgcn_perm(c, c, 0x03020302u));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t a, b;
+      if constexpr (S::kCols == 64) {                 // the same eight keys for all lanes
+        a = __builtin_amdgcn_readlane(info.v, wave * S::kKeys + 2 * x);
+        b = __builtin_amdgcn_readlane(info.v, wave * S::kKeys + 2 * x + 1);
       } else {
-#pragma unroll
-        for (int w = 0; w < S::kWords; w += 4)
-          *reinterpret_cast<u32x4_alias*>(mine + 4 * S::kWords * lane + 4 * w) =
-              u32x4_alias{t.w[w], t.w[w + 1], t.w[w + 2], t.w[w + 3]};
+        a = __shfl(info.v, wave * S::kKeys + 8 * group + 2 * x);
+        b = __shfl(info.v, wave * S::kKeys + 8 * group + 2 * x + 1);
       }
-      __builtin_amdgcn_wave_barrier();
+      const uint32_t z = (a & 0xFFFF) | (b << 16);
+      z1[x] = as_half2(z | 0x64006400u);
+      z2[x] = as_half2((z << 4) | 0x54005400u);
+      by[x] = as_half2((a >> 16) | (b & 0xFFFF0000u));
+    }
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* p = mine + (lane / S::kCols * 8 + j) * (DIM / 2) + lane % S::kCols * (S::kVals / 2);
-        if constexpr (S::kVals == 2) raw[j] = *p;
-        else if constexpr (S::kVals == 4) raw[j] = *reinterpret_cast<const u16_alias*>(p);
-        else if constexpr (S::kVals == 8) raw[j] = *reinterpret_cast<const u32_alias*>(p);
-        else raw[2 * j] = reinterpret_cast<const u32_alias*>(p)[0], raw[2 * j + 1] = reinterpret_cast<const u32_alias*>(p)[1];
-      }
-      const u32x4_alias c0 = *reinterpret_cast<const u32x4_alias*>(shelf + 8 * (id / S::kCols));
-      const u32x4_alias c1 = *reinterpret_cast<const u32x4_alias*>(shelf + 8 * (id / S::kCols) + 4);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t a = x < 2 ? c0[2 * x] : c1[2 * x - 4], b = x < 2 ? c0[2 * x + 1] : c1[2 * x - 3];
-        const uint32_t z = __builtin_amdgcn_perm(b, a, 0x0C040C00u);
-        z1[x] = as_half2(z | 0x64006400u);
-        z2[x] = as_half2((z << 4) | 0x54005400u);
-        by[x] = as_half2(__builtin_amdgcn_perm(b, a, 0x07060302u));
-      }
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* p = mine + (8 * group + j) * (DIM / 2) + lane % S::kCols * S::kVals / 2;
+      if constexpr (S::kVals == 1) raw[j] = lane & 1 ? *p >> 4 : *p;
+      else if constexpr (S::kVals == 2) raw[j] = *p;
+      else if constexpr (S::kVals == 4) raw[j] = *reinterpret_cast<const u16_alias*>(p);
+      else if constexpr (S::kVals == 8) raw[j] = *reinterpret_cast<const u32_alias*>(p);
+      else raw[2 * j] = reinterpret_cast<const u32_alias*>(p)[0], raw[2 * j + 1] = reinterpret_cast<const u32_alias*>(p)[1];
     }
   }
 
   template <int W>
-  __device__ __forceinline__ void piece(const Unpacker& un, const Raw<DIM, WAVES>& t,
+  __device__ __forceinline__ void piece(int wave, const Unpacker& un, const Raw<DIM, WAVES>& t,
                                         Tile<DIM, FOLD>* __restrict__ out) {
-    const int id = threadIdx.x & (S::kThreads - 1);
-    if constexpr (KEYS) {
-      const int key = id / S::kParts, part = id % S::kParts;
+    const int lane = threadIdx.x & 63;
+    if constexpr (W < S::kWords) {
+      const int key = wave * S::kKeys + lane / S::kParts, part = lane % S::kParts;
       // bits 2 and 3 exchanged: see the scores' layout
       const int row = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
-      half8_t x = un.word(t.w[W], z1[0], z2[0]);
-      if constexpr (FOLD) x *= __builtin_shufflevector(by[0], by[0], 0, 1, 0, 1, 0, 1, 0, 1);
+      half8_t x = un.word(t.k[W], kz1, kz2);
+      if constexpr (FOLD) x *= __builtin_shufflevector(kby, kby, 0, 1, 0, 1, 0, 1, 0, 1);
       *reinterpret_cast<half8_t*>(&out->k[row][8 * S::key_piece(part * S::kWords + W, row)]) = x;
     } else {
       // keys 2 x and 2 x + 1, values 4 n and up
-      constexpr int n = W / 4, x = W % 4;
-      const int kg = id / S::kCols, col = id % S::kCols;
+      constexpr int n = (W - S::kWords) / 4, x = (W - S::kWords) % 4;
+      const int kg = wave * (S::kKeys / 8) + lane / S::kCols, col = lane % S::kCols;
       const uint32_t wa = S::kVals > 8 ? raw[4 * x + (n >> 1)] : raw[2 * x];
       const uint32_t wb = S::kVals > 8 ? raw[4 * x + 2 + (n >> 1)] : raw[2 * x + 1];
       const uint32_t p = __builtin_amdgcn_perm(wb, wa, n & 1 ? 0x07060302u : 0x05040100u);
@@ -259,7 +263,7 @@ struct Unpacking {
         return __builtin_bit_cast(uint32_t, pair);
       };
       v0[x] = put(un.low_pair(p, z1[x]));
-      v1[x] = put(un.high_pair(p, z2[x]));
+      if constexpr (S::kVals > 1) v1[x] = put(un.high_pair(p, z2[x]));
       if constexpr (S::kVals > 2) {
         v2[x] = put(un.low_pair(p >> 8, z1[x]));
         v3[x] = put(un.high_pair(p >> 8, z2[x]));
@@ -270,7 +274,7 @@ struct Unpacking {
           *reinterpret_cast<half8_t*>(&out->v[d + y][8 * S::value_piece(kg, d + y)]) = __builtin_bit_cast(half8_t, v);
         };
         store(0, v0);
-        store(1, v1);
+        if constexpr (S::kVals > 1) store(1, v1);
         if constexpr (S::kVals > 2) {
           store(2, v2);
           store(3, v3);
@@ -281,15 +285,16 @@ struct Unpacking {
 };
 
 // One stage: the scores of the tile `cur`, and the next tile's codes into `out`.
-// Operands are read two steps ahead.
-template <int DIM, int WAVES, bool FOLD, int QP, bool QLDS, bool KEYS>
+// Operands are read a step ahead (further ahead there are no registers).
+template <int DIM, int WAVES, bool FOLD, int QP, bool QLDS>
 __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restrict__ cur, Tile<DIM, FOLD>* __restrict__ out,
                                                   const Unpacker& un, const Raw<DIM, WAVES>& t,
-                                                  uint32_t* __restrict__ shelf, const half8_t (&q1)[DIM / 16],
+                                                  const KeyInfo& info, int wave, uint8_t* __restrict__ mine,
+                                                  const half8_t (&q1)[DIM / 16],
                                                   const half8_t (&q2)[QP > 1 ? DIM / 16 : 1],
                                                   const half8_t (*__restrict__ lds_q)[64], f32x16 (&sc)[2]) {
   using S = Split<DIM, WAVES>;
-  constexpr int KS = DIM / 16, AHEAD = KQ_AHEAD, RING = AHEAD + 1;
+  constexpr int KS = DIM / 16, AHEAD = 1, RING = AHEAD + 1;
   const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
   half8_t kv[RING][2], second[QLDS ? RING : 1];
   auto read = [&](int k) __attribute__((always_inline)) {
@@ -300,8 +305,8 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
   };
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k) read(k);
-  Unpacking<DIM, WAVES, FOLD, KEYS> work;
-  work.begin(shelf, t);
+  Unpacking<DIM, WAVES, FOLD> work;
+  work.begin(info, wave, mine, t);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -309,14 +314,14 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
   in_order();
   // half step `at`: a product (or two) and its share of the pieces
   each<2 * KS>([&](auto at) __attribute__((always_inline)) {
-    constexpr int k = at / 2, s = at % 2, N = Unpacking<DIM, WAVES, FOLD, KEYS>::kPieces;
+    constexpr int k = at / 2, s = at % 2, N = Unpacking<DIM, WAVES, FOLD>::kPieces;
     if constexpr (s == 0 && k + AHEAD < KS) read(k + AHEAD);
     sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], q1[k], sc[s], 0, 0, 0);
     if constexpr (QP > 1)
       sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], QLDS ? second[QLDS ? k % RING : 0] : q2[QP > 1 ? k : 0],
                                                      sc[s], 0, 0, 0);
     each<N>([&](auto w) __attribute__((always_inline)) {
-      if constexpr (w * 2 * KS / N == at) work.template piece<w>(un, t, out);
+      if constexpr (w * 2 * KS / N == at) work.template piece<w>(wave, un, t, out);
     });
     in_order();
   });
@@ -332,7 +337,7 @@ void kv_attention_rows(AttnView a) {
   constexpr bool QLDS = QP > 1 && DIM == 128 && WAVES == 8;   // queries' second parts: no registers left
   __shared__ Tile<DIM, FOLD> lds[2];
   __shared__ half8_t lds_q[QLDS ? WAVES : 1][QLDS ? KS : 1][64];
-  __shared__ __align__(16) uint32_t shelves[WAVES][64 + 64 * S::kWords];
+  __shared__ __align__(16) uint8_t packed[WAVES][256 * S::kWords];
   Unit u;
   // key heads are the faster index, so that workgroups on one XCD read few heads;
   // later row tiles see more keys: they come first
@@ -340,7 +345,6 @@ void kv_attention_rows(AttnView a) {
   if (!find_unit<BM, KT>(a, unit, false, u)) return;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool keys = wave < WAVES / 2;
   int pos_lo, pos_hi;
   const Span span = span_of(a.c, a.shape, u, BM, KT, pos_lo, pos_hi);
   int v0, v1;
@@ -389,32 +393,34 @@ void kv_attention_rows(AttnView a) {
     next = page_entry(a.c, table, page_key(v0 + 1));
     left = unseen();
   }
-  // a pass's choice; its tile's data are gone from the registers after the stage that
-  // unpacks it, and the next tile's are asked for
-  auto take = [&](int buf) __attribute__((always_inline)) {
-    return choose<DIM, WAVES, FOLD>(raw, tile_key(at), keys, shelves[wave], keys ? lds[buf].ks : lds[buf].vs, left, most);
-  };
+  KeyInfo info{};
   f32x16 sc[2];
-  auto stage = [&](int buf) __attribute__((always_inline)) {
-    __builtin_amdgcn_wave_barrier();                  // the shelf is the wave's own
-    if (keys)
-      scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS, true>(&lds[buf], &lds[buf ^ 1], un, raw, shelves[wave], q1, q2,
-                                                          lds_q[QLDS ? wave : 0], sc);
-    else
-      scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS, false>(&lds[buf], &lds[buf ^ 1], un, raw, shelves[wave], q1, q2,
-                                                           lds_q[QLDS ? wave : 0], sc);
+  // chooses the next pass, for the buffer `to`
+  auto take = [&](int to) __attribute__((always_inline)) {
+    if constexpr (!FOLD)
+      if (wave == 0) {
+        lds[to].ks[lane] = raw.bad ? kNan : __uint_as_float(raw.kw & ~15u);
+        lds[to].vs[lane] = raw.bad ? kNan : __uint_as_float(raw.vw & ~15u);
+      }
+    return choose<DIM, WAVES, FOLD>(raw, tile_key(at), left, most, info);
+  };
+  // the scores of the buffer `from` and the chosen pass into the other; when a tile
+  // has gone there the next one's data are asked for
+  auto stage = [&](int from) __attribute__((always_inline)) {
+    scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS>(&lds[from], &lds[from ^ 1], un, raw, info, wave, packed[wave], q1, q2,
+                                                  lds_q[QLDS ? wave : 0], sc);
     if (!left) {
       ++at;
       here = page_from(a.c, next, page_key(at));
       left = unseen();
     }
-    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), keys, raw);
+    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), wave, raw);
     next = page_entry(a.c, table, page_key(at + 1));
   };
   Pass cur{};
   bool more = v0 < v1;
   if (more) {
-    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), keys, raw);
+    load_raw<DIM, WAVES>(a.c, here, whole, head, tile_key(at), wave, raw);
     cur = take(0);
     stage(1);                                         // no scores yet
   }
