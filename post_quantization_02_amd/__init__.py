@@ -9,7 +9,9 @@ it raises, there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -812,7 +814,7 @@ class Rope:
 
 
 def _heads3(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype, device) -> _Heads:
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise ValueError("%s must be %s on %s" % (name, dtype, device))
     if t.shape != (rows, heads, dim):
         raise ValueError("%s must have shape (%d, %d, %d)" % (name, rows, heads, dim))
@@ -823,47 +825,53 @@ def _heads3(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype, 
     return _Heads(t.data_ptr(), sr if rows > 1 else heads * dim, sh if heads > 1 else dim)
 
 
-class _OnStream:
-    """The device of the call's tensors is current, and torch allocates for the
-    stream that the call runs on."""
+def _new_heads3(shape, dtype, device):
+    """A new tensor (rows, heads, dim) and its description."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
 
-    def __init__(self, device, stream):
-        cur = torch.cuda.current_stream(device)
-        self.handle = cur.cuda_stream if stream is None else _stream(stream)
-        self.ctx = None
-        if self.handle != cur.cuda_stream:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(self.handle, device=device)
-            self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
+_AS_IT_IS = contextlib.nullcontext()
 
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
+
+def _on_stream(device, stream):
+    """(handle of the stream to run on, a context in which the device is current
+    and torch allocates for that stream)."""
+    # the current stream's handle without an object for it: calls for one token
+    # cost as much as their parts in Python do
+    cur = torch._C._cuda_getCurrentRawStream(device.index)
+    handle = cur if stream is None else _stream(stream)
+    if handle != cur:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(handle, device=device)
+        return handle, torch.cuda.stream(stream)
+    return handle, _AS_IT_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_attention_ws(rows: int, seqs: int, q_heads: int, heads: int, dim: int) -> int:
+    return load().kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim)
 
 
 def _kv_check(dtype, cache: KVCache, batch: KVBatch, rope: Rope | None):
     if dtype not in _KV_DTYPES:
         raise ValueError("dtype must be float32, bfloat16 or float16")
-    _same_device(cache.device, batch, *(() if rope is None else (rope,)))
+    if batch.device != cache.device or (rope is not None and rope.device != cache.device):
+        _same_device(cache.device, batch, *(() if rope is None else (rope,)))
 
 
 def kronq_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch,
                     rope: Rope | None = None, stream=None) -> None:
     """k and v (rows, heads, dim) join the cache at the batch's positions, the
     keys rotated first when `rope` is given."""
-    _kv_check(k.dtype, cache, batch, rope)
+    dtype = k.dtype
+    _kv_check(dtype, cache, batch, rope)
     rows = k.shape[0]
-    kh = _heads3(k, "k", rows, cache.heads, cache.dim, k.dtype, cache.device)
-    vh = _heads3(v, "v", rows, cache.heads, cache.dim, k.dtype, cache.device)
-    with _OnStream(cache.device, stream) as st:
-        _check(load().kronq_kv_append(kh, vh, _KV_DTYPES[k.dtype], rows, cache._c, batch._c,
+    kh = _heads3(k, "k", rows, cache.heads, cache.dim, dtype, cache.device)
+    vh = _heads3(v, "v", rows, cache.heads, cache.dim, dtype, cache.device)
+    st, here = _on_stream(cache.device, stream)
+    with here:
+        _check(load().kronq_kv_append(kh, vh, _KV_DTYPES[dtype], rows, cache._c, batch._c,
                                       None if rope is None else rope._c, st), "kronq_kv_append")
 
 
@@ -874,13 +882,14 @@ def kronq_kv_read(cache: KVCache, batch: KVBatch, rows: int, dtype=torch.float32
     (undefined when k or v is allocated here)."""
     _kv_check(dtype, cache, batch, None)
     shape = (rows, cache.heads, cache.dim)
-    with _OnStream(cache.device, stream) as st:
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=cache.device)
-        if v is None:
-            v = torch.empty(shape, dtype=dtype, device=cache.device)
-        kh = _heads3(k, "k", *shape, dtype, cache.device)
-        vh = _heads3(v, "v", *shape, dtype, cache.device)
+    kh = None if k is None else _heads3(k, "k", *shape, dtype, cache.device)
+    vh = None if v is None else _heads3(v, "v", *shape, dtype, cache.device)
+    st, here = _on_stream(cache.device, stream)
+    with here:
+        if kh is None:
+            k, kh = _new_heads3(shape, dtype, cache.device)
+        if vh is None:
+            v, vh = _new_heads3(shape, dtype, cache.device)
         _check(load().kronq_kv_read(kh, vh, _KV_DTYPES[dtype], rows, cache._c, batch._c, st), "kronq_kv_read")
     return k, v
 
@@ -891,28 +900,33 @@ def kronq_kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: f
                        lse: torch.Tensor | None = None, stream=None, ws: torch.Tensor | None = None):
     """Causal attention of q (rows, q_heads, dim) over the cache: out in q's
     dtype, or (out, lse) when lse is asked for.  Rows of no sequence are left as
-    they were (undefined when out is allocated here)."""
-    _kv_check(q.dtype, cache, batch, rope)
+    they were (undefined when out is allocated here).  `ws`: device memory of at
+    least the bytes that the call needs, not shared by calls that may run at the
+    same time (one that is too small is replaced)."""
+    dtype, device = q.dtype, cache.device
+    _kv_check(dtype, cache, batch, rope)
     if q.dim() != 3:
         raise ValueError("q must be (rows, q_heads, dim)")
     rows, qheads, _ = q.shape
     shape = (rows, qheads, cache.dim)
-    qh = _heads3(q, "q", *shape, q.dtype, cache.device)
-    lib = load()
-    with _OnStream(cache.device, stream) as st:
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=cache.device)
-        oh = _heads3(out, "out", *shape, q.dtype, cache.device)
+    qh = _heads3(q, "q", *shape, dtype, device)
+    oh = None if out is None else _heads3(out, "out", *shape, dtype, device)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, qheads) or
+                            not lse.is_contiguous() or lse.device != device):
+        raise ValueError("lse must be a contiguous float32 (rows, q_heads) tensor on %s" % device)
+    need = _kv_attention_ws(rows, batch.seqs, qheads, cache.heads, cache.dim)
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device):
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
+    st, here = _on_stream(device, stream)
+    with here:
+        if oh is None:
+            out, oh = _new_heads3(shape, dtype, device)
         if lse is None and want_lse:
-            lse = torch.empty((rows, qheads), dtype=torch.float32, device=cache.device)
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, qheads) or
-                                not lse.is_contiguous() or lse.device != cache.device):
-            raise ValueError("lse must be a contiguous float32 (rows, q_heads) tensor on %s" % cache.device)
-        need = lib.kronq_kv_attention_ws(rows, batch.seqs, qheads, cache.heads, cache.dim)
+            lse = torch.empty((rows, qheads), dtype=torch.float32, device=device)
         if ws is None or ws.numel() < need:
-            ws = _ws(need, cache.device)
-        _check(lib.kronq_kv_attention(qh, _KV_DTYPES[q.dtype], rows, qheads, cache._c, batch._c,
-                                      None if rope is None else rope._c,
-                                      cache.dim ** -0.5 if scale is None else scale, window, sinks, oh,
-                                      _ptr(lse), _ptr(ws), need, st), "kronq_kv_attention")
+            ws = _ws(need, device)
+        _check(load().kronq_kv_attention(qh, _KV_DTYPES[dtype], rows, qheads, cache._c, batch._c,
+                                         None if rope is None else rope._c,
+                                         cache.dim ** -0.5 if scale is None else scale, window, sinks, oh,
+                                         _ptr(lse), _ptr(ws), need, st), "kronq_kv_attention")
     return out if lse is None else (out, lse)
