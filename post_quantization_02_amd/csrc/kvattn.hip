@@ -336,14 +336,15 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
   }
 }
 
-// Joins the chunks of one row's head, in the order of the chunks.  blockIdx.x:
-// a row; or, where few rows of each sequence are this kernel's (per > 0), a
-// sequence's row, per for each.
+// Joins the chunks of a row's heads, in the order of the chunks.  blockIdx.x: a
+// row; or, where few rows of each sequence are this kernel's (per > 0), a
+// sequence's row, per for each.  A head is joined by `slots` groups of lanes (a
+// power of two), each of which adds up every slots-th chunk.
 template <int DIM, int BM, int KT, typename T>
-__global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per) {
-  constexpr int LANES = DIM / 8, SLOTS = 256 / LANES;
-  __shared__ float lds_x[SLOTS][DIM + 4];
-  __shared__ float lds_l[SLOTS];
+__global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, int slots) {
+  constexpr int LANES = DIM / 8, GROUPS = 256 / LANES;
+  __shared__ float lds_x[GROUPS][DIM + 4];
+  __shared__ float lds_l[GROUPS];
   Unit u;
   const int share = a.shape.share;
   int row = blockIdx.x;
@@ -352,46 +353,50 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per) {
     if ((int)blockIdx.x % per >= s.len) return;
     row = s.row0 + blockIdx.x % per;
   }
-  const int qh = blockIdx.y, head = qh / share;
   if (!find_unit<BM, KT>(a, row, true, u) || u.chunks == 1) return;
-  const int r = (row - u.row0) * share + qh % share;
-  const int tid = threadIdx.x, slot = tid / LANES, d = (tid % LANES) * 8;
+  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, d = lane * 8;
+  const int slot = group & (slots - 1), qh = (int)blockIdx.y * (GROUPS / slots) + group / slots;
+  const bool in = qh < a.qheads;
+  const int head = qh / share, r = (row - u.row0) * share + qh % share;
   auto at = [&](int chunk) {
     return ((int64_t)(u.base + r / BM * u.chunks + chunk) * a.c.heads + head) * BM + r % BM;
   };
+  const int width = min(slots * LANES, 64);          // lanes of a wave that share the head
   float m = -INFINITY;
-  for (int c = tid & 63; c < u.chunks; c += 64) m = fmaxf(m, a.stat[2 * at(c)]);
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) m = fmaxf(m, __shfl_xor(m, s));
+  if (in)
+    for (int c = threadIdx.x & (width - 1); c < u.chunks; c += width) m = fmaxf(m, a.stat[2 * at(c)]);
+  for (int s = 1; s < width; s <<= 1) m = fmaxf(m, __shfl_xor(m, s));
   float l = 0, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (in) {
 #pragma unroll 4
-  for (int c = slot; c < u.chunks; c += SLOTS) {
-    float y[8];
-    load8(a.part + at(c) * DIM + d, y);
-    const float mc = a.stat[2 * at(c)], by = mc == -INFINITY ? 0.0f : exp2f(mc - m);
-    l += a.stat[2 * at(c) + 1] * by;
+    for (int c = slot; c < u.chunks; c += slots) {
+      float y[8];
+      load8(a.part + at(c) * DIM + d, y);
+      const float mc = a.stat[2 * at(c)], by = mc == -INFINITY ? 0.0f : exp2f(mc - m);
+      l += a.stat[2 * at(c) + 1] * by;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] += y[k] * by;
+      for (int k = 0; k < 8; ++k) x[k] += y[k] * by;
+    }
   }
-  store8(&lds_x[slot][d], x);
-  if (d == 0) lds_l[slot] = l;
-  __syncthreads();
-  if (slot) return;
-  l = 0;
+  if (slots > 1) {
+    store8(&lds_x[group][d], x);
+    if (lane == 0) lds_l[group] = l;
+    __syncthreads();
+    if (slot) return;
+    for (int s = 1; s < min(slots, u.chunks); ++s) {
+      float y[8];
+      load8(&lds_x[group + s][d], y);
+      l += lds_l[group + s];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = 0;
-  for (int s = 0; s < SLOTS; ++s) {
-    float y[8];
-    load8(&lds_x[s][d], y);
-    l += lds_l[s];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] += y[k];
+      for (int k = 0; k < 8; ++k) x[k] += y[k];
+    }
   }
+  if (!in) return;
   const float inv = l == 0 ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int k = 0; k < 8; ++k) x[k] = l == 0 ? 0.0f : x[k] * inv;
   store8(static_cast<T*>(a.out.data) + (int64_t)row * a.out.row + (int64_t)qh * a.out.head + d, x);
-  if (a.lse && d == 0) a.lse[(int64_t)row * a.qheads + qh] = l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (a.lse && lane == 0) a.lse[(int64_t)row * a.qheads + qh] = l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- launch
@@ -420,6 +425,10 @@ constexpr int kMinTilesRows = 4;         // 256 keys
 // Workgroups resident at once: two of four waves on a CU, or one of eight.  Row
 // tiles alone are enough at twice that; fewer are cut along the keys.
 constexpr int kResident = 512, kResidentTall = 256;
+
+// The join gives each row's head as many groups of lanes as make this many
+// workgroups.
+constexpr int64_t kJoinGroups = 512;
 
 // How a call is cut: units of each kernel (0: not launched; a bound of its row
 // tiles, and chunks on top), and whether there can be chunks to join.
@@ -458,8 +467,13 @@ kronq_status join(const AttnView& a, int64_t per, hipStream_t s) {
   if (room_of(a.c) <= (int64_t)a.min_tiles * KT) return KRONQ_OK;
   const bool by_seq = per > 0 && per * a.c.seqs < a.c.rows;
   const int64_t grid = by_seq ? per * a.c.seqs : a.c.rows;
-  hipLaunchKernelGGL((kv_attention_join<DIM, BM, KT, T>), dim3((unsigned)grid, (unsigned)a.qheads), dim3(256), 0, s, a,
-                     by_seq ? (int)per : 0);
+  constexpr int groups = 256 / (DIM / 8);
+  int slots = 1;
+  while (slots < groups && grid * a.qheads * slots / groups < kJoinGroups) slots *= 2;
+  const int at_once = groups / slots;
+  hipLaunchKernelGGL((kv_attention_join<DIM, BM, KT, T>),
+                     dim3((unsigned)grid, (unsigned)((a.qheads + at_once - 1) / at_once)), dim3(256), 0, s, a,
+                     by_seq ? (int)per : 0, slots);
   KQ_LAUNCHED("kv_attention_join");
   return KRONQ_OK;
 }
