@@ -88,4 +88,18 @@ __device__ inline void store4(_Float16* p, const float* x) {
   *reinterpret_cast<half4*>(p) = half4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
 }
 
+// The value of another lane of a group of eight or sixteen: its partner in step
+// `CTRL` of a reduction (DPP: exchanged pairs, halves of four, of eight, of sixteen lanes).
+template <int CTRL>
+__device__ inline float partner(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ inline double partner(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 }  // namespace kronq

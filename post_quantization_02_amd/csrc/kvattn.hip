@@ -97,6 +97,91 @@ __device__ inline void load_tile(const KvView& c, const TilePages& p, int head, 
   }
 }
 
+// A tile's queries, made ready by all threads: a thread has eight values of a row
+// (two such where dim is 256), asked for before the first keys, and leaves them as
+// the products' operands in LDS.  What load_query does for a wave by itself.
+template <typename T, int DIM>
+struct QueryPiece {
+  static constexpr int kLanes = DIM / 8, kPieces = (16 * kLanes + 255) / 256;
+  float x[kPieces][8], o[kPieces][8], c[kPieces][8], s[kPieces][8];
+  bool turn[kPieces], fine[kPieces], second[kPieces];
+
+  __device__ __forceinline__ void ask(const AttnView& a, const Unit& u, int head) {
+    const RopeView& rope = a.rope;
+    const int share = a.shape.share;
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      const int row = ((int)threadIdx.x / kLanes + n * (256 / kLanes)) & 15, d = (int)threadIdx.x % kLanes * 8;
+      const int r = u.qtile * 16 + row, tok = min(r / share, u.len - 1), pos = u.ctx - u.len + tok;
+      const T* p = static_cast<const T*>(a.q.data) + (int64_t)(u.row0 + tok) * a.q.row +
+                   (int64_t)(head * share + r % share) * a.q.head + d;
+      fine[n] = !rope.half || pos < rope.positions;
+      turn[n] = fine[n] && pos >= 0 && d < 2 * rope.half;   // before the sequence's start: sees nothing
+      second[n] = !rope.neighbours && d >= rope.half;
+      // every load happens, for branches would wait for theirs: what is not rotated
+      // loads its own values in the angles' place
+      const int other = !turn[n] || rope.neighbours ? 0 : second[n] ? -rope.half : rope.half;
+      const int j = rope.neighbours ? d / 2 : second[n] ? d - rope.half : d;
+      const float* ct = turn[n] ? rope.cos + (int64_t)pos * rope.ld + j : reinterpret_cast<const float*>(p);
+      const float* st = turn[n] ? rope.sin + (int64_t)pos * rope.ld + j : reinterpret_cast<const float*>(p);
+      const int more = turn[n] && !rope.neighbours ? 4 : 0;
+      load8(p, x[n]);
+      load8(p + other, o[n]);
+      const f32x4 c0 = *reinterpret_cast<const f32x4*>(ct), c1 = *reinterpret_cast<const f32x4*>(ct + more);
+      const f32x4 s0 = *reinterpret_cast<const f32x4*>(st), s1 = *reinterpret_cast<const f32x4*>(st + more);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[n][k] = c0[k], c[n][4 + k] = c1[k], s[n][k] = s0[k], s[n][4 + k] = s1[k];
+    }
+  }
+
+  template <int PARTS>
+  __device__ __forceinline__ void put(const AttnView& a, const Unit& u, half8_t (*__restrict__ q)[DIM / 32][64],
+                                      float* __restrict__ f) {
+    const int share = a.shape.share;
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      if (kLanes == 8 && threadIdx.x >= 128) break;         // 16 rows of eight threads
+      const int row = (int)threadIdx.x / kLanes + n * (256 / kLanes), d8 = (int)threadIdx.x % kLanes;
+      float y[8], big = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float cc = a.rope.neighbours ? c[n][k / 2] : c[n][k], ss = a.rope.neighbours ? s[n][k / 2] : s[n][k];
+        const float z = a.rope.neighbours ? x[n][k ^ 1] : o[n][k];
+        const bool minus = a.rope.neighbours ? !(k & 1) : !second[n];
+        const float by = minus ? -ss : ss;
+        y[k] = turn[n] ? x[n][k] * cc + z * by : x[n][k];
+        big = fmaxf(big, y[k] - y[k] == 0 ? fabsf(y[k]) : INFINITY);
+      }
+      if (!fine[n]) big = INFINITY;
+      big = fmaxf(big, partner<0xB1>(big));
+      big = fmaxf(big, partner<0x4E>(big));
+      big = fmaxf(big, partner<0x141>(big));
+      if constexpr (kLanes > 8) big = fmaxf(big, partner<0x140>(big));
+      if constexpr (kLanes > 16) big = fmaxf(big, __shfl_xor(big, 16));
+      const bool bad = big == INFINITY;
+      int e2 = 0;
+      if (!bad && big > 0) {
+        frexpf(big, &e2);                                   // big < 2^e2
+        e2 = 11 - e2;
+      }
+      half8_t q1, q2;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float z = bad ? 0.0f : ldexpf(y[kOrder[k]], e2);
+        q1[k] = (_Float16)z;
+        if constexpr (PARTS > 1) q2[k] = (_Float16)(z - (float)q1[k]);
+      }
+      const int lane = row + 16 * (d8 / (DIM / 32)), k = d8 % (DIM / 32);
+      q[0][k][lane] = q1;
+      if constexpr (PARTS > 1) q[PARTS - 1][k][lane] = q2;
+      if (d8 == 0) {
+        const int tok = min((u.qtile * 16 + row) / share, u.len - 1);
+        f[row] = bad && u.ctx - u.len + tok >= 0 ? kNan : fmaxf(ldexpf(a.scale * kLog2e, -e2), 0x1p-126f);
+      }
+    }
+  }
+};
+
 template <int DIM, typename T, int PARTS, bool SMALL>
 __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnView a) {
   constexpr int BM = 16, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
@@ -107,6 +192,8 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
   __shared__ __align__(16) float lds_s[4][64];
   __shared__ __align__(16) uint32_t lds_kz[4][32][2];
   __shared__ __align__(16) uint16_t lds_vz[4][2][32];
+  __shared__ half8_t lds_q[PARTS][KS][64];
+  __shared__ float lds_f[BM];
   Unit u;
   if (!find_unit<BM, KT>(a, blockIdx.x, false, u)) return;
   const int head = blockIdx.y;
@@ -129,14 +216,27 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
   if (w0 < v1) {
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) at[n] = tile_pages<SMALL>(a.c, table, tile_key(w0 + 4 * n));
+  }
+  QueryPiece<T, DIM> piece;
+  piece.ask(a, u, head);
+  __builtin_amdgcn_sched_barrier(0);
+  if (w0 < v1) {
 #pragma unroll
     for (int n = 0; n < AHEAD - 1; ++n) load_tile<DIM, SMALL>(a.c, at[n], head, tile_key(w0 + 4 * n), raw[n]);
   }
+  __builtin_amdgcn_sched_barrier(0);
 
   // this lane's query row
   const int r = u.qtile * BM + i, pos = u.ctx - u.len + min(r / share, u.len - 1);
   half8_t q1[KS], q2[PARTS > 1 ? KS : 1];
-  const float f = load_query<T, PARTS, KS, 4>(a, u, head, r, g * (DIM / 4), 8, q1, q2);
+  piece.template put<PARTS>(a, u, lds_q, lds_f);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    q1[k] = lds_q[0][k][lane];
+    if constexpr (PARTS > 1) q2[k] = lds_q[PARTS - 1][k][lane];
+  }
+  const float f = lds_f[i];
 
   const Unpacker un;
   f32x4 o[VT];

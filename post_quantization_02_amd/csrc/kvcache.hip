@@ -25,20 +25,6 @@ __device__ inline const int32_t* stage_cu(const KvView& c, int32_t* lds) {
   return lds;
 }
 
-// The value of another lane of the group: its partner in step `CTRL` of a
-// reduction (DPP: exchanged pairs, halves of four, of eight, of sixteen lanes).
-template <int CTRL>
-__device__ inline float partner(float x) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
-}
-template <int CTRL>
-__device__ inline double partner(double x) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, true);
-  const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, true);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
 template <typename V>
 __device__ inline V least(V a, V b) { return __builtin_elementwise_min(a, b); }
 template <typename V>
