@@ -458,6 +458,8 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, in
   const int slot = group & (slots - 1), qh = (int)blockIdx.y * (GROUPS / slots) + group / slots;
   const bool in = qh < a.qheads;
   const int head = qh / share, r = (row - u.row0) * share + qh % share;
+  // cannot be in a batch whose rows are each one sequence's
+  if (u.base < 0 || u.base + ((int64_t)u.len * share - 1) / BM * u.chunks + u.chunks > a.units) return;
   auto at = [&](int chunk) {
     return ((int64_t)(u.base + r / BM * u.chunks + chunk) * a.c.heads + head) * BM + r % BM;
   };

@@ -122,6 +122,34 @@ def test_many_sequences():
     check_attention(c, out, lse)
 
 
+@pytest.mark.parametrize("heads,dim,new", [(11, 64, 1900), (3, 256, 9), (130, 64, 1), (8, 128, 2100)])
+def test_append_and_read_of_head_blocks(heads, dim, new):
+    # lane groups that take eight, fewer and one head each, and a last block of fewer
+    c = Case([(new + 5, new), (40, min(new, 40)), (3, 0), (1, 1)], heads=heads, dim=dim, page=32,
+             dtype=torch.bfloat16, rot=32, neighbours=True, padding=3, seed=heads)
+    cache, batch = append_both(c)
+    cache_equal(cache, c.cache)
+    k, v = kq.kronq_kv_read(cache, batch, c.rows, k=torch.full((c.rows, heads, dim), 7.0, device=DEV),
+                            v=torch.full((c.rows, heads, dim), 7.0, device=DEV))
+    for t, nm in ((k, "k"), (v, "v")):
+        rows = K.read(c.cache, c.batch, c.rows, nm)
+        want = np.stack([np.full((heads, dim), 7.0) if r is None else r for r in rows])
+        assert np.array_equal(f64(t), want.astype(np.float32))
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.bfloat16), (256, torch.float32)])
+def test_append_groups_with_an_entry_that_is_not_finite(dim, dtype):
+    # in the rotated part, behind it, and in the values: that group alone is lost
+    c = Case([(20, 20)], heads=3, dim=dim, dtype=dtype, rot=dim // 2)
+    for row, head, d, x in ((0, 0, 0, np.inf), (3, 1, dim // 4 - 1, -np.inf), (5, 2, dim - 1, np.nan), (6, 0, dim // 2, np.inf)):
+        c.k[row, head, d] = x
+        c.v[row + 1, head, d] = x
+    cache, batch = append_both(c)
+    cache_equal(cache, c.cache)
+    k, v = kq.kronq_kv_read(cache, batch, c.rows)
+    assert int(torch.isnan(k).any(-1).sum()) == 4 and int(torch.isnan(v).any(-1).sum()) == 4
+
+
 # ---------------------------------------------------------------- attention
 
 def attend(c, window=0, sinks=0, scale=None):
@@ -342,7 +370,84 @@ def test_nothing_to_do():
     cache_equal(cache, c.cache)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("page,window,sinks", [(16, 0, 0), (64, 0, 0), (32, 150, 3), (128, 40, 70)])
+def test_prompts_among_single_tokens(dtype, page, window, sinks):
+    # tiles of 256 rows for the prompts, 16 for the others, in one call
+    c = Case([(520, 400), (33, 1), (470, 470), (7, 7), (300, 0), (900, 351)], heads=2, share=3, dim=64, page=page,
+             dtype=dtype, rot=64, padding=2, seed=page)
+    attend(c, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("dim", [128, 256])
+def test_prompts_of_wide_heads(dtype, dim):
+    c = Case([(300, 300), (411, 290)], heads=1, share=2, dim=dim, page=16, dtype=dtype, rot=dim // 2, neighbours=True,
+             spread=2.0, seed=dim)
+    attend(c)
+
+
+def test_sequences_that_share_pages():
+    c = Case([(200, 1), (200, 4), (200, 90)], heads=2, share=2, dim=64, page=32, dtype=torch.float32, rot=64)
+    c.table[1:] = c.table[0]
+    attend(c)
+
+
 # ---------------------------------------------------------------- streams, graphs, together
+
+def test_two_calls_at_once():
+    one = Case([(3000, 2), (700, 600)], heads=2, share=2, dim=128, page=64, dtype=torch.bfloat16, rot=128, seed=1)
+    two = Case([(2000, 600), (2500, 1)], heads=2, share=2, dim=128, page=16, dtype=torch.float16, rot=64, seed=2)
+    ready = [(c.dev(kq), c.q.to(DEV), torch.cuda.Stream()) for c in (one, two)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        for (cache, batch, rope), q, stream in ready:
+            outs.append(kq.kronq_kv_attention(q, cache, batch, rope=rope, stream=stream))
+    torch.cuda.synchronize()
+    for i, c in enumerate((one, two)):
+        check_attention(c, outs[i], None)
+        assert torch.equal(outs[i], outs[i + 2]) and torch.equal(outs[i], outs[i + 4])
+
+
+def test_two_captured_calls_with_workspaces_of_their_own():
+    c = Case([(3000, 2), (700, 300), (90, 1)], heads=2, share=2, dim=64, page=32, dtype=torch.float16, rot=64)
+    cache, batch, rope = c.dev(kq)
+    qs = [c.q.to(DEV), c.q.to(DEV) * 0.5]
+    need = kq.load().kronq_kv_attention_ws(c.rows, 3, 4, 2, 64)
+    outs, graphs, side = [torch.empty_like(q) for q in qs], [], torch.cuda.Stream()
+    spaces = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in qs]
+    torch.cuda.synchronize()
+    for q, out, ws in zip(qs, outs, spaces):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            kq.kronq_kv_attention(q, cache, batch, rope=rope, out=out, ws=ws)
+    other = torch.cuda.Stream()
+    for _ in range(4):
+        for out in outs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(other):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for q, out in zip(qs, outs):
+            assert torch.equal(out, kq.kronq_kv_attention(q, cache, batch, rope=rope))
+        torch.cuda.synchronize()
+        for q in qs:
+            q.copy_(torch.randn_like(q))
+
+
+def test_a_workspace_that_is_too_small_is_replaced_and_a_wrong_one_refused():
+    c = Case([(3000, 2)], heads=2, share=2, dim=64, page=32, dtype=torch.float32)
+    cache, batch, _ = c.dev(kq)
+    q = c.q.to(DEV)
+    want = kq.kronq_kv_attention(q, cache, batch)
+    assert torch.equal(kq.kronq_kv_attention(q, cache, batch, ws=torch.empty(16, dtype=torch.uint8, device=DEV)), want)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.int32, device=DEV)):
+        with pytest.raises(ValueError):
+            kq.kronq_kv_attention(q, cache, batch, ws=ws)
+
 
 def test_another_stream():
     c = Case([(3000, 2), (40, 1)], heads=2, share=2, dim=128, page=16, dtype=torch.bfloat16, rot=128)

@@ -179,6 +179,14 @@ def test_refused_before_any_launch(call, bad):
         assert kq.load().kronq_last_error()
 
 
+@pytest.mark.parametrize("stride", ["k_codes_stride", "v_codes_stride", "k_grid_stride", "v_grid_stride"])
+def test_page_strides_fit_32_bits(stride):
+    for call in ("append", "read", "attention"):
+        a = Raw()
+        setattr(a.cache, stride, 1 << 32)
+        assert getattr(a, call)() == kq.KRONQ_EUNSUPPORTED
+
+
 def test_nothing_to_do_is_fine_without_operands():
     for call in ("append", "read", "attention"):
         a = Raw()
