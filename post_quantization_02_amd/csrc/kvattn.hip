@@ -14,10 +14,13 @@
 namespace kronq {
 namespace {
 
-// ---- one tile of 16 rows
+// ---- one or two tiles of 16 rows
 //
-// A workgroup takes a unit of 16 rows (rows x share of one key head); its four
-// waves take the unit's tiles of 32 keys in turn.  With 16x16x32 fp16 products
+// A workgroup takes a unit of 16 QT rows (rows x share of one key head); its four
+// waves take the unit's tiles of 32 keys in turn.  QT is 2 where sequences have
+// more than 16 such rows on average, for a tile of keys is then unpacked once for
+// 32 (40 sequences of 4 rows x 8, dim 128: 115 us against 135; 24 of 5 rows x 4,
+// dim 64 in fp16: 47 against 51); not for dim 256, which has no registers for it.  With 16x16x32 fp16 products
 // everything stays in registers:
 //   S^T = K Q^T: row i of the 16-key operand a (0, 1) is key 8 (i / 4) + 4 a +
 //     i % 4 of the tile, and lane (i, g) holds values (dim / 4) g and up of it:
@@ -100,9 +103,9 @@ __device__ inline void load_tile(const KvView& c, const TilePages& p, int head, 
 // A tile's queries, made ready by all threads: a thread has eight values of a row
 // (two such where dim is 256), asked for before the first keys, and leaves them as
 // the products' operands in LDS.  What load_query does for a wave by itself.
-template <typename T, int DIM>
+template <typename T, int DIM, int QT>
 struct QueryPiece {
-  static constexpr int kLanes = DIM / 8, kPieces = (16 * kLanes + 255) / 256;
+  static constexpr int kLanes = DIM / 8, kRows = 16 * QT, kPieces = (kRows * kLanes + 255) / 256;
   float x[kPieces][8], o[kPieces][8], c[kPieces][8], s[kPieces][8];
   bool turn[kPieces], fine[kPieces], second[kPieces];
 
@@ -111,8 +114,8 @@ struct QueryPiece {
     const int share = a.shape.share;
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
-      const int row = ((int)threadIdx.x / kLanes + n * (256 / kLanes)) & 15, d = (int)threadIdx.x % kLanes * 8;
-      const int r = u.qtile * 16 + row, tok = min(r / share, u.len - 1), pos = u.ctx - u.len + tok;
+      const int row = ((int)threadIdx.x / kLanes + n * (256 / kLanes)) & (kRows - 1), d = (int)threadIdx.x % kLanes * 8;
+      const int r = u.qtile * kRows + row, tok = min(r / share, u.len - 1), pos = u.ctx - u.len + tok;
       const T* p = static_cast<const T*>(a.q.data) + (int64_t)(u.row0 + tok) * a.q.row +
                    (int64_t)(head * share + r % share) * a.q.head + d;
       fine[n] = !rope.half || pos < rope.positions;
@@ -140,7 +143,7 @@ struct QueryPiece {
     const int share = a.shape.share;
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
-      if (kLanes == 8 && threadIdx.x >= 128) break;         // 16 rows of eight threads
+      if (kRows * kLanes < 256 && (int)threadIdx.x >= kRows * kLanes) break;   // whole waves
       const int row = (int)threadIdx.x / kLanes + n * (256 / kLanes), d8 = (int)threadIdx.x % kLanes;
       float y[8], big = 0;
 #pragma unroll
@@ -171,28 +174,28 @@ struct QueryPiece {
         q1[k] = (_Float16)z;
         if constexpr (PARTS > 1) q2[k] = (_Float16)(z - (float)q1[k]);
       }
-      const int lane = row + 16 * (d8 / (DIM / 32)), k = d8 % (DIM / 32);
-      q[0][k][lane] = q1;
-      if constexpr (PARTS > 1) q[PARTS - 1][k][lane] = q2;
+      const int lane = (row & 15) + 16 * (d8 / (DIM / 32)), k = d8 % (DIM / 32), at = (row >> 4) * PARTS;
+      q[at][k][lane] = q1;
+      if constexpr (PARTS > 1) q[at + 1][k][lane] = q2;
       if (d8 == 0) {
-        const int tok = min((u.qtile * 16 + row) / share, u.len - 1);
+        const int tok = min((u.qtile * kRows + row) / share, u.len - 1);
         f[row] = bad && u.ctx - u.len + tok >= 0 ? kNan : fmaxf(ldexpf(a.scale * kLog2e, -e2), 0x1p-126f);
       }
     }
   }
 };
 
-template <int DIM, typename T, int PARTS, bool SMALL>
-__global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnView a) {
-  constexpr int BM = 16, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
+template <int DIM, typename T, int PARTS, bool SMALL, int QT>
+__global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3) void kv_attention16(AttnView a) {
+  constexpr int BM = 16 * QT, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
   constexpr int AHEAD = 2;                            // tiles in registers; a third one gained nothing
-  __shared__ float lds_o[4][BM][PAD];
-  __shared__ float lds_m[4][BM], lds_l[4][BM];
+  __shared__ float lds_o[4][16][PAD];
+  __shared__ float lds_m[4][16], lds_l[4][16];
   // of a tile's grids: scales (32 keys, 32 values) and the zero points' constants
   __shared__ __align__(16) float lds_s[4][64];
   __shared__ __align__(16) uint32_t lds_kz[4][32][2];
   __shared__ __align__(16) uint16_t lds_vz[4][2][32];
-  __shared__ half8_t lds_q[PARTS][KS][64];
+  __shared__ half8_t lds_q[QT * PARTS][KS][64];
   __shared__ float lds_f[BM];
   Unit u;
   if (!find_unit<BM, KT>(a, blockIdx.x, false, u)) return;
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) at[n] = tile_pages<SMALL>(a.c, table, tile_key(w0 + 4 * n));
   }
-  QueryPiece<T, DIM> piece;
+  QueryPiece<T, DIM, QT> piece;
   piece.ask(a, u, head);
   __builtin_amdgcn_sched_barrier(0);
   if (w0 < v1) {
@@ -226,24 +229,35 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  // this lane's query row
-  const int r = u.qtile * BM + i, pos = u.ctx - u.len + min(r / share, u.len - 1);
-  half8_t q1[KS], q2[PARTS > 1 ? KS : 1];
+  // this lane's query rows
   piece.template put<PARTS>(a, u, lds_q, lds_f);
   __syncthreads();
+  int pos[QT];
+  half8_t q1[QT][KS], q2[QT][PARTS > 1 ? KS : 1];
+  float f[QT];
 #pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    q1[k] = lds_q[0][k][lane];
-    if constexpr (PARTS > 1) q2[k] = lds_q[PARTS - 1][k][lane];
+  for (int t = 0; t < QT; ++t) {
+    pos[t] = u.ctx - u.len + min((u.qtile * BM + 16 * t + i) / share, u.len - 1);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q1[t][k] = lds_q[t * PARTS][k][lane];
+      if constexpr (PARTS > 1) q2[t][k] = lds_q[t * PARTS + 1][k][lane];
+    }
+    f[t] = lds_f[16 * t + i];
   }
-  const float f = lds_f[i];
 
   const Unpacker un;
-  f32x4 o[VT];
+  f32x4 o[QT][VT];
+  float m[QT], l[QT];                                 // m of f S; l of this lane's keys
+  int e[QT];
 #pragma unroll
-  for (int k = 0; k < VT; ++k) o[k] = f32x4{0, 0, 0, 0};
-  float m = -INFINITY, l = 0;                         // of f S; l of this lane's keys
-  int e = kLeast;
+  for (int t = 0; t < QT; ++t) {
+#pragma unroll
+    for (int k = 0; k < VT; ++k) o[t][k] = f32x4{0, 0, 0, 0};
+    m[t] = -INFINITY;
+    l[t] = 0;
+    e[t] = kLeast;
+  }
 
   // Tile v, whose data and pages are given: the data of tile v + 4 (AHEAD - 1) (of
   // pages looked up a tile before) and the pages of the tile after that are asked
@@ -267,91 +281,98 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
     load_tile<DIM, SMALL>(a.c, ahead, head, tile_key(v + 4 * (AHEAD - 1)), next);
     pages = tile_pages<SMALL>(a.c, table, tile_key(v + 4 * AHEAD));
     __builtin_amdgcn_wave_barrier();                  // those parts of LDS are this wave's alone
-    f32x4 sc[2];
+    f32x4 sc[QT][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const u32x2_alias z = *reinterpret_cast<const u32x2_alias*>(lds_kz[wave][8 * (i >> 2) + 4 * b + (i & 3)]);
       const half2_t z1 = as_half2(z.x), z2 = as_half2(z.y);
-      sc[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int t = 0; t < QT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const half8_t kv = un.word(cur.k[b][k], z1, z2);
-        sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q1[k], sc[b], 0, 0, 0);
-        if constexpr (PARTS > 1) sc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q2[k], sc[b], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          sc[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q1[t][k], sc[t][b], 0, 0, 0);
+          if constexpr (PARTS > 1) sc[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv, q2[t][k], sc[t][b], 0, 0, 0);
+        }
       }
     }
-    float s[8], vs[8], top = -INFINITY;
+    half8_t p1[QT], p2[QT];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const f32x4_alias ks = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][8 * g + 4 * b]);
-      const f32x4_alias vv = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][32 + 8 * g + 4 * b]);
+    for (int t = 0; t < QT; ++t) {
+      float s[8], vs[8], top = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s[4 * b + x] = sc[b][x] * ks[x];
-        vs[4 * b + x] = vv[x];
+      for (int b = 0; b < 2; ++b) {
+        const f32x4_alias ks = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][8 * g + 4 * b]);
+        const f32x4_alias vv = *reinterpret_cast<const f32x4_alias*>(&lds_s[wave][32 + 8 * g + 4 * b]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[4 * b + x] = sc[t][b][x] * ks[x];
+          vs[4 * b + x] = vv[x];
+        }
       }
-    }
-    if (edge) {
+      if (edge) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int j = key0 + 8 * g + x;
+          const bool seen = (j <= pos[t]) & ((window == 0) | (j > pos[t] - window) | (j < sinks));
+          s[x] = !seen ? -INFINITY : bad ? kNan : s[x];
+          vs[x] = seen ? vs[x] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) top = fmaxf(top, s[x]);
+      top *= f[t];
+      if (__any(top > m[t] + kLazy || (m[t] == -INFINITY && top > m[t]))) {
+        float nm = fmaxf(top, __shfl_xor(top, 16));
+        nm = fmaxf(nm, __shfl_xor(nm, 32));
+        nm = fmaxf(nm, m[t]);
+        if (m[t] != -INFINITY) {
+          const float down = fminf(nm - m[t], 300.0f);
+          const int ne = max(e[t] - (int)ceilf(down), kLeast);
+          const float by = __builtin_amdgcn_exp2f((float)(e[t] - ne) - down);
+          l[t] *= __builtin_amdgcn_exp2f(-down);
+#pragma unroll
+          for (int k = 0; k < VT; ++k) o[t][k] *= by;
+          e[t] = ne;
+        }
+        m[t] = nm;
+      }
+      // weights times 2^-ue, the part of the row's factor that they can carry (none
+      // before the first is known)
+      const int ue = e[t] == kLeast ? 0 : min(max(e[t], -60), 30);
+      const float base = (m[t] == -INFINITY ? 0.0f : m[t]) + (float)ue;
+      float y[8], ytop = 0, sum = 0;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const int j = key0 + 8 * g + x;
-        const bool seen = (j <= pos) & ((window == 0) | (j > pos - window) | (j < sinks));
-        s[x] = !seen ? -INFINITY : bad ? kNan : s[x];
-        vs[x] = seen ? vs[x] : 0.0f;
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[x], f[t], -base));
+        sum += p;
+        y[x] = p * vs[x];
+        ytop = fmaxf(ytop, y[x]);
       }
-    }
+      l[t] += sum * ldexpf(1.0f, ue);
+      if (__any(ytop > ldexpf(1.0f, min(kTop + e[t] - ue, 127)))) {
+        ytop = fmaxf(ytop, __shfl_xor(ytop, 16));
+        ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
+        if (ytop > ldexpf(1.0f, min(kTop + e[t] - ue, 127))) {
+          const int ne = min(max(exponent_for(ytop) + ue, kLeast), kMost);
+          const float by = ldexpf(1.0f, e[t] - ne);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) top = fmaxf(top, s[x]);
-    top *= f;
-    if (__any(top > m + kLazy || (m == -INFINITY && top > m))) {
-      float nm = fmaxf(top, __shfl_xor(top, 16));
-      nm = fmaxf(nm, __shfl_xor(nm, 32));
-      nm = fmaxf(nm, m);
-      if (m != -INFINITY) {
-        const float down = fminf(nm - m, 300.0f);
-        const int ne = max(e - (int)ceilf(down), kLeast);
-        const float by = __builtin_amdgcn_exp2f((float)(e - ne) - down);
-        l *= __builtin_amdgcn_exp2f(-down);
-#pragma unroll
-        for (int k = 0; k < VT; ++k) o[k] *= by;
-        e = ne;
+          for (int k = 0; k < VT; ++k) o[t][k] *= by;
+          e[t] = ne;
+        }
       }
-      m = nm;
-    }
-    // weights times 2^-ue, the part of the row's factor that they can carry (none
-    // before the first is known)
-    const int ue = e == kLeast ? 0 : min(max(e, -60), 30);
-    const float base = (m == -INFINITY ? 0.0f : m) + (float)ue;
-    float y[8], ytop = 0, sum = 0;
+      if (__any(e[t] != ue)) {
+        const float by = ldexpf(1.0f, ue - e[t]);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[x], f, -base));
-      sum += p;
-      y[x] = p * vs[x];
-      ytop = fmaxf(ytop, y[x]);
-    }
-    l += sum * ldexpf(1.0f, ue);
-    if (__any(ytop > ldexpf(1.0f, min(kTop + e - ue, 127)))) {
-      ytop = fmaxf(ytop, __shfl_xor(ytop, 16));
-      ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
-      if (ytop > ldexpf(1.0f, min(kTop + e - ue, 127))) {
-        const int ne = min(max(exponent_for(ytop) + ue, kLeast), kMost);
-        const float by = ldexpf(1.0f, e - ne);
-#pragma unroll
-        for (int k = 0; k < VT; ++k) o[k] *= by;
-        e = ne;
+        for (int x = 0; x < 8; ++x) y[x] *= by;
       }
-    }
-    if (__any(e != ue)) {
-      const float by = ldexpf(1.0f, ue - e);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) y[x] *= by;
-    }
-    half8_t p1, p2;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      p1[x] = (_Float16)y[x];
-      if constexpr (PARTS > 1) p2[x] = (_Float16)(y[x] - (float)p1[x]);
+      for (int x = 0; x < 8; ++x) {
+        p1[t][x] = (_Float16)y[x];
+        if constexpr (PARTS > 1) p2[t][x] = (_Float16)(y[x] - (float)p1[t][x]);
+      }
     }
     const u32x4_alias z1 = *reinterpret_cast<const u32x4_alias*>(&lds_vz[wave][0][8 * g]);
     const u32x4_alias z2 = *reinterpret_cast<const u32x4_alias*>(&lds_vz[wave][1][8 * g]);
@@ -367,11 +388,14 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
       }
       const half8_t va{lo[0].x, lo[0].y, lo[1].x, lo[1].y, lo[2].x, lo[2].y, lo[3].x, lo[3].y};
       const half8_t vb{hi[0].x, hi[0].y, hi[1].x, hi[1].y, hi[2].x, hi[2].y, hi[3].x, hi[3].y};
-      o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p1, o[2 * b], 0, 0, 0);
-      o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p1, o[2 * b + 1], 0, 0, 0);
-      if constexpr (PARTS > 1) {
-        o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p2, o[2 * b], 0, 0, 0);
-        o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p2, o[2 * b + 1], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        o[t][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p1[t], o[t][2 * b], 0, 0, 0);
+        o[t][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p1[t], o[t][2 * b + 1], 0, 0, 0);
+        if constexpr (PARTS > 1) {
+          o[t][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va, p2[t], o[t][2 * b], 0, 0, 0);
+          o[t][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vb, p2[t], o[t][2 * b + 1], 0, 0, 0);
+        }
       }
     }
   };
@@ -383,54 +407,58 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : 3) void kv_attention16(AttnVi
     }
   }
 
-  // the four waves' parts
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  if (lane < 16) {
-    lds_m[wave][i] = m;
-    lds_l[wave][i] = l;
-  }
-  const float back = ldexpf(1.0f, e);
+  // the four waves' parts, sixteen rows at a time
 #pragma unroll
-  for (int rr = 0; rr < 4; ++rr) {
-#pragma unroll
-    for (int k = 0; k < VT; k += 4)
-      *reinterpret_cast<f32x4*>(&lds_o[wave][i][VT * (4 * g + rr) + k]) =
-          f32x4{o[k][rr], o[k + 1][rr], o[k + 2][rr], o[k + 3][rr]} * back;
-  }
-  __syncthreads();
-  // thread: 8 values of one row at a time
-  for (int c = tid; c < BM * DIM / 8; c += 256) {
-    const int row = c / (DIM / 8), d = (c % (DIM / 8)) * 8;
-    const int rg = u.qtile * BM + row;
-    if (rg >= u.len * share) continue;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, lds_m[w][row]);
-    float ll = 0, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float by = lds_m[w][row] == -INFINITY ? 0.0f : exp2f(lds_m[w][row] - mm);
-      ll += lds_l[w][row] * by;
-#pragma unroll
-      for (int y = 0; y < 8; ++y) x[y] += lds_o[w][row][d + y] * by;
+  for (int t = 0; t < QT; ++t) {
+    if (t) __syncthreads();
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (lane < 16) {
+      lds_m[wave][i] = m[t];
+      lds_l[wave][i] = l[t];
     }
-    const int tok = rg / share, qh = head * share + rg % share;
-    // a position without a column: its row sees at least itself
-    if (u.ctx - u.len + tok >= room_of(a.c)) ll = kNan;
-    if (u.chunks == 1) {
-      const float inv = ll == 0 ? 0.0f : 1.0f / ll;
+    const float back = ldexpf(1.0f, e[t]);
 #pragma unroll
-      for (int y = 0; y < 8; ++y) x[y] = ll == 0 ? 0.0f : x[y] * inv;
-      store8(static_cast<T*>(a.out.data) + (int64_t)(u.row0 + tok) * a.out.row + (int64_t)qh * a.out.head + d, x);
-      if (a.lse && d == 0)
-        a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = ll == 0 ? -INFINITY : (mm + log2f(ll)) * kLn2;
-    } else {
-      const int64_t at = ((int64_t)blockIdx.x * a.c.heads + head) * BM + row;
-      store8(a.part + at * DIM + d, x);
-      if (d == 0) {
-        a.stat[2 * at] = mm;
-        a.stat[2 * at + 1] = ll;
+    for (int rr = 0; rr < 4; ++rr) {
+#pragma unroll
+      for (int k = 0; k < VT; k += 4)
+        *reinterpret_cast<f32x4*>(&lds_o[wave][i][VT * (4 * g + rr) + k]) =
+            f32x4{o[t][k][rr], o[t][k + 1][rr], o[t][k + 2][rr], o[t][k + 3][rr]} * back;
+    }
+    __syncthreads();
+    // thread: 8 values of one row at a time
+    for (int c = tid; c < 16 * DIM / 8; c += 256) {
+      const int row = c / (DIM / 8), d = (c % (DIM / 8)) * 8;
+      const int rg = u.qtile * BM + 16 * t + row;
+      if (rg >= u.len * share) continue;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, lds_m[w][row]);
+      float ll = 0, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float by = lds_m[w][row] == -INFINITY ? 0.0f : exp2f(lds_m[w][row] - mm);
+        ll += lds_l[w][row] * by;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) x[y] += lds_o[w][row][d + y] * by;
+      }
+      const int tok = rg / share, qh = head * share + rg % share;
+      // a position without a column: its row sees at least itself
+      if (u.ctx - u.len + tok >= room_of(a.c)) ll = kNan;
+      if (u.chunks == 1) {
+        const float inv = ll == 0 ? 0.0f : 1.0f / ll;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) x[y] = ll == 0 ? 0.0f : x[y] * inv;
+        store8(static_cast<T*>(a.out.data) + (int64_t)(u.row0 + tok) * a.out.row + (int64_t)qh * a.out.head + d, x);
+        if (a.lse && d == 0)
+          a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = ll == 0 ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        const int64_t at = ((int64_t)blockIdx.x * a.c.heads + head) * BM + 16 * t + row;
+        store8(a.part + at * DIM + d, x);
+        if (d == 0) {
+          a.stat[2 * at] = mm;
+          a.stat[2 * at + 1] = ll;
+        }
       }
     }
   }
@@ -518,6 +546,7 @@ constexpr int kWholeTiles16 = 32;
 // search, its query, the first tile) takes 8 us and all units' starts then pass
 // together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72.
 constexpr int kUnits16 = 704;
+constexpr int kUnits32 = 480;            // of 512: two tiles of rows, dim 128
 // The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
 // have that many on average (a tile of keys is unpacked once for all of its rows).
 // 2047 and 1774 rows x 4 behind 9001 and 4830 keys, dim 128: 616 us in tiles of 128
@@ -536,6 +565,7 @@ constexpr int64_t kJoinGroups = 512;
 // tiles, and chunks on top), and whether there can be chunks to join.
 struct Plan {
   int units16, units_rows, waves;
+  int tall;                              // the first's tiles are of 16 << tall rows
   bool join16, join_rows;
   size_t part16, part_rows;              // floats of partial results
 };
@@ -545,8 +575,10 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
   const int64_t n = rows * share, some = std::min(rows, seqs);
   const bool few = n <= kFewRows * some;   // on average, or for sure
   if (few || seqs > 1) {
-    const int64_t tiles = std::min((n + 15 * some) / 16, few ? n : some * ((kFewRows + 15) / 16));
-    const int64_t more = std::max<int64_t>(kUnits16 / heads - tiles / 2, 1);
+    p.tall = few && n > 16 * some && dim < 256;
+    const int64_t bm = 16 << p.tall;
+    const int64_t tiles = std::min((n + (bm - 1) * some) / bm, few ? n : some * ((kFewRows + 15) / 16));
+    const int64_t more = std::max<int64_t>((p.tall && dim == 128 ? kUnits32 : kUnits16) / heads - tiles / 2, 1);
     p.units16 = (int)(tiles + more);
     p.join16 = more > 1;
   }
@@ -558,7 +590,7 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
     p.units_rows = (int)(tiles + more);
     p.join_rows = more > 1;
   }
-  if (p.join16) p.part16 = (size_t)p.units16 * heads * 16 * (dim + 2);
+  if (p.join16) p.part16 = (size_t)p.units16 * heads * (16 << p.tall) * (dim + 2);
   if (p.join_rows) p.part_rows = (size_t)p.units_rows * heads * 32 * p.waves * (dim + 2);
   return p;
 }
@@ -580,25 +612,33 @@ kronq_status join(const AttnView& a, int64_t per, hipStream_t s) {
   return KRONQ_OK;
 }
 
+template <int DIM, typename T, int PARTS, int QT>
+kronq_status launch_few(AttnView a, const Plan& p, bool both, float* ws, hipStream_t s) {
+  a.shape.least = 1;
+  a.shape.most = both ? kFewRows : INT32_MAX;
+  a.units = p.units16;
+  a.min_tiles = room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
+  a.part = ws;
+  a.stat = ws + (size_t)p.units16 * a.c.heads * (16 * QT) * DIM;
+  const dim3 grid((unsigned)a.units, (unsigned)a.c.heads);
+  if (a.c.lgp == 4) hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, true, QT>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, false, QT>), grid, dim3(256), 0, s, a);
+  KQ_LAUNCHED("kv_attention16");
+  if (!p.join16) return KRONQ_OK;
+  return join<DIM, 16 * QT, 32, T>(a, both ? std::max(kFewRows / a.shape.share, 1) : 0, s);
+}
+
 template <int DIM, typename T, int PARTS>
 kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s) {
   const Plan p = plan_of(a.c.rows, a.c.seqs, a.shape.share, a.c.heads, DIM);
   const bool both = p.units16 && p.units_rows;
   if (p.units16) {
-    a.shape.least = 1;
-    a.shape.most = both ? kFewRows : INT32_MAX;
-    a.units = p.units16;
-    a.min_tiles = room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
-    a.part = ws;
-    a.stat = ws + (size_t)p.units16 * a.c.heads * 16 * DIM;
-    const dim3 grid((unsigned)a.units, (unsigned)a.c.heads);
-    if (a.c.lgp == 4) hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, false>), grid, dim3(256), 0, s, a);
-    KQ_LAUNCHED("kv_attention16");
-    if (p.join16) {
-      const kronq_status st = join<DIM, 16, 32, T>(a, std::max(kFewRows / a.shape.share, 1), s);
-      if (st) return st;
-    }
+    kronq_status st;
+    if constexpr (DIM < 256)
+      st = p.tall ? launch_few<DIM, T, PARTS, 2>(a, p, both, ws, s) : launch_few<DIM, T, PARTS, 1>(a, p, both, ws, s);
+    else
+      st = launch_few<DIM, T, PARTS, 1>(a, p, both, ws, s);
+    if (st) return st;
   }
   if (p.units_rows) {
     a.shape.least = both ? kFewRows + 1 : 1;

@@ -387,6 +387,22 @@ def test_prompts_of_wide_heads(dtype, dim):
     attend(c)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("dim,page,window", [(64, 16, 0), (128, 16, 0), (128, 64, 700), (256, 32, 300), (64, 64, 5)])
+def test_short_drafts(dtype, dim, page, window):
+    # 17 to 32 rows x share on average, some sequences of fewer and of more
+    c = Case([(1500, 6), (40, 6), (900, 1), (6, 6), (333, 9)], heads=2, share=4, dim=dim, page=page, dtype=dtype,
+             rot=64, padding=1, seed=dim + page)
+    attend(c, window, 3 if window else 0)
+
+
+def test_chunks_of_uneven_rows_are_all_joined():
+    # more rows than one a sequence, of so many query heads that 32 / share is one
+    c = Case([(2600, 1), (2500, 4), (30, 1), (2700, 1), (2600, 1), (2600, 1), (2600, 1)], heads=1, share=20, dim=64,
+             page=64, dtype=torch.float32)
+    attend(c)
+
+
 def test_sequences_that_share_pages():
     c = Case([(200, 1), (200, 4), (200, 90)], heads=2, share=2, dim=64, page=32, dtype=torch.float32, rot=64)
     c.table[1:] = c.table[0]
