@@ -9,7 +9,7 @@
 //   S^T = K Q^T: lane (row, h) gets, of each 16 keys, the eight keys 8 h and up
 //     (the LDS rows of the keys are ordered for that),
 //   O^T = V^T P^T: which are its k slots, so weights stay in registers.
-// The 16-byte pieces of an LDS row are exchanged so that eight lanes that read or
+// The 16-byte pieces of an LDS row are exchanged so that sixteen lanes that read or
 // write at once use all banks.
 //
 // FOLD (bf16 results): the scales, too, go into the fp16 operands, as s 2^-e with
@@ -47,8 +47,11 @@ template <int DIM, int WAVES>
 struct Split {
   static constexpr int kKeys = KT / WAVES, kParts = 64 / kKeys, kWords = DIM / 8 / kParts;
   static constexpr int kCols = 64 / (kKeys / 8), kVals = DIM / kCols;
-  // Where a piece (eight values of a key, or of eight keys a value) stands in its row
-  __device__ static constexpr int key_piece(int piece, int row) { return piece ^ (row & 7); }
+  // Where a piece (eight values of a key, or of eight keys a value) stands in its row:
+  // sixteen neighbouring rows' same pieces lie in all 64 banks (256 bytes)
+  __device__ static constexpr int key_piece(int piece, int row) {
+    return DIM == 64 ? value_piece(piece, row) : piece ^ (row & 15);
+  }
   __device__ static constexpr int value_piece(int piece, int d) { return piece ^ ((d ^ (d >> 3)) & 7); }
 };
 
@@ -300,7 +303,7 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
   auto read = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      kv[k % RING][s] = *reinterpret_cast<const half8_t*>(&cur->k[32 * s + i][8 * S::key_piece(2 * k + h, i)]);
+      kv[k % RING][s] = *reinterpret_cast<const half8_t*>(&cur->k[32 * s + i][8 * S::key_piece(2 * k + h, 32 * s + i)]);
     if constexpr (QLDS) second[k % RING] = lds_q[k][lane];
   };
 #pragma unroll
