@@ -185,6 +185,13 @@ struct QueryPiece {
   }
 };
 
+// In its loop bound by HBM and the vector pipes alike: dim 128, bf16, 131071 keys of
+// 8 key heads for one token 33 us (143 MB: 4.3 TB/s, 7 in the loop; 8 us pass before
+// it, in three misses one behind the other), 40 sequences of up to 12000 keys 63 us
+// (281 MB).  By the vector pipes alone with one query head a key head (fp32, 12 of
+// up to 4095 keys, 32 heads: 41 us, 122 MB) and with dim 64 (fp16, 24 x 5 rows x 4 in a
+// window of 4096: 42 us).  A wave issues 250 vector operations a tile for 16 rows and
+// 8 products a part.
 template <int DIM, typename T, int PARTS, bool SMALL, int QT>
 __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3) void kv_attention16(AttnView a) {
   constexpr int BM = 16 * QT, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
@@ -467,7 +474,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
 // Joins the chunks of a row's heads, in the order of the chunks.  blockIdx.x: a
 // row; or, where few rows of each sequence are this kernel's (per > 0), a
 // sequence's row, per for each.  A head is joined by `slots` groups of lanes (a
-// power of two), each of which adds up every slots-th chunk.
+// power of two), each of which adds up every slots-th chunk.  Latency: 5 to 6 us.
 template <int DIM, int BM, int KT, typename T>
 __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, int slots) {
   constexpr int LANES = DIM / 8, GROUPS = 256 / LANES;
@@ -531,20 +538,27 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, in
 
 // ---- launch
 //
-// Sequences of up to kFewRows rows x share go to the 16-row kernel, which reads
-// the cache once for each 16 of them; longer ones to the 128-row kernel.  Both
-// take any length, so a batch whose sequences have few rows on average is one
-// launch of the first (a launch that finds nothing costs 5 us).
+// Sequences of up to kFewRows rows x share go to the kernel of few rows, which
+// reads and unpacks the cache once for each 16 or 32 of them; longer ones to the
+// kernel of 128 or 256.  Both take any length, so a batch whose sequences have few
+// rows on average is one launch of the first (a launch that finds nothing costs
+// 5 us).  8 sequences of up to 8000 keys, dim 128, bf16, with up to 64, 96, 128 rows x
+// share: 32, 40, 44 us by the kernel of few, 70, 75, 77 by both; 24 sequences of up to
+// 96, 128, 192: 105, 130, 181 and 129, 134, 158.
 
-constexpr int kFewRows = 32;
-constexpr int kMinTiles16 = 8;           // tiles of a chunk at least: two for each wave
-// Where the table has room for no more than this, the keys are not cut: eight
-// steps of a wave cost less than a join behind two.
-constexpr int kWholeTiles16 = 32;
+constexpr int kFewRows = 64;
+// Tiles of a chunk at least: two for each wave (3000 keys: 14.4 us at 4, 13.8 at 8,
+// 14.8 at 16; 6000 keys: 15.3, 16.4, 16.8).
+constexpr int kMinTiles16 = 8;
+// Where the table has room for no more than this, the keys are not cut: six steps
+// of a wave cost less than a join behind two (one token, whole and cut: 613 keys
+// 11.5 and 12.3 us, 1000 keys 14.7 and 12.3).
+constexpr int kWholeTiles16 = 24;
 // Chunks over all key heads that a launch aims at: a little under the 768
 // workgroups that are resident at once (three on a CU), because a unit's start (its
 // search, its query, the first tile) takes 8 us and all units' starts then pass
-// together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72.
+// together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72 (when a
+// start was 2 us longer).
 constexpr int kUnits16 = 704;
 constexpr int kUnits32 = 480;            // of 512: two tiles of rows, dim 128
 // The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
@@ -558,7 +572,7 @@ constexpr int kMinTilesRows = 4;         // 256 keys
 constexpr int kResident = 512, kResidentTall = 256;
 
 // The join gives each row's head as many groups of lanes as make this many
-// workgroups.
+// workgroups (40 sequences, attention and join: 72 us at 128, 71 at 512, 76 at 2048).
 constexpr int64_t kJoinGroups = 512;
 
 // How a call is cut: units of each kernel (0: not launched; a bound of its row

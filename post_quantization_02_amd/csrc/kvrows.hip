@@ -331,7 +331,11 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
 }
 
 // Bound by the vector pipes (the exponentials and what surrounds them, and
-// unpacking) and the matrix cores together.
+// unpacking: 335 operations a wave and 64 keys at dim 128 in bf16) and the matrix
+// cores (32 products of 32 cycles) together, which two waves on a SIMD overlap in
+// part; LDS conflicts are 2 % of it.  2047 + 1774 rows x 4 of 8 key heads behind 9001
+// and 4830 keys: 562 us, 680 TFLOP/s; fp16 in a window of 2048, queries in two parts:
+// 177 us.
 template <int DIM, typename T, int QP, int PP, bool FOLD, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && QP > 1 && WAVES == 4) ? 1 : 2)
 void kv_attention_rows(AttnView a) {
@@ -375,8 +379,9 @@ void kv_attention_rows(AttnView a) {
   int e = kLeast;                                     // not FOLD: O is held times 2^-e
   float ref = -INFINITY;                              // FOLD: O is held times 2^(kUp - ref)
 
-  // The tile `at` on its way to LDS, and its keys that are still to go there.  What is asked for is asked for every time, the last
-  // tile again behind the end: see the kernel of few rows.
+  // The tile `at` on its way to LDS, and its keys that are still to go there.  What
+  // is asked for is asked for every time, the last tile again behind the end: see
+  // the kernel of few rows.
   const Unpacker un;
   Raw<DIM, WAVES> raw;
   const bool whole = a.c.lgp >= 6;                    // pages hold whole tiles
