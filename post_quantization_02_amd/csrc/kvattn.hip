@@ -575,6 +575,10 @@ constexpr int kResident = 512, kResidentTall = 256;
 // workgroups (40 sequences, attention and join: 72 us at 128, 71 at 512, 76 at 2048).
 constexpr int64_t kJoinGroups = 512;
 
+// Tiles of a chunk at least where nothing may be cut: the units that a batch does
+// not need for its row tiles (they are a bound) would otherwise be taken for chunks.
+constexpr int kUncut = INT32_MAX;
+
 // How a call is cut: units of each kernel (0: not launched; a bound of its row
 // tiles, and chunks on top), and whether there can be chunks to join.
 struct Plan {
@@ -631,7 +635,7 @@ kronq_status launch_few(AttnView a, const Plan& p, bool both, float* ws, hipStre
   a.shape.least = 1;
   a.shape.most = both ? kFewRows : INT32_MAX;
   a.units = p.units16;
-  a.min_tiles = room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
+  a.min_tiles = !p.join16 ? kUncut : room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
   a.part = ws;
   a.stat = ws + (size_t)p.units16 * a.c.heads * (16 * QT) * DIM;
   const dim3 grid((unsigned)a.units, (unsigned)a.c.heads);
@@ -658,7 +662,7 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
     a.shape.least = both ? kFewRows + 1 : 1;
     a.shape.most = INT32_MAX;
     a.units = p.units_rows;
-    a.min_tiles = kMinTilesRows;
+    a.min_tiles = p.join_rows ? kMinTilesRows : kUncut;
     a.part = ws + p.part16;
     a.stat = a.part + (size_t)p.units_rows * a.c.heads * 32 * p.waves * DIM;
     const kronq_status st = kv_rows_launch(a, dim, dtype, p.waves, s);

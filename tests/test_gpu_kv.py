@@ -454,6 +454,19 @@ def test_two_captured_calls_with_workspaces_of_their_own():
             q.copy_(torch.randn_like(q))
 
 
+@pytest.mark.parametrize("lengths", [[(1000, 3)] * 20 + [(7, 0)] * 40, [(800, 780)] + [(7, 0)] * 11],
+                         ids=["few rows", "many rows"])
+def test_row_tiles_enough_are_not_cut(lengths):
+    # rows of few of the sequences: row tiles are less than the bound the launch is made for
+    c = Case(lengths, heads=32, share=1, dim=64, page=64, dtype=torch.bfloat16, rot=64)
+    cache, batch, rope = c.dev(kq)
+    need = kq.load().kronq_kv_attention_ws(c.rows, len(lengths), 32, 32, 64)
+    space = torch.full((need + (1 << 24),), 7, dtype=torch.uint8, device=DEV)
+    out, lse = kq.kronq_kv_attention(c.q.to(DEV), cache, batch, rope=rope, want_lse=True, ws=space[:need])
+    check_attention(c, out, lse)
+    assert bool((space[need:] == 7).all())
+
+
 def test_a_workspace_that_is_too_small_is_replaced_and_a_wrong_one_refused():
     c = Case([(3000, 2)], heads=2, share=2, dim=64, page=32, dtype=torch.float32)
     cache, batch, _ = c.dev(kq)

@@ -264,6 +264,18 @@ def test_units_cover_each_visible_key_once(index, bm, kt):
             assert used >= sum(k > 0 for _, k in lengths)
 
 
+@pytest.mark.parametrize("bm,kt", [(16, 32), (32, 32), (128, 64), (256, 64)])
+def test_where_nothing_may_be_cut_no_unit_is_a_chunk(index, bm, kt):
+    # units for every sequence's rows, of which few have any
+    for lengths in ([(1000, 3)] * 20 + [(7, 0)] * 40, [(800, 780)] + [(7, 0)] * 11, [(0, 0), (64, 1)]):
+        ctx = np.array([c for c, _ in lengths], np.int32)
+        cu = np.concatenate([[0], np.cumsum([k for _, k in lengths])]).astype(np.int32)
+        table = np.zeros((len(lengths), 70), np.int32)
+        rows = int(cu[-1])
+        st, used = cover(index, table, ctx, cu, 9, 4, rows, 2, 0, 0, bm, kt, rows + 100, 2 ** 31 - 1, True)
+        assert st == 0 and used == sum(-(-2 * k // bm) for _, k in lengths)
+
+
 def test_any_batch_content_stays_in_bounds(index):
     rng = np.random.default_rng(1)
     big = 2 ** 31 - 1
