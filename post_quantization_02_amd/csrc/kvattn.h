@@ -66,19 +66,22 @@ __device__ inline double wave_sum(double x) {
 template <int BM, int KT>
 __device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit& u) {
   const int lane = threadIdx.x & 63;
-  // sums of integers below 2^53: exact
-  double rows = 0, work = 0;
   Seq s = seq_at(a.c, a.shape, lane, BM, KT);
-  for (int b0 = 0;;) {
-    rows += s.qtiles;
-    work += (double)s.qtiles * s.tiles;
-    b0 += 64;
-    if (b0 >= a.c.seqs) break;
-    s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
+  int per = a.min_tiles;
+  if (room_of(a.c) > (int64_t)per * KT) {             // else nothing is cut
+    // sums of integers below 2^53: exact
+    double rows = s.qtiles, work = (double)s.qtiles * s.tiles;
+    for (int b0 = 64; b0 < a.c.seqs; b0 += 64) {
+      s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
+      rows += s.qtiles;
+      work += (double)s.qtiles * s.tiles;
+    }
+    if (a.c.seqs > 1) {                               // one sequence is lane 0's
+      rows = wave_sum(rows);
+      work = wave_sum(work);
+    }
+    per = chunk_tiles(work, rows, a.units, per);
   }
-  rows = wave_sum(rows);
-  work = wave_sum(work);
-  const int per = chunk_tiles(work, rows, a.units, a.min_tiles);
   int before = 0;
   for (int b0 = 0; b0 < a.c.seqs; b0 += 64) {
     if (a.c.seqs > 64) s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
