@@ -18,6 +18,7 @@ struct AttnView {
   float scale;
   AttnShape shape;
   int units;               // work units of a key head
+  int aim;                 // of them to be used, as a rule
   int min_tiles;           // tiles of a chunk at least
   float* part;             // [units][heads][BM][dim] unnormalized outputs
   float* stat;             // [units][heads][BM][2]   maximum (of f S), sum
@@ -80,7 +81,9 @@ __device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit&
       rows = wave_sum(rows);
       work = wave_sum(work);
     }
-    per = chunk_tiles(work, rows, a.units, per);
+    // a sequence's last row tile leaves half a chunk empty on average
+    const double some = rows + fmax(a.aim - 0.5 * rows, 1.0);
+    per = chunk_tiles(work, rows, some < a.units ? (int)some : a.units, per);
   }
   int before = 0;
   for (int b0 = 0; b0 < a.c.seqs; b0 += 64) {

@@ -186,11 +186,11 @@ struct QueryPiece {
 };
 
 // In its loop bound by HBM and the vector pipes alike: dim 128, bf16, 131071 keys of
-// 8 key heads for one token 33 us (143 MB: 4.3 TB/s, 7 in the loop; 8 us pass before
-// it, in three misses one behind the other), 40 sequences of up to 12000 keys 63 us
+// 8 key heads for one token 32 us (143 MB: 4.4 TB/s, 7 in the loop; 8 us pass before
+// it, in three misses one behind the other), 40 sequences of up to 12000 keys 62 us
 // (281 MB).  By the vector pipes alone with one query head a key head (fp32, 12 of
-// up to 4095 keys, 32 heads: 41 us, 122 MB) and with dim 64 (fp16, 24 x 5 rows x 4 in a
-// window of 4096: 42 us).  A wave issues 250 vector operations a tile for 16 rows and
+// up to 4095 keys, 32 heads: 38 us, 122 MB) and with dim 64 (fp16, 24 x 5 rows x 4 in a
+// window of 4096: 43 us).  A wave issues 250 vector operations a tile for 16 rows and
 // 8 products a part.
 template <int DIM, typename T, int PARTS, bool SMALL, int QT>
 __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3) void kv_attention16(AttnView a) {
@@ -557,10 +557,10 @@ constexpr int kWholeTiles16 = 24;
 // Chunks over all key heads that a launch aims at: a little under the 768
 // workgroups that are resident at once (three on a CU), because a unit's start (its
 // search, its query, the first tile) takes 8 us and all units' starts then pass
-// together.  131071 keys: 37 us at 704, 45 at 1408; 40 sequences: 68 and 72 (when a
-// start was 2 us longer).
-constexpr int kUnits16 = 704;
-constexpr int kUnits32 = 480;            // of 512: two tiles of rows, dim 128
+// together.  Call times at 672, 744, 768: 131071 keys 42, 41, 40 us (48 at 1450); 40
+// sequences 77, 70, 71; 12 of 32 key heads 43, 42, 46.
+constexpr int kUnits16 = 744;
+constexpr int kUnits32 = 496;            // of 512: two tiles of rows, dim 128
 // The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
 // have that many on average (a tile of keys is unpacked once for all of its rows).
 // 2047 and 1774 rows x 4 behind 9001 and 4830 keys, dim 128: 616 us in tiles of 128
@@ -583,6 +583,7 @@ constexpr int kUncut = INT32_MAX;
 // tiles, and chunks on top), and whether there can be chunks to join.
 struct Plan {
   int units16, units_rows, waves;
+  int aim16;                             // units that the first is to use, as a rule
   int tall;                              // the first's tiles are of 16 << tall rows
   bool join16, join_rows;
   size_t part16, part_rows;              // floats of partial results
@@ -596,7 +597,8 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
     p.tall = few && n > 16 * some && dim < 256;
     const int64_t bm = 16 << p.tall;
     const int64_t tiles = std::min((n + (bm - 1) * some) / bm, few ? n : some * ((kFewRows + 15) / 16));
-    const int64_t more = std::max<int64_t>((p.tall && dim == 128 ? kUnits32 : kUnits16) / heads - tiles / 2, 1);
+    p.aim16 = (p.tall && dim == 128 ? kUnits32 : kUnits16) / heads;
+    const int64_t more = std::max<int64_t>(p.aim16 - tiles / 2, 1);
     p.units16 = (int)(tiles + more);
     p.join16 = more > 1;
   }
@@ -635,6 +637,7 @@ kronq_status launch_few(AttnView a, const Plan& p, bool both, float* ws, hipStre
   a.shape.least = 1;
   a.shape.most = both ? kFewRows : INT32_MAX;
   a.units = p.units16;
+  a.aim = p.aim16;
   a.min_tiles = !p.join16 ? kUncut : room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
   a.part = ws;
   a.stat = ws + (size_t)p.units16 * a.c.heads * (16 * QT) * DIM;
@@ -661,7 +664,7 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
   if (p.units_rows) {
     a.shape.least = both ? kFewRows + 1 : 1;
     a.shape.most = INT32_MAX;
-    a.units = p.units_rows;
+    a.units = a.aim = p.units_rows;
     a.min_tiles = p.join_rows ? kMinTilesRows : kUncut;
     a.part = ws + p.part16;
     a.stat = a.part + (size_t)p.units_rows * a.c.heads * 32 * p.waves * DIM;
