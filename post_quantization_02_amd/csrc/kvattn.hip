@@ -568,7 +568,11 @@ constexpr int kUnits32 = 496;            // of 512: two tiles of rows, dim 128
 constexpr int kTallRows = 256;
 constexpr int kMinTilesRows = 4;         // 256 keys
 // Workgroups resident at once: two of four waves on a CU, or one of eight.  Row
-// tiles alone are enough at twice that; fewer are cut along the keys.
+// tiles that fill half of them or less are cut along the keys to fill 7/8 (one
+// round), fewer than all to twice that (two rounds of smaller ones).  One sequence of
+// up to 8000 keys, rows x 4, dim 128, bf16: 256 rows 74 us in one round, 91 in two;
+// 1024 rows 188 and 231 (fp32: 314 and 397); two such sequences, more than half: 319
+// and 287.
 constexpr int kResident = 512, kResidentTall = 256;
 
 // The join gives each row's head as many groups of lanes as make this many
@@ -583,7 +587,7 @@ constexpr int kUncut = INT32_MAX;
 // tiles, and chunks on top), and whether there can be chunks to join.
 struct Plan {
   int units16, units_rows, waves;
-  int aim16;                             // units that the first is to use, as a rule
+  int aim16, aim_rows;                   // units that are to be used, as a rule
   int tall;                              // the first's tiles are of 16 << tall rows
   bool join16, join_rows;
   size_t part16, part_rows;              // floats of partial results
@@ -604,10 +608,12 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
   }
   if (!few) {
     p.waves = dim < 256 && n >= kTallRows * some ? 8 : 4;
-    const int64_t bm = 32 * p.waves, aim = 2 * (p.waves == 8 ? kResidentTall : kResident) / heads;
+    const int64_t bm = 32 * p.waves, resident = (p.waves == 8 ? kResidentTall : kResident) / heads;
     const int64_t tiles = (n + (bm - 1) * std::min<int64_t>(some, n / (kFewRows + 1))) / bm;
-    const int64_t more = 2 * tiles < aim ? aim - tiles : 1;
+    const bool half = 2 * tiles <= resident;
+    const int64_t more = std::max(half ? resident * 7 / 8 - tiles / 2 : tiles < resident ? 2 * resident - tiles : 1, int64_t(1));
     p.units_rows = (int)(tiles + more);
+    p.aim_rows = half ? (int)(resident * 7 / 8) : p.units_rows;
     p.join_rows = more > 1;
   }
   if (p.join16) p.part16 = (size_t)p.units16 * heads * (16 << p.tall) * (dim + 2);
@@ -664,7 +670,8 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
   if (p.units_rows) {
     a.shape.least = both ? kFewRows + 1 : 1;
     a.shape.most = INT32_MAX;
-    a.units = a.aim = p.units_rows;
+    a.units = p.units_rows;
+    a.aim = p.aim_rows;
     a.min_tiles = p.join_rows ? kMinTilesRows : kUncut;
     a.part = ws + p.part16;
     a.stat = a.part + (size_t)p.units_rows * a.c.heads * 32 * p.waves * DIM;
