@@ -492,7 +492,9 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
  *   grid  : pages x heads x page 32-bit words, keys and values each.  A word
  *           with its low four bits cleared is the fp32 scale s; those four bits
  *           are the zero point z.  Code c stands for s (c - z), which is exact
- *           in fp32 (s has 20 significant bits).
+ *           in fp32 (s has 20 significant bits).  kronq_kv_append writes s > 0
+ *           or NaN; a word of the caller's own may have s below 0, too, or
+ *           infinite (what the rows that see it then give is not defined).
  *   A page's heads x page x dim/2 bytes (heads x page words) are contiguous;
  *   the distance between pages is *_stride (bytes for codes, words for grids),
  *   below 2^32, so the pages of several layers may share one buffer.

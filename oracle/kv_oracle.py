@@ -135,7 +135,7 @@ def attention(cache, batch, q: np.ndarray, scale: float, window=0, sinks=0, rope
     """(out, lse, size), lists of rows (None for a row of no sequence) but for
     lse: out (q_heads, dim), NaN where it is not defined, and what error bounds
     are made of, size (q_heads, dim + 2): sum_j w_j |v_j| for each value, then
-    max_j scale sum |q| |k_j| and max_j w_j s_j, weights w of sum 1."""
+    max_j scale sum |q| |k_j| and max_j w_j |s_j|, weights w of sum 1."""
     rows, qheads, dim = q.shape
     heads = cache["k_codes"].shape[1]
     share = qheads // heads
@@ -177,5 +177,5 @@ def attention(cache, batch, q: np.ndarray, scale: float, window=0, sinks=0, rope
                 lse[r, h] = top + math.log(w.sum())
                 size[r][h, :dim] = (w @ np.abs(vh)) / w.sum()
                 size[r][h, dim] = (scale * (np.abs(kh) @ np.abs(x))).max()
-                size[r][h, dim + 1] = (w * S[:, h // share]).max() / w.sum()
+                size[r][h, dim + 1] = (w * np.abs(S[:, h // share])).max() / w.sum()
     return out, lse, size

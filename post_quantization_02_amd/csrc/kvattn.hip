@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
         const float p = __builtin_amdgcn_exp2f(fmaf(s[x], f[t], -base));
         sum += p;
         y[x] = p * vs[x];
-        ytop = fmaxf(ytop, y[x]);
+        ytop = fmaxf(ytop, fabsf(y[x]));              // a grid's scale may be below 0
       }
       l[t] += sum * ldexpf(1.0f, ue);
       if (__any(ytop > ldexpf(1.0f, min(kTop + e[t] - ue, 127)))) {

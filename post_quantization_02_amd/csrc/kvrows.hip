@@ -514,7 +514,7 @@ void kv_attention_rows(AttnView a) {
             sum += p;
             const bool seen = sc[s][x] != -INFINITY;  // not seen: whatever scale is there
             sc[s][x] = seen ? p * tile.vs[32 * s + 16 * (x >> 3) + 8 * h + (x & 7)] : 0.0f;
-            ytop = fmaxf(ytop, sc[s][x]);
+            ytop = fmaxf(ytop, fabsf(sc[s][x]));      // a grid's scale may be below 0
           }
         if (__any(ytop > ldexpf(1.0f, min(kTop + e - ue, 127)))) {
           ytop = fmaxf(ytop, __shfl_xor(ytop, 32));
