@@ -512,7 +512,8 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
  *           columns * page is at most 2^30 (KRONQ_EUNSUPPORTED otherwise).
  *   Entries of columns that no visible position needs are not followed and may
  *   hold anything.  A row outside cu[0] .. cu[seqs] - 1 (padding) belongs to no
- *   sequence: it is not read, and its outputs are left as they were.
+ *   sequence: it is not read, and its outputs are left as they were.  cu may
+ *   name more rows than a call has: those that it has keep their positions.
  *   Nothing outside the caller's buffers is touched whatever these arrays
  *   hold: a position with no column, or a page outside 0 .. pages - 1, is not
  *   written by kronq_kv_append, reads back as NaN, and makes the attention of

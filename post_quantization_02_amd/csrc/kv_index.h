@@ -71,7 +71,7 @@ __host__ __device__ inline Place place_of(const KvView& c, int seq, int row, int
 
 struct AttnShape { int share, window, sinks, least, most; };   // window 0: none
 
-struct Seq { int row0, len, ctx, tiles, qtiles; };
+struct Seq { int row0, len, ctx, tiles, qtiles; };   // ctx: the position behind its last row
 
 __host__ __device__ inline int tiles_of(int n, int kt) { return n / kt + (n % kt != 0); }
 
@@ -113,7 +113,10 @@ __host__ __device__ inline Seq seq_at(const KvView& c, const AttnShape& a, int b
   if (n < a.least || n > a.most) return s;
   s.row0 = lo;
   s.len = hi - lo;
-  s.ctx = c.ctx[b] > 0 ? c.ctx[b] : 0;
+  // where its last row of this call stands, which a batch that names more rows
+  // than there are (cu beyond them) does not end with
+  const int64_t end = (int64_t)c.ctx[b] - ((int64_t)c.cu[b + 1] - hi);
+  s.ctx = end > 0 ? (int)end : 0;
   const Span all = span_between(c, a, s.ctx > s.len ? s.ctx - s.len : 0, s.ctx - 1, kt);
   s.tiles = all.sink + all.upto - all.from;
   s.qtiles = (int)((n + bm - 1) / bm);

@@ -3,7 +3,8 @@ what the calls allow, against the 64-bit oracle."""
 import numpy as np
 import pytest
 
-from kv_helpers import Case
+import post_quantization_02_amd as kq
+from kv_helpers import DEV, Case, check_attention
 from test_gpu_kv import TYPES, attend, ids
 
 pytestmark = pytest.mark.gpu
@@ -20,3 +21,18 @@ def test_negative_scales(dtype, new, which):
         w = c.cache[nm + "_grid"]
         w[rng.random(w.shape) < (1.0 if which == "all" else 0.5)] |= np.uint32(1 << 31)
     attend(c)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("lengths,rows", [([(100, 40), (90, 30)], 55), ([(300, 150), (260, 120)], 200),
+                                          ([(900, 500), (50, 3)], 77), ([(5, 9), (20, 20)], 8)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_rows_of_a_batch_cut_short_keep_their_positions(dtype, lengths, rows, window):
+    # cu names more rows than the call has: those that it has are what they are in the whole call
+    c = Case(lengths, heads=2, share=2, dim=64, dtype=dtype, rot=64, seed=rows)
+    cache, batch, rope = c.dev(kq)
+    q = c.q.to(DEV)
+    got, lse = kq.kronq_kv_attention(q, cache, batch, rope=rope, window=window, sinks=2, want_lse=True)
+    got[:rows], lse[:rows] = kq.kronq_kv_attention(q[:rows], cache, batch, rope=rope, window=window, sinks=2,
+                                                   want_lse=True)
+    check_attention(c, got, lse, None, window, 2)

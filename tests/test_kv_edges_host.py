@@ -1,0 +1,38 @@
+"""4-bit paged key/value cache without a GPU: batches at the edge of what the
+calls allow, through the kernels' index functions (built for the host)."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "post_quantization_02_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def index(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("kv") / "edges.so")
+    subprocess.run(["/opt/rocm/bin/hipcc", "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-fPIC", "-shared",
+                    "-ftrapv", "-I", CSRC, os.path.join(HERE, "kv_edges_host.cpp"), "-o", out], check=True)
+    return ctypes.CDLL(out)
+
+
+def ptr(a):
+    return a.ctypes.data_as(ctypes.c_void_p)
+
+
+def test_attention_and_append_place_a_row_alike(index):
+    rng = np.random.default_rng(2)
+    big = 2 ** 31 - 1
+    for n in range(400):
+        seqs = int(rng.integers(1, 6))
+        ctx = rng.integers(-5, 90, seqs).astype(np.int32)
+        cu = np.concatenate([[rng.integers(-20, 3)], rng.integers(0, 30, seqs)]).cumsum().astype(np.int32)
+        if n % 4 == 0:
+            ctx[rng.integers(seqs)] = rng.choice([big, -big - 1])
+            cu[-1] = big
+        # as many rows as cu names, fewer, and more
+        rows = max(0, min(int(cu[-1]), 150) + int(rng.integers(-40, 10)))
+        assert index.places_differ(ptr(ctx), ptr(cu), seqs, rows) == 0, (ctx, cu, rows)
