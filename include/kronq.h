@@ -503,6 +503,7 @@ kronq_status kronq_decode_matvec_noalloc(const uint8_t* codes, int64_t m, int64_
  * 16 bytes.
  *
  * Batch (device arrays, read by the kernels when they run):
+ *   seqs is at most 2^20 (KRONQ_EUNSUPPORTED otherwise).
  *   cu    : int32[seqs + 1], not decreasing: rows cu[i] .. cu[i + 1] - 1 of the
  *           calls' q, k, v and outputs belong to sequence i (none is allowed).
  *   ctx   : int32[seqs]: tokens of sequence i in the cache, its rows of this
@@ -599,7 +600,7 @@ kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t d
  *           they must not overlap each other, the cache or ws.
  * lse     : rows x q_heads fp32, contiguous, or NULL.
  * q_heads : a multiple of the cache's heads; at most 2^22 rows and 2^26 rows x
- *           q_heads, at most 2^20 sequences.
+ *           q_heads, at most 2^14 sequences (KRONQ_EUNSUPPORTED otherwise).
  * scale   : > 0 and finite, 1 / sqrt(dim) as a rule.
  * Scores, the running maximum and sum and the outputs are fp32.  Queries and
  * weights enter the matrix cores as fp16 scaled by powers of two: for KRONQ_F32

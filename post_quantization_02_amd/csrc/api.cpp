@@ -185,6 +185,11 @@ static kronq_status kv_view(const char* fn, const kronq_kv_cache* c, const kronq
   return KRONQ_OK;
 }
 
+// Sequences of an attention call: each unit of work looks through all of them, so
+// time grows with their square (one head of one token each of up to 60 keys: 1024
+// sequences 26 us, 4096 230 us, 16384 3.0 ms; 2^20 would be minutes for a few heads).
+static constexpr int64_t kAttnSeqs = 1 << 14;
+
 static kronq_status kv_rope(const char* fn, const kronq_rope* r, int32_t dim, RopeView* out) {
   *out = RopeView{};
   if (!r) return KRONQ_OK;
@@ -641,6 +646,7 @@ kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t d
 size_t kronq_kv_attention_ws(int64_t rows, int64_t seqs, int32_t q_heads, int32_t heads, int32_t dim) {
   if (rows < 1 || seqs < 1 || heads < 1 || q_heads < heads || q_heads % heads || dim < 1) return 0;
   if (rows > (int64_t(1) << 22) || q_heads > 65535 || rows * q_heads > (int64_t(1) << 26) || dim > 256) return 0;
+  if (seqs > kAttnSeqs) return 0;
   return kv_attention_ws_bytes(rows, seqs, q_heads, heads, dim);
 }
 
@@ -656,6 +662,8 @@ kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t row
   kronq_status st = kv_view(fn, cache, batch, rows, &c);
   if (st) return st;
   if ((st = kv_rows(fn, dtype, rows, q_heads))) return st;
+  if (batch->seqs > kAttnSeqs)
+    return fail(KRONQ_EUNSUPPORTED, "%s: %d sequences (at most 2^14)", fn, (int)batch->seqs);
   if (q_heads % cache->heads)
     return fail(KRONQ_EINVAL, "%s: %d query heads on %d key heads", fn, (int)q_heads, (int)cache->heads);
   if ((st = kv_rope(fn, rope, cache->dim, &r))) return st;

@@ -2,6 +2,7 @@
 what the calls allow, against the 64-bit oracle."""
 import numpy as np
 import pytest
+import torch
 
 import post_quantization_02_amd as kq
 from kv_helpers import DEV, Case, check_attention
@@ -36,3 +37,10 @@ def test_rows_of_a_batch_cut_short_keep_their_positions(dtype, lengths, rows, wi
     got[:rows], lse[:rows] = kq.kronq_kv_attention(q[:rows], cache, batch, rope=rope, window=window, sinks=2,
                                                    want_lse=True)
     check_attention(c, got, lse, None, window, 2)
+
+
+def test_as_many_sequences_as_a_call_takes():
+    rng = np.random.default_rng(4)
+    lengths = [(int(rng.integers(0, 4)), 1) for _ in range(1 << 14)]
+    c = Case(lengths, heads=1, share=1, dim=64, dtype=torch.bfloat16)
+    attend(c)

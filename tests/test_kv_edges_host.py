@@ -7,6 +7,9 @@ import subprocess
 import numpy as np
 import pytest
 
+import post_quantization_02_amd as kq
+from test_kv_host import Raw
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "post_quantization_02_amd", "csrc")
 
@@ -36,3 +39,13 @@ def test_attention_and_append_place_a_row_alike(index):
         # as many rows as cu names, fewer, and more
         rows = max(0, min(int(cu[-1]), 150) + int(rng.integers(-40, 10)))
         assert index.places_differ(ptr(ctx), ptr(cu), seqs, rows) == 0, (ctx, cu, rows)
+
+
+def test_attention_refuses_more_sequences_than_it_can_look_through():
+    # each unit of work goes through all sequences: a call of 2^20 would hold the GPU for minutes
+    for seqs in ((1 << 14) + 1, 1 << 20):
+        a = Raw()
+        a.batch.seqs, a.rows = seqs, seqs
+        assert a.attention() == kq.KRONQ_EUNSUPPORTED and b"2^14" in kq.load().kronq_last_error()
+        assert kq.load().kronq_kv_attention_ws(seqs, seqs, 8, 8, 128) == 0
+    assert kq.load().kronq_kv_attention_ws(1 << 14, 1 << 14, 8, 8, 128) > 0
