@@ -837,6 +837,8 @@ _AS_IT_IS = contextlib.nullcontext()
 def _on_stream(device, stream):
     """(handle of the stream to run on, a context in which the device is current
     and torch allocates for that stream)."""
+    if getattr(stream, "device", device) != device:    # default streams of all devices have one handle
+        raise ValueError("stream must be one of %s" % device)
     # the current stream's handle without an object for it: calls for one token
     # cost as much as their parts in Python do
     cur = torch._C._cuda_getCurrentRawStream(device.index)

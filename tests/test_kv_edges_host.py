@@ -6,6 +6,7 @@ import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 import post_quantization_02_amd as kq
 from test_kv_host import Raw
@@ -49,3 +50,12 @@ def test_attention_refuses_more_sequences_than_it_can_look_through():
         assert a.attention() == kq.KRONQ_EUNSUPPORTED and b"2^14" in kq.load().kronq_last_error()
         assert kq.load().kronq_kv_attention_ws(seqs, seqs, 8, 8, 128) == 0
     assert kq.load().kronq_kv_attention_ws(1 << 14, 1 << 14, 8, 8, 128) > 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    # default streams of all devices have handle 0: the call would run beside the caller's work, not after it
+    class Stream:
+        device, cuda_stream = torch.device("cuda:1"), 0
+
+    with pytest.raises(ValueError, match="stream"):
+        kq._on_stream(torch.device("cuda:0"), Stream())
