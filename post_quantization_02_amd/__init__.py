@@ -757,15 +757,15 @@ class KVCache:
             _dev(t, nm, dt)
             if tuple(t.shape) != shape:
                 raise ValueError("%s must have shape %s" % (nm, shape))
-            inner = tuple(math.prod(shape[i + 1:]) for i in range(1, len(shape)))
-            if t.stride()[1:] != inner:
+            # a dimension of one entry has no distance to speak of
+            if any(n > 1 and t.stride(i) != math.prod(shape[i + 1:]) for i, n in enumerate(shape) if i):
                 raise ValueError("%s: a page must be contiguous" % nm)
         _same_device(self.device, v_codes, k_grid, v_grid)
         self.k_codes, self.v_codes, self.k_grid, self.v_grid = k_codes, v_codes, k_grid, v_grid
         self.pages, self.heads, self.page, self.dim = pages, heads, page, 2 * half
         self._c = _Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_grid.data_ptr(), v_grid.data_ptr(),
-                         k_codes.stride(0), v_codes.stride(0), k_grid.stride(0), v_grid.stride(0), pages,
-                         heads, page, 2 * half)
+                         *(t.stride(0) if pages > 1 else t[0].numel() for t in (k_codes, v_codes, k_grid, v_grid)),
+                         pages, heads, page, 2 * half)
 
     @classmethod
     def empty(cls, pages: int, heads: int, page: int, dim: int, device="cuda:0") -> "KVCache":

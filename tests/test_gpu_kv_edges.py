@@ -44,3 +44,16 @@ def test_as_many_sequences_as_a_call_takes():
     lengths = [(int(rng.integers(0, 4)), 1) for _ in range(1 << 14)]
     c = Case(lengths, heads=1, share=1, dim=64, dtype=torch.bfloat16)
     attend(c)
+
+
+def test_dimensions_of_one_entry_have_any_stride():
+    c = Case([(14, 3)], heads=1, share=2, dim=64, dtype=torch.float16, rot=64)
+    own, batch, rope = c.dev(kq)
+    head = [t.as_strided(t.shape, (t.stride(0), 7) + t.stride()[2:]) for t in (own.k_codes, own.v_codes, own.k_grid, own.v_grid)]
+    q = c.q.to(DEV)
+    out = kq.kronq_kv_attention(q, kq.KVCache(*head), batch, rope=rope)
+    check_attention(c, out, None)
+    page = int(c.table[0, 0])
+    one = kq.KVCache(*(t[page:page + 1].as_strided((1,) + t.shape[1:], (1,) + t.stride()[1:]) for t in head))
+    at_0 = kq.KVBatch(torch.zeros_like(batch.table), batch.ctx, batch.cu)
+    assert torch.equal(kq.kronq_kv_attention(q, one, at_0, rope=rope), out)
