@@ -133,6 +133,25 @@ __host__ __device__ inline int chunk_tiles(double work, double rows, int units, 
   return per > least ? per : least;
 }
 
+// How a launch is cut: its units, how many of them are to be used as a rule
+// (`aim`), and how many at least are left for chunks (`spare`) where the row tiles
+// alone are more than that, so that one long sequence among many is cut still.
+struct Cut { int units, aim, spare; };
+
+// Units to be used: a sequence's last row tile leaves half a chunk empty on average.
+__host__ __device__ inline int used_units(const Cut& c, double rows) {
+  const double some = rows + fmax(c.aim - 0.5 * rows, (double)c.spare);
+  return some < c.units ? (int)some : c.units;
+}
+
+// Units of sequences that are cut in chunks, at most, which have a place for their
+// partial results: the sum of qtiles * (chunks - 1) is below work / per <= used -
+// rows <= max(aim, spare), whatever the batch holds, and chunks <= 2 (chunks - 1).
+__host__ __device__ inline int places_of(const Cut& c) {
+  const int64_t n = 2 * (int64_t)(c.aim > c.spare ? c.aim : c.spare);
+  return n < c.units ? (int)n : c.units;
+}
+
 __host__ __device__ inline int chunks_of(const Seq& s, int per) {
   const int n = tiles_of(s.tiles, per);
   return n > 1 ? n : 1;
@@ -141,6 +160,7 @@ __host__ __device__ inline int chunks_of(const Seq& s, int per) {
 struct Unit {
   int b, qtile, chunk, chunks, base;   // base: the sequence's first unit
   int row0, len, ctx;
+  int place;               // of its chunk's partial results, where chunks > 1
 };
 
 __host__ __device__ inline Span span_of(const KvView& c, const AttnShape& a, const Unit& u, int bm, int kt, int& pos_lo,

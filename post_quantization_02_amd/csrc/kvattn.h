@@ -9,6 +9,9 @@ namespace kronq {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kNan = __builtin_nanf("");
 
+// What kv_attention_cut leaves for a kernel and its join.
+struct CutTold { int per, any; };   // tiles of a chunk, whether any sequence is cut
+
 struct AttnView {
   KvView c;
   HeadsView q, out;
@@ -17,11 +20,12 @@ struct AttnView {
   int qheads;              // query heads
   float scale;
   AttnShape shape;
-  int units;               // work units of a key head
-  int aim;                 // of them to be used, as a rule
+  Cut cut;                 // work units of a key head
   int min_tiles;           // tiles of a chunk at least
-  float* part;             // [units][heads][BM][dim] unnormalized outputs
-  float* stat;             // [units][heads][BM][2]   maximum (of f S), sum
+  const CutTold* told;     // how long chunks are, where that was worked out before
+  int places;              // of partial results, for each key head
+  float* part;             // [places][heads][BM][dim] unnormalized outputs
+  float* stat;             // [places][heads][BM][2]   maximum (of f S), sum
 };
 
 // ---- work units
@@ -29,7 +33,7 @@ struct AttnView {
 // The host knows neither the lengths nor the contexts, only how many rows and
 // sequences there are, so the launch has a fixed number of units and the kernels
 // cut the keys.  Every wave works its unit out from cu and ctx by itself, 64
-// sequences at a time.
+// sequences at a time; how long a chunk is, too, unless kv_attention_cut did.
 
 // Data-parallel moves within the wave (rows of 16 lanes, then their last lanes):
 // they wait for nothing, where exchanges through LDS cost 100 cycles a step.
@@ -62,6 +66,16 @@ __device__ inline double wave_sum(double x) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+__device__ inline int wave_max(int x) {               // x >= 0
+  x = max(x, moved<0x111, 0xF>(x));
+  x = max(x, moved<0x112, 0xF>(x));
+  x = max(x, moved<0x114, 0xF>(x));
+  x = max(x, moved<0x118, 0xF>(x));
+  x = max(x, moved<0x142, 0xA>(x));
+  x = max(x, moved<0x143, 0xC>(x));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
 // The unit `want`; by_row: the sequence of row `want`, its first unit.  false:
 // there is none.
 template <int BM, int KT>
@@ -70,26 +84,29 @@ __device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit&
   Seq s = seq_at(a.c, a.shape, lane, BM, KT);
   int per = a.min_tiles;
   if (room_of(a.c) > (int64_t)per * KT) {             // else nothing is cut
-    // sums of integers below 2^53: exact
-    double rows = s.qtiles, work = (double)s.qtiles * s.tiles;
-    for (int b0 = 64; b0 < a.c.seqs; b0 += 64) {
-      s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
-      rows += s.qtiles;
-      work += (double)s.qtiles * s.tiles;
+    if (a.told) {
+      per = a.told->per;
+    } else {                                          // at most 64 sequences
+      // sums of integers below 2^53: exact
+      double rows = s.qtiles, work = (double)s.qtiles * s.tiles;
+      if (a.c.seqs > 1) {                             // one sequence is lane 0's
+        rows = wave_sum(rows);
+        work = wave_sum(work);
+      }
+      per = chunk_tiles(work, rows, used_units(a.cut, rows), per);
     }
-    if (a.c.seqs > 1) {                               // one sequence is lane 0's
-      rows = wave_sum(rows);
-      work = wave_sum(work);
-    }
-    // a sequence's last row tile leaves half a chunk empty on average
-    const double some = rows + fmax(a.aim - 0.5 * rows, 1.0);
-    per = chunk_tiles(work, rows, some < a.units ? (int)some : a.units, per);
   }
-  int before = 0;
+  int before = 0, places = 0;
   for (int b0 = 0; b0 < a.c.seqs; b0 += 64) {
     if (a.c.seqs > 64) s = seq_at(a.c, a.shape, b0 + lane, BM, KT);
     const int chunks = chunks_of(s, per);
     const int n = s.qtiles * chunks, upto = before + wave_scan(n);
+    int place = 0;                                    // of the sequence's first unit
+    if (__any(chunks > 1)) {
+      const int k = chunks > 1 ? n : 0, all = places + wave_scan(k);
+      place = all - k;
+      places = __builtin_amdgcn_readlane(all, 63);
+    }
     const bool mine = by_row ? (want >= s.row0 && want < s.row0 + s.len) : (want < upto && want >= upto - n);
     const uint64_t hit = __ballot(mine);
     if (hit) {
@@ -103,6 +120,7 @@ __device__ inline bool find_unit(const AttnView& a, int want, bool by_row, Unit&
       const int rest = by_row ? 0 : want - u.base;
       u.qtile = rest / u.chunks;
       u.chunk = rest % u.chunks;
+      u.place = u.chunks > 1 ? __builtin_amdgcn_readlane(place, l) + rest : 0;
       return true;
     }
     before = __builtin_amdgcn_readlane(upto, 63);

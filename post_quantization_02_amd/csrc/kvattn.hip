@@ -459,8 +459,8 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
         store8(static_cast<T*>(a.out.data) + (int64_t)(u.row0 + tok) * a.out.row + (int64_t)qh * a.out.head + d, x);
         if (a.lse && d == 0)
           a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = ll == 0 ? -INFINITY : (mm + log2f(ll)) * kLn2;
-      } else {
-        const int64_t at = ((int64_t)blockIdx.x * a.c.heads + head) * BM + 16 * t + row;
+      } else if (u.place < a.places) {
+        const int64_t at = ((int64_t)u.place * a.c.heads + head) * BM + 16 * t + row;
         store8(a.part + at * DIM + d, x);
         if (d == 0) {
           a.stat[2 * at] = mm;
@@ -480,6 +480,7 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, in
   constexpr int LANES = DIM / 8, GROUPS = 256 / LANES;
   __shared__ float lds_x[GROUPS][DIM + 4];
   __shared__ float lds_l[GROUPS];
+  if (a.told && !a.told->any) return;
   Unit u;
   const int share = a.shape.share;
   int row = blockIdx.x;
@@ -489,14 +490,13 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, in
     row = s.row0 + blockIdx.x % per;
   }
   if (!find_unit<BM, KT>(a, row, true, u) || u.chunks == 1) return;
+  if (u.place + ((int64_t)u.len * share - 1) / BM * u.chunks + u.chunks > a.places) return;
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, d = lane * 8;
   const int slot = group & (slots - 1), qh = (int)blockIdx.y * (GROUPS / slots) + group / slots;
   const bool in = qh < a.qheads;
   const int head = qh / share, r = (row - u.row0) * share + qh % share;
-  // cannot be in a batch whose rows are each one sequence's
-  if (u.base < 0 || u.base + ((int64_t)u.len * share - 1) / BM * u.chunks + u.chunks > a.units) return;
   auto at = [&](int chunk) {
-    return ((int64_t)(u.base + r / BM * u.chunks + chunk) * a.c.heads + head) * BM + r % BM;
+    return ((int64_t)(u.place + r / BM * u.chunks + chunk) * a.c.heads + head) * BM + r % BM;
   };
   const int width = min(slots * LANES, 64);          // lanes of a wave that share the head
   float m = -INFINITY;
@@ -534,6 +534,42 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnView a, int per, in
   for (int k = 0; k < 8; ++k) x[k] = l == 0 ? 0.0f : x[k] * inv;
   store8(static_cast<T*>(a.out.data) + (int64_t)row * a.out.row + (int64_t)qh * a.out.head + d, x);
   if (a.lse && lane == 0) a.lse[(int64_t)row * a.qheads + qh] = l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// How long the chunks of up to two launches are, where each of their waves adding
+// that up for itself would cost more (more than 64 sequences: 1000 of 200 to 700
+// keys, 8 key heads, 260 us with this kernel, 369 without), or a join that finds
+// nothing (many rows).  A workgroup for each.  Latency: 4 us.
+struct CutAsked {
+  AttnShape shape;
+  Cut cut;
+  int min_tiles, bm, kt;
+  CutTold* told;
+};
+
+__global__ __launch_bounds__(256) void kv_attention_cut(KvView c, CutAsked first, CutAsked second) {
+  __shared__ double sums[2][4];
+  __shared__ int most[4];
+  const CutAsked a = blockIdx.x ? second : first;
+  double rows = 0, work = 0;
+  int longest = 0;
+#pragma unroll 4
+  for (int b = threadIdx.x; b < c.seqs; b += 256) {
+    const Seq s = seq_at(c, a.shape, b, a.bm, a.kt);
+    rows += s.qtiles;                                 // sums of integers below 2^53: exact
+    work += (double)s.qtiles * s.tiles;
+    longest = max(longest, s.tiles);
+  }
+  const int wave = threadIdx.x >> 6;
+  rows = wave_sum(rows);
+  work = wave_sum(work);
+  longest = wave_max(longest);
+  if ((threadIdx.x & 63) == 0) sums[0][wave] = rows, sums[1][wave] = work, most[wave] = longest;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < 4; ++w) rows += sums[0][w], work += sums[1][w], longest = max(longest, most[w]);
+  const int per = chunk_tiles(work, rows, used_units(a.cut, rows), a.min_tiles);
+  *a.told = CutTold{per, longest > per};
 }
 
 // ---- launch
@@ -585,13 +621,24 @@ constexpr int kUncut = INT32_MAX;
 
 // How a call is cut: units of each kernel (0: not launched; a bound of its row
 // tiles, and chunks on top), and whether there can be chunks to join.
+//
 struct Plan {
-  int units16, units_rows, waves;
-  int aim16, aim_rows;                   // units that are to be used, as a rule
+  Cut few, rows;
+  int waves;
   int tall;                              // the first's tiles are of 16 << tall rows
   bool join16, join_rows;
-  size_t part16, part_rows;              // floats of partial results
+  bool told16, told_rows;                // kv_attention_cut runs before them
+  size_t told, part16, part_rows;        // floats: what it leaves, partial results
 };
+
+// Where row tiles alone fill the chip, a kSpare-th part of it is left for chunks all
+// the same, and the join is launched: one sequence may be longer than all others
+// together.  131071 keys among 255 sequences of 200 to 700, 8 key heads x 4: 1047 us
+// whole, 134 cut; 64 rows behind 131071 keys among 40 prompts of 512: 5035 and 946;
+// 200 sequences of 1500 to 12000, x 8: 370 and 342.  Where nothing is cut the two
+// launches cost 5 us (200 sequences of 200 to 700 keys: 44 and 49; 8 prompts of 1024:
+// 200 and 206).
+constexpr int kSpare = 2;
 
 Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
   Plan p{};
@@ -601,23 +648,32 @@ Plan plan_of(int64_t rows, int64_t seqs, int share, int heads, int dim) {
     p.tall = few && n > 16 * some && dim < 256;
     const int64_t bm = 16 << p.tall;
     const int64_t tiles = std::min((n + (bm - 1) * some) / bm, few ? n : some * ((kFewRows + 15) / 16));
-    p.aim16 = (p.tall && dim == 128 ? kUnits32 : kUnits16) / heads;
-    const int64_t more = std::max<int64_t>(p.aim16 - tiles / 2, 1);
-    p.units16 = (int)(tiles + more);
+    const int64_t aim = (p.tall && dim == 128 ? kUnits32 : kUnits16) / heads;
+    const int64_t spare = std::max<int64_t>(aim / kSpare, 1), more = std::max(aim - tiles / 2, spare);
+    p.few = Cut{(int)(tiles + more), (int)aim, (int)spare};
     p.join16 = more > 1;
   }
   if (!few) {
     p.waves = dim < 256 && n >= kTallRows * some ? 8 : 4;
     const int64_t bm = 32 * p.waves, resident = (p.waves == 8 ? kResidentTall : kResident) / heads;
     const int64_t tiles = (n + (bm - 1) * std::min<int64_t>(some, n / (kFewRows + 1))) / bm;
-    const bool half = 2 * tiles <= resident;
-    const int64_t more = std::max(half ? resident * 7 / 8 - tiles / 2 : tiles < resident ? 2 * resident - tiles : 1, int64_t(1));
-    p.units_rows = (int)(tiles + more);
-    p.aim_rows = half ? (int)(resident * 7 / 8) : p.units_rows;
-    p.join_rows = more > 1;
+    if (2 * tiles <= resident) {
+      const int64_t more = std::max<int64_t>(resident * 7 / 8 - tiles / 2, 1);
+      p.rows = Cut{(int)(tiles + more), (int)(resident * 7 / 8), 1};
+    } else if (tiles < resident) {
+      p.rows = Cut{(int)(2 * resident), (int)(2 * resident), 1};
+    } else {
+      // tiles of one sequence are equally long but for their own rows
+      const int64_t spare = some > 1 ? std::max<int64_t>(resident / kSpare, 1) : 1;
+      p.rows = Cut{(int)(tiles + spare), (int)(some > 1 ? resident : 0), (int)spare};
+    }
+    p.join_rows = p.rows.units - tiles > 1;
+    p.told_rows = p.join_rows && (seqs > 64 || tiles >= resident);
   }
-  if (p.join16) p.part16 = (size_t)p.units16 * heads * (16 << p.tall) * (dim + 2);
-  if (p.join_rows) p.part_rows = (size_t)p.units_rows * heads * 32 * p.waves * (dim + 2);
+  p.told16 = p.join16 && seqs > 64;
+  if (p.told16 || p.told_rows) p.told = 4;
+  if (p.join16) p.part16 = (size_t)places_of(p.few) * heads * (16 << p.tall) * (dim + 2);
+  if (p.join_rows) p.part_rows = (size_t)places_of(p.rows) * heads * 32 * p.waves * (dim + 2);
   return p;
 }
 
@@ -639,15 +695,8 @@ kronq_status join(const AttnView& a, int64_t per, hipStream_t s) {
 }
 
 template <int DIM, typename T, int PARTS, int QT>
-kronq_status launch_few(AttnView a, const Plan& p, bool both, float* ws, hipStream_t s) {
-  a.shape.least = 1;
-  a.shape.most = both ? kFewRows : INT32_MAX;
-  a.units = p.units16;
-  a.aim = p.aim16;
-  a.min_tiles = !p.join16 ? kUncut : room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16;
-  a.part = ws;
-  a.stat = ws + (size_t)p.units16 * a.c.heads * (16 * QT) * DIM;
-  const dim3 grid((unsigned)a.units, (unsigned)a.c.heads);
+kronq_status launch_few(const AttnView& a, const Plan& p, bool both, hipStream_t s) {
+  const dim3 grid((unsigned)a.cut.units, (unsigned)a.c.heads);
   if (a.c.lgp == 4) hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, true, QT>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((kv_attention16<DIM, T, PARTS, false, QT>), grid, dim3(256), 0, s, a);
   KQ_LAUNCHED("kv_attention16");
@@ -658,28 +707,52 @@ kronq_status launch_few(AttnView a, const Plan& p, bool both, float* ws, hipStre
 template <int DIM, typename T, int PARTS>
 kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s) {
   const Plan p = plan_of(a.c.rows, a.c.seqs, a.shape.share, a.c.heads, DIM);
-  const bool both = p.units16 && p.units_rows;
-  if (p.units16) {
+  const bool both = p.few.units && p.rows.units;
+  CutTold* told = reinterpret_cast<CutTold*>(ws);
+  AttnView few = a, rows = a;
+  int asked = 0;
+  CutAsked ask[2] = {};
+  // a kernel's part of the workspace, and what is asked for it beforehand
+  auto ready = [&](AttnView& v, const Cut& cut, bool joined, bool ahead, int min_tiles, int bm, int kt, float* part) {
+    v.cut = cut;
+    v.min_tiles = joined ? min_tiles : kUncut;
+    v.places = joined ? places_of(cut) : 0;
+    v.part = part;
+    v.stat = part + (size_t)v.places * a.c.heads * bm * DIM;
+    if (!ahead || room_of(a.c) <= (int64_t)v.min_tiles * kt) return;
+    v.told = told + asked;
+    ask[asked] = CutAsked{v.shape, cut, v.min_tiles, bm, kt, told + asked};
+    ++asked;
+  };
+  if (p.few.units) {
+    few.shape.least = 1;
+    few.shape.most = both ? kFewRows : INT32_MAX;
+    ready(few, p.few, p.join16, p.told16, room_of(a.c) <= kWholeTiles16 * 32 ? kWholeTiles16 : kMinTiles16, 16 << p.tall,
+          32, ws + p.told);
+  }
+  if (p.rows.units) {
+    rows.shape.least = both ? kFewRows + 1 : 1;
+    rows.shape.most = INT32_MAX;
+    ready(rows, p.rows, p.join_rows, p.told_rows, kMinTilesRows, 32 * p.waves, 64, ws + p.told + p.part16);
+  }
+  if (asked) {
+    hipLaunchKernelGGL(kv_attention_cut, dim3((unsigned)asked), dim3(256), 0, s, a.c, ask[0], ask[1]);
+    KQ_LAUNCHED("kv_attention_cut");
+  }
+  if (p.few.units) {
     kronq_status st;
     if constexpr (DIM < 256)
-      st = p.tall ? launch_few<DIM, T, PARTS, 2>(a, p, both, ws, s) : launch_few<DIM, T, PARTS, 1>(a, p, both, ws, s);
+      st = p.tall ? launch_few<DIM, T, PARTS, 2>(few, p, both, s) : launch_few<DIM, T, PARTS, 1>(few, p, both, s);
     else
-      st = launch_few<DIM, T, PARTS, 1>(a, p, both, ws, s);
+      st = launch_few<DIM, T, PARTS, 1>(few, p, both, s);
     if (st) return st;
   }
-  if (p.units_rows) {
-    a.shape.least = both ? kFewRows + 1 : 1;
-    a.shape.most = INT32_MAX;
-    a.units = p.units_rows;
-    a.aim = p.aim_rows;
-    a.min_tiles = p.join_rows ? kMinTilesRows : kUncut;
-    a.part = ws + p.part16;
-    a.stat = a.part + (size_t)p.units_rows * a.c.heads * 32 * p.waves * DIM;
-    const kronq_status st = kv_rows_launch(a, dim, dtype, p.waves, s);
+  if (p.rows.units) {
+    const kronq_status st = kv_rows_launch(rows, dim, dtype, p.waves, s);
     if (st || !p.join_rows) return st;
     if constexpr (DIM < 256)
-      if (p.waves == 8) return join<DIM, 256, 64, T>(a, 0, s);
-    return join<DIM, 128, 64, T>(a, 0, s);
+      if (p.waves == 8) return join<DIM, 256, 64, T>(rows, 0, s);
+    return join<DIM, 128, 64, T>(rows, 0, s);
   }
   return KRONQ_OK;
 }
@@ -695,7 +768,7 @@ kronq_status launch_dim(const AttnView& a, int32_t dtype, float* ws, hipStream_t
 
 size_t kv_attention_ws_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int dim) {
   const Plan p = plan_of(rows, seqs, q_heads / heads, heads, dim);
-  return std::max((p.part16 + p.part_rows) * sizeof(float), size_t(16));
+  return std::max((p.told + p.part16 + p.part_rows) * sizeof(float), size_t(16));
 }
 
 kronq_status kv_attention_launch(const KvView& c, int dim, int32_t dtype, const HeadsView& q, int q_heads,

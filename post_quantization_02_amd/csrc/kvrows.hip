@@ -100,16 +100,6 @@ __device__ inline int exponent_of(uint32_t word) {
   return x == 255 ? 0 : x;
 }
 
-__device__ inline int wave_max(int x) {               // x >= 0
-  x = max(x, moved<0x111, 0xF>(x));
-  x = max(x, moved<0x112, 0xF>(x));
-  x = max(x, moved<0x114, 0xF>(x));
-  x = max(x, moved<0x118, 0xF>(x));
-  x = max(x, moved<0x142, 0xA>(x));
-  x = max(x, moved<0x143, 0xC>(x));
-  return __builtin_amdgcn_readlane(x, 63);
-}
-
 // The n lowest bits (all for n > 31, none for n < 1).
 __device__ inline uint32_t below(int n) { return n > 31 ? ~0u : n < 1 ? 0u : (1u << n) - 1; }
 
@@ -348,7 +338,7 @@ void kv_attention_rows(AttnView a) {
   Unit u;
   // key heads are the faster index, so that workgroups on one XCD read few heads;
   // later row tiles see more keys: they come first
-  const int head = blockIdx.x % a.c.heads, unit = a.units - 1 - (int)(blockIdx.x / a.c.heads);
+  const int head = blockIdx.x % a.c.heads, unit = a.cut.units - 1 - (int)(blockIdx.x / a.c.heads);
   if (!find_unit<BM, KT>(a, unit, false, u)) return;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -591,8 +581,8 @@ void kv_attention_rows(AttnView a) {
       }
     if (a.lse && h == 0)
       a.lse[(int64_t)(u.row0 + tok) * a.qheads + qh] = l == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
-  } else {
-    const int64_t at = ((int64_t)unit * a.c.heads + head) * BM + 32 * wave + i;
+  } else if (u.place < a.places) {
+    const int64_t at = ((int64_t)u.place * a.c.heads + head) * BM + 32 * wave + i;
 #pragma unroll
     for (int k = 0; k < VT; ++k)
 #pragma unroll
@@ -611,7 +601,7 @@ void kv_attention_rows(AttnView a) {
 
 template <int DIM, int WAVES>
 void rows_waves(const AttnView& a, int32_t dtype, hipStream_t s) {
-  const dim3 grid((unsigned)(a.c.heads * a.units)), block(64 * WAVES);
+  const dim3 grid((unsigned)(a.c.heads * a.cut.units)), block(64 * WAVES);
   if (dtype == KRONQ_F32)
     hipLaunchKernelGGL((kv_attention_rows<DIM, float, 2, 2, false, WAVES>), grid, block, 0, s, a);
   else if (dtype == KRONQ_BF16)

@@ -57,3 +57,21 @@ def test_dimensions_of_one_entry_have_any_stride():
     one = kq.KVCache(*(t[page:page + 1].as_strided((1,) + t.shape[1:], (1,) + t.stride()[1:]) for t in head))
     at_0 = kq.KVBatch(torch.zeros_like(batch.table), batch.ctx, batch.cu)
     assert torch.equal(kq.kronq_kv_attention(q, one, at_0, rope=rope), out)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("heads,lengths,padding", [
+    (32, [(300, 1)] * 30 + [(4000, 1)] + [(200, 1)] * 40, 0),        # one long among many short, one row each
+    (8, [(100, 1)] * 290 + [(3000, 1)] + [(50, 1)] * 230 + [(2500, 1)], 0),   # more than a workgroup looks through at once
+    (32, [(0, 0)] * 60 + [(3000, 1), (100, 1)], 60),                 # mostly empty places of a padded batch
+    (32, [(400, 300)] * 5 + [(4000, 70), (500, 1)], 3),              # row tiles of prompts, and one behind a long context
+], ids=["single rows", "hundreds", "padded", "prompts"])
+def test_a_long_sequence_among_many_is_cut(dtype, heads, lengths, padding):
+    c = Case(lengths, heads=heads, share=1, dim=64, page=64, dtype=dtype, rot=64, padding=padding, seed=len(lengths))
+    cache, batch, rope = c.dev(kq)
+    need = kq.load().kronq_kv_attention_ws(c.rows, len(lengths), heads, heads, 64)
+    assert need > 1 << 16
+    space = torch.full((need + (1 << 24),), 7, dtype=torch.uint8, device=DEV)
+    out, lse = kq.kronq_kv_attention(c.q.to(DEV), cache, batch, rope=rope, want_lse=True, ws=space[:need])
+    check_attention(c, out, lse)
+    assert bool((space[need:] == 7).all()) and not bool((space[:need] == 7).all())

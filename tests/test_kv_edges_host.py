@@ -59,3 +59,59 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="stream"):
         kq._on_stream(torch.device("cuda:0"), Stream())
+
+
+def places(index, ctx, cu, rows, share, bm, kt, units, aim, spare, least, sane):
+    most = ctypes.c_int(0)
+    st = index.places_suffice(ptr(ctx), ptr(cu), len(ctx), 1 << 13, rows, share, bm, kt, units, aim, spare, least,
+                              int(sane), ctypes.byref(most))
+    return st, most.value
+
+
+@pytest.mark.parametrize("bm,kt", [(16, 32), (32, 32), (128, 64), (256, 64)])
+def test_cut_sequences_have_places_for_their_chunks(index, bm, kt):
+    rng = np.random.default_rng(bm + kt)
+    for n in range(400):
+        seqs, share = int(rng.integers(1, 120)), int(rng.choice([1, 3, 4, 16]))
+        long = rng.random(seqs) < 0.05
+        ctx = np.where(long, rng.integers(1, 60000, seqs), rng.integers(0, 700, seqs)).astype(np.int32)
+        new = np.minimum(ctx, rng.integers(0, 400 if n % 3 == 0 else 3, seqs))
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        rows = int(cu[-1])
+        sane = n % 4 != 0
+        if not sane:                       # any content: overlapping rows, ends before starts
+            cu = rng.integers(-5, rows + 5, seqs + 1).astype(np.int32)
+        tiles = (rows * share + (bm - 1) * min(rows, seqs)) // bm
+        aim, least = int(rng.choice([1, 5, 23, 93, 744])), int(rng.choice([1, 4, 8]))
+        spare = max(aim // 2, 1)
+        st, _ = places(index, ctx, cu, rows, share, bm, kt, tiles + max(aim - tiles // 2, spare), aim, spare, least, sane)
+        assert st == 0, (n, st)
+
+
+def test_a_long_sequence_is_cut_however_many_there_are(index):
+    # as 256 single tokens of 8 key heads are planned, one of them 131071 keys behind
+    ctx = np.array([131071] + [500] * 255, np.int32)[np.random.default_rng(0).permutation(256)]
+    cu = np.arange(257, dtype=np.int32)
+    st, chunks = places(index, ctx, cu, 256, 4, 16, 32, 256 + 46, 93, 46, 8, True)
+    assert st == 0 and chunks >= 10
+    st, chunks = places(index, np.full(256, 4000, np.int32), cu, 256, 4, 16, 32, 256 + 46, 93, 46, 8, True)
+    assert st == 0 and chunks == 1         # equal ones are not
+
+
+@pytest.mark.parametrize("rows,seqs,q_heads,heads,dim", [(256, 256, 64, 8, 128), (200, 200, 64, 8, 128),
+                                                         (48, 48, 32, 32, 128), (20000, 60, 32, 8, 128),
+                                                         (1 << 14, 1 << 14, 8, 8, 64), (40000, 300, 16, 4, 256)])
+def test_full_batches_leave_workspace_for_chunks(rows, seqs, q_heads, heads, dim):
+    need = kq.load().kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim)
+    assert need >= 2 * 16 * (dim + 2) * 4  # two chunks of a row tile at least
+
+
+def test_workspace_is_bounded():
+    # both kernels' chunks of all key heads: twice 744 of 16 rows, twice 512 of 128 (or 256 of 256)
+    for rows in (1, 10, 100, 500, 1000, 1100, 4000, 1 << 17, 1 << 20, 1 << 22):
+        for seqs in (1, 2, 8, 64, 256, 1 << 14):
+            for q_heads, heads in ((1, 1), (8, 8), (32, 8), (64, 8), (16, 4), (64, 1), (128, 128)):
+                for dim in (64, 128, 256):
+                    if rows * q_heads <= 1 << 26:
+                        need = kq.load().kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim)
+                        assert 16 <= need <= (2 * 744 * 16 + 2 * 512 * 128) * (dim + 2) * 4 + 16
