@@ -75,3 +75,28 @@ def test_a_long_sequence_among_many_is_cut(dtype, heads, lengths, padding):
     out, lse = kq.kronq_kv_attention(c.q.to(DEV), cache, batch, rope=rope, want_lse=True, ws=space[:need])
     check_attention(c, out, lse)
     assert bool((space[need:] == 7).all()) and not bool((space[:need] == 7).all())
+
+
+def test_a_captured_call_of_many_sequences_follows_the_batch():
+    # which sequence is long, and so cut, changes from replay to replay
+    n, heads = 100, 32
+    c = Case([(2000, 1)] * n, heads=heads, share=1, dim=64, page=64, dtype=torch.bfloat16, rot=64)
+    c.table[:] = c.table[0]
+    cache, batch, rope = c.dev(kq)
+    q = c.q.to(DEV)
+    out, side, graph = torch.empty_like(q), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    ws = torch.empty(kq.load().kronq_kv_attention_ws(n, n, heads, heads, 64), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        kq.kronq_kv_attention(q, cache, batch, rope=rope, out=out, ws=ws)
+    rng = np.random.default_rng(1)
+    for step in range(4):
+        ctx = rng.integers(0, 60, n).astype(np.int32)
+        ctx[rng.integers(n, size=2)] = 2000, 1500 if step % 2 else 3
+        batch.ctx.copy_(torch.from_numpy(ctx))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, kq.kronq_kv_attention(q, cache, batch, rope=rope))
+        c.ctx = ctx
+        check_attention(c, out, None)
