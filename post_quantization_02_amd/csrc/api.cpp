@@ -187,7 +187,7 @@ static kronq_status kv_view(const char* fn, const kronq_kv_cache* c, const kronq
 
 // Sequences of an attention call: each unit of work looks through all of them, so
 // time grows with their square (one head of one token each of up to 60 keys: 1024
-// sequences 26 us, 4096 230 us, 16384 3.0 ms; 2^20 would be minutes for a few heads).
+// sequences 33 us, 4096 260 us, 16384 3.2 ms; 2^20 would be minutes for a few heads).
 static constexpr int64_t kAttnSeqs = 1 << 14;
 
 static kronq_status kv_rope(const char* fn, const kronq_rope* r, int32_t dim, RopeView* out) {

@@ -191,7 +191,8 @@ struct QueryPiece {
 // (281 MB).  By the vector pipes alone with one query head a key head (fp32, 12 of
 // up to 4095 keys, 32 heads: 38 us, 122 MB) and with dim 64 (fp16, 24 x 5 rows x 4 in a
 // window of 4096: 43 us).  A wave issues 250 vector operations a tile for 16 rows and
-// 8 products a part.
+// 8 products a part.  Tiles of 32 rows keep registers in scratch: fp32 and fp16 18 to
+// 24 at dim 64, 5 or 6 at dim 128.
 template <int DIM, typename T, int PARTS, bool SMALL, int QT>
 __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3) void kv_attention16(AttnView a) {
   constexpr int BM = 16 * QT, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
@@ -580,7 +581,11 @@ __global__ __launch_bounds__(256) void kv_attention_cut(KvView c, CutAsked first
 // rows on average is one launch of the first (a launch that finds nothing costs
 // 5 us).  8 sequences of up to 8000 keys, dim 128, bf16, with up to 64, 96, 128 rows x
 // share: 32, 40, 44 us by the kernel of few, 70, 75, 77 by both; 24 sequences of up to
-// 96, 128, 192: 105, 130, 181 and 129, 134, 158.
+// 96, 128, 192: 105, 130, 181 and 129, 134, 158.  One prompt among 40 single tokens x
+// 4, bf16: of 60, 250, 500 rows 78, 168, 228 by the kernel of few, 94, 156, 223 by
+// both; among 140 of 500 and 2000 rows 342 and 653, 381 and 608 (fp16: 809 and 1182).
+// What the average gives up: dim 256 (250 rows among 40: 384 and 305; 2000 among 140:
+// 1836 and 1202), and a batch padded to 256 sequences (one of 4000 rows: 795 and 629).
 
 constexpr int kFewRows = 64;
 // Tiles of a chunk at least: two for each wave (3000 keys: 14.4 us at 4, 13.8 at 8,
@@ -594,7 +599,9 @@ constexpr int kWholeTiles16 = 24;
 // workgroups that are resident at once (three on a CU), because a unit's start (its
 // search, its query, the first tile) takes 8 us and all units' starts then pass
 // together.  Call times at 672, 744, 768: 131071 keys 42, 41, 40 us (48 at 1450); 40
-// sequences 77, 70, 71; 12 of 32 key heads 43, 42, 46.
+// sequences 77, 70, 71; 12 of 32 key heads 43, 42, 46.  Measured for dim 64 and 128:
+// of dim 256 one workgroup fits a CU (its registers), and 744 are three rounds (60000
+// keys 61 us; no other number was measured).
 constexpr int kUnits16 = 744;
 constexpr int kUnits32 = 496;            // of 512: two tiles of rows, dim 128
 // The kernel of many rows: tiles of 128 or 256 rows, the latter where sequences
@@ -608,7 +615,8 @@ constexpr int kMinTilesRows = 4;         // 256 keys
 // round), fewer than all to twice that (two rounds of smaller ones).  One sequence of
 // up to 8000 keys, rows x 4, dim 128, bf16: 256 rows 74 us in one round, 91 in two;
 // 1024 rows 188 and 231 (fp32: 314 and 397); two such sequences, more than half: 319
-// and 287.
+// and 287.  Of dim 256, and of 128 rows in fp32 and fp16 at dim 128, one workgroup
+// fits a CU: for them these are twice as many, and no other number was measured.
 constexpr int kResident = 512, kResidentTall = 256;
 
 // The join gives each row's head as many groups of lanes as make this many
@@ -621,7 +629,6 @@ constexpr int kUncut = INT32_MAX;
 
 // How a call is cut: units of each kernel (0: not launched; a bound of its row
 // tiles, and chunks on top), and whether there can be chunks to join.
-//
 struct Plan {
   Cut few, rows;
   int waves;
@@ -759,6 +766,8 @@ kronq_status launch(AttnView a, int dim, int32_t dtype, float* ws, hipStream_t s
 
 template <int DIM>
 kronq_status launch_dim(const AttnView& a, int32_t dtype, float* ws, hipStream_t s) {
+  // Operands in two fp16 parts are as good as fp32 ones (2^-22); in bf16 one part's
+  // 2^-11 lies below the result's own 2^-8.
   if (dtype == KRONQ_F32) return launch<DIM, float, 2>(a, DIM, dtype, ws, s);
   if (dtype == KRONQ_BF16) return launch<DIM, bf16_t, 1>(a, DIM, dtype, ws, s);
   return launch<DIM, _Float16, 2>(a, DIM, dtype, ws, s);

@@ -126,8 +126,9 @@ __device__ inline Work work_of(const KvView& c, int per) {
   return {row, (int)(threadIdx.x & (LANES - 1)) * 8, head0, min(head0 + per, c.heads), (blockIdx.y & 1) == 0};
 }
 
-// Bound by the vector pipes at size (the extremes of rotated keys in fp64, then
-// twelve operations a value), by the launch for few rows.  19000 rows of 8 heads of
+// Bound by the vector pipes at size (28.6 operations a value by the counters: what a
+// group's lanes do for their eight values each, extremes of rotated keys in fp64 and
+// the grid among it), by the launch for few rows.  19000 rows of 8 heads of
 // 128 bf16 values, keys and values: 40 us (118 MB: 2.9 TB/s); one row 4 us.  With
 // a lane group for each (row, head), its sequence searched each time, 67 us.
 template <typename T, int LANES>

@@ -321,11 +321,13 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
 }
 
 // Bound by the vector pipes (the exponentials and what surrounds them, and
-// unpacking: 335 operations a wave and 64 keys at dim 128 in bf16) and the matrix
-// cores (32 products of 32 cycles) together, which two waves on a SIMD overlap in
-// part; LDS conflicts are 2 % of it.  2047 + 1774 rows x 4 of 8 key heads behind 9001
-// and 4830 keys: 562 us, 680 TFLOP/s; fp16 in a window of 2048, queries in two parts:
-// 177 us.
+// unpacking: by the counters 400 operations a wave and 64 keys at dim 128 in bf16,
+// 540 in fp16) and the matrix cores (32 products of 32 cycles) together, of which two
+// waves on a SIMD overlap little, for one barrier a pass keeps all in one phase; LDS
+// conflicts are 2 % of it.  2047 + 1774 rows x 4 of 8 key heads behind 9001 and 4830
+// keys: 540 us, 700 TFLOP/s, and 570 once the clock has fallen under a run of such
+// launches; fp16 in a window of 2048, queries in two parts: 180 us.  Dim 256 keeps 59
+// registers in scratch in fp32 and fp16.
 template <int DIM, typename T, int QP, int PP, bool FOLD, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && QP > 1 && WAVES == 4) ? 1 : 2)
 void kv_attention_rows(AttnView a) {
@@ -607,6 +609,10 @@ void rows_waves(const AttnView& a, int32_t dtype, hipStream_t s) {
   else if (dtype == KRONQ_BF16)
     hipLaunchKernelGGL((kv_attention_rows<DIM, bf16_t, 1, 1, true, WAVES>), grid, block, 0, s, a);
   else
+    // weights in one part, 2^-11 as the result itself: in two, as the kernel of few rows
+    // holds them, a prompt of 2047 rows x 4 takes 623 us, not 559, one in a window of
+    // 2048 210, not 189; the latter's error against 64 bits is 0.00029 with one, 0.00021
+    // of it the result's own rounding
     hipLaunchKernelGGL((kv_attention_rows<DIM, _Float16, 2, 1, false, WAVES>), grid, block, 0, s, a);
 }
 
