@@ -764,7 +764,8 @@ class KVCache:
         self.k_codes, self.v_codes, self.k_grid, self.v_grid = k_codes, v_codes, k_grid, v_grid
         self.pages, self.heads, self.page, self.dim = pages, heads, page, 2 * half
         self._c = _Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_grid.data_ptr(), v_grid.data_ptr(),
-                         *(t.stride(0) if pages > 1 else t[0].numel() for t in (k_codes, v_codes, k_grid, v_grid)),
+                         *(t.stride(0) if pages != 1 else math.prod(t.shape[1:])
+                           for t in (k_codes, v_codes, k_grid, v_grid)),
                          pages, heads, page, 2 * half)
 
     @classmethod

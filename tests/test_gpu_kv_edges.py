@@ -100,3 +100,10 @@ def test_a_captured_call_of_many_sequences_follows_the_batch():
         assert torch.equal(out, kq.kronq_kv_attention(q, cache, batch, rope=rope))
         c.ctx = ctx
         check_attention(c, out, None)
+
+
+def test_a_cache_of_no_pages_is_refused_by_the_calls():
+    c = Case([(3, 1)], heads=2, dim=64)
+    _, batch, _ = c.dev(kq)
+    with pytest.raises(kq.KronqError):
+        kq.kronq_kv_read(kq.KVCache.empty(0, 2, 16, 64, DEV), batch, c.rows)
