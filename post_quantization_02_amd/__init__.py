@@ -785,7 +785,8 @@ class KVBatch:
     def __init__(self, table: torch.Tensor, ctx: torch.Tensor, cu: torch.Tensor):
         self.device = table.device
         for t, nm, d in ((table, "table", 2), (ctx, "ctx", 1), (cu, "cu", 1)):
-            _dev(t, nm, torch.int32)
+            # a dimension of one entry, or none, has no distance to speak of
+            _dev(t.reshape(-1) if t.dim() == 2 and t.shape[1] < 2 else t, nm, torch.int32)
             if t.dim() != d or (d == 1 and not t.is_contiguous()):
                 raise ValueError("%s must be a contiguous %d-D tensor" % (nm, d))
         _same_device(self.device, ctx, cu)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import post_quantization_02_amd as kq
-from kv_helpers import DEV, Case, check_attention
+from kv_helpers import DEV, Case, cache_equal, check_attention
 from test_gpu_kv import TYPES, attend, ids
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +107,16 @@ def test_a_cache_of_no_pages_is_refused_by_the_calls():
     _, batch, _ = c.dev(kq)
     with pytest.raises(kq.KronqError):
         kq.kronq_kv_read(kq.KVCache.empty(0, 2, 16, 64, DEV), batch, c.rows)
+
+
+def test_tables_of_one_column_and_of_none_have_any_stride():
+    c = Case([(14, 3), (9, 1)], heads=2, share=2, dim=64, rot=64)
+    cache, batch, rope = c.dev(kq)
+    q = c.q.to(DEV)
+    one = kq.KVBatch(batch.table.as_strided((2, 1), (1, 5)), batch.ctx, batch.cu)
+    check_attention(c, kq.kronq_kv_attention(q, cache, one, rope=rope), None)
+    none = kq.KVBatch(batch.table.as_strided((2, 0), (3, 5)), batch.ctx, batch.cu)
+    assert bool(torch.isnan(kq.kronq_kv_attention(q, cache, none, rope=rope)).all())
+    assert bool(torch.isnan(kq.kronq_kv_read(cache, none, c.rows)[0]).all())
+    kq.kronq_kv_append(c.k.to(DEV), c.v.to(DEV), cache, none, rope=rope)
+    cache_equal(cache, c.cache)
