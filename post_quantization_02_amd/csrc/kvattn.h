@@ -253,6 +253,12 @@ __device__ inline uint32_t zero64_of(uint32_t z) { return (z * 0x00100010u) | 0x
 constexpr int kLazy = 8, kRoom = 6, kTop = 14;
 constexpr int kLeast = -126, kMost = 120;             // of e; kLeast where nothing was seen yet
 
+// Beyond this f S and its maximum, which is rounded to fp32, no longer cancel to 0 for
+// the largest score (from 2^28 on its weight would overflow, or vanish): there what
+// the rounding left is taken off, too.  Asking for it costs 0 to 2 % (dim 64
+// and 256: up to 6).
+constexpr float kSteep = 0x1p+16f;
+
 // Exponent e for a row's largest product (positive).
 __device__ inline int exponent_for(float largest) {
   return (int)(__float_as_uint(largest) >> 23) - 126 - kRoom;

@@ -191,8 +191,8 @@ struct QueryPiece {
 // (281 MB).  By the vector pipes alone with one query head a key head (fp32, 12 of
 // up to 4095 keys, 32 heads: 38 us, 122 MB) and with dim 64 (fp16, 24 x 5 rows x 4 in a
 // window of 4096: 43 us).  A wave issues 250 vector operations a tile for 16 rows and
-// 8 products a part.  Tiles of 32 rows keep registers in scratch: fp32 and fp16 18 to
-// 24 at dim 64, 5 or 6 at dim 128.
+// 8 products a part.  Tiles of 32 rows keep registers in scratch: fp32 and fp16 16 to
+// 25 at dim 64, 5 or 6 at dim 128.
 template <int DIM, typename T, int PARTS, bool SMALL, int QT>
 __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3) void kv_attention16(AttnView a) {
   constexpr int BM = 16 * QT, KT = 32, KS = DIM / 32, VT = DIM / 16, PAD = DIM + 4;
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
 
   const Unpacker un;
   f32x4 o[QT][VT];
-  float m[QT], l[QT];                                 // m of f S; l of this lane's keys
+  float m[QT], l[QT];                                 // m of S; l of this lane's keys
   int e[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -331,13 +331,12 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x) top = fmaxf(top, s[x]);
-      top *= f[t];
-      if (__any(top > m[t] + kLazy || (m[t] == -INFINITY && top > m[t]))) {
+      if (__any(top * f[t] > fmaf(m[t], f[t], kLazy) || (m[t] == -INFINITY && top > m[t]))) {
         float nm = fmaxf(top, __shfl_xor(top, 16));
         nm = fmaxf(nm, __shfl_xor(nm, 32));
         nm = fmaxf(nm, m[t]);
         if (m[t] != -INFINITY) {
-          const float down = fminf(nm - m[t], 300.0f);
+          const float down = fminf((nm - m[t]) * f[t], 300.0f);
           const int ne = max(e[t] - (int)ceilf(down), kLeast);
           const float by = __builtin_amdgcn_exp2f((float)(e[t] - ne) - down);
           l[t] *= __builtin_amdgcn_exp2f(-down);
@@ -350,7 +349,13 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
       // weights times 2^-ue, the part of the row's factor that they can carry (none
       // before the first is known)
       const int ue = e[t] == kLeast ? 0 : min(max(e[t], -60), 30);
-      const float base = (m[t] == -INFINITY ? 0.0f : m[t]) + (float)ue;
+      const float most = m[t] == -INFINITY ? 0.0f : m[t] * f[t];
+      float base = most + (float)ue;
+      if (__any(fabsf(most) > kSteep)) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s[x] -= m[t] == -INFINITY ? 0.0f : m[t];
+        base = (float)ue;
+      }
       float y[8], ytop = 0, sum = 0;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
@@ -422,7 +427,7 @@ __global__ __launch_bounds__(256, DIM == 256 ? 1 : QT > 1 && DIM == 128 ? 2 : 3)
     l[t] += __shfl_xor(l[t], 16);
     l[t] += __shfl_xor(l[t], 32);
     if (lane < 16) {
-      lds_m[wave][i] = m[t];
+      lds_m[wave][i] = m[t] == -INFINITY ? -INFINITY : m[t] * f[t];
       lds_l[wave][i] = l[t];
     }
     const float back = ldexpf(1.0f, e[t]);

@@ -326,7 +326,7 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
 // waves on a SIMD overlap little, for one barrier a pass keeps all in one phase; LDS
 // conflicts are 2 % of it.  2047 + 1774 rows x 4 of 8 key heads behind 9001 and 4830
 // keys: 540 us, 700 TFLOP/s, and 570 once the clock has fallen under a run of such
-// launches; fp16 in a window of 2048, queries in two parts: 180 us.  Dim 256 keeps 59
+// launches; fp16 in a window of 2048, queries in two parts: 180 us.  Dim 256 keeps 70
 // registers in scratch in fp32 and fp16.
 template <int DIM, typename T, int QP, int PP, bool FOLD, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && QP > 1 && WAVES == 4) ? 1 : 2)
@@ -369,7 +369,8 @@ void kv_attention_rows(AttnView a) {
     for (int x = 0; x < 16; ++x) o[k][x] = 0;
   float m = -INFINITY, l = 0;                         // of f S; l of this lane's keys
   int e = kLeast;                                     // not FOLD: O is held times 2^-e
-  float ref = -INFINITY;                              // FOLD: O is held times 2^(kUp - ref)
+  float rest = 0;                                     // what rounding m left of f S
+  float d = -INFINITY;                                // FOLD: O is held times 2^(kUp - m - d)
 
   // The tile `at` on its way to LDS, and its keys that are still to go there.  What
   // is asked for is asked for every time, the last tile again behind the end: see
@@ -457,18 +458,19 @@ void kv_attention_rows(AttnView a) {
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[s][x]);
-      top *= ff;
-      const float vtop = FOLD ? top + (float)pass.ve : top;
-      if (__any(top > m + kLazy || (m == -INFINITY && top > m) || (FOLD && vtop > ref + kLazy))) {
-        const float row = fmaxf(top, __shfl_xor(top, 32)), nm = fmaxf(row, m);
+      const float mine = top * ff;
+      if (__any(mine > m + kLazy || (m == -INFINITY && mine > m) || (FOLD && mine - m + (float)pass.ve > d + kLazy))) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float row = top * ff, nm = fmaxf(row, m);
+        const float nrest = row > m ? fmaf(top, ff, -row) : rest;
         if (m != -INFINITY) {
-          const float down = fminf(nm - m, 300.0f);
+          const float far = fmaxf(nm - m + (nrest - rest), 0.0f), down = fminf(far, 300.0f);
           float by = __builtin_amdgcn_exp2f(-down);
           l *= by;
           if constexpr (FOLD) {
-            const float nref = fmaxf(row + (float)pass.ve, ref);
-            by = __builtin_amdgcn_exp2f(fmaxf(ref - nref, -300.0f));
-            ref = nref;
+            const float nd = fmaxf(row - nm + (float)pass.ve, d - far);
+            by = __builtin_amdgcn_exp2f(fmaxf(d - far - nd, -300.0f));
+            d = nd;
           } else {
             const int ne = max(e - (int)ceilf(down), kLeast);
             by = __builtin_amdgcn_exp2f((float)(e - ne) - down);
@@ -477,24 +479,34 @@ void kv_attention_rows(AttnView a) {
 #pragma unroll
           for (int k = 0; k < VT; ++k) o[k] *= by;
         } else if (FOLD && nm != -INFINITY) {
-          ref = nm + (float)pass.ve;
+          d = (float)pass.ve;
         }
         m = nm;
+        rest = nrest;
       }
-      const float base = m == -INFINITY ? 0.0f : m;
-      // Weights are 2^(ff sc + up).  FOLD: as O is held; times 2^(-base - up) they
-      // are the sum's, and where that is too far for one fp32 number to do for both
-      // (`far`), they are added up by themselves.  Otherwise: times 2^-ue, the part of
-      // the row's factor that they can carry (none before the first is known).
+      // Weights are 2^(ff sc - base + up).  FOLD: as O is held; times 2^-up they are the
+      // sum's, and where that is too far for one fp32 number to do for both (`far`),
+      // they are added up by themselves.  Otherwise: times 2^-ue, the part of the row's
+      // factor that they can carry (none before the first is known).
       const int ue = e == kLeast ? 0 : min(max(e, -60), 30);
-      const float up = !FOLD ? -base - (float)ue : ref == -INFINITY ? 0.0f : (float)(pass.ve + kUp) - ref;
-      const bool far = FOLD && __any(-base - up > 60.0f);
+      const float up = !FOLD ? -(float)ue : d == -INFINITY ? 0.0f : (float)(pass.ve + kUp) - d;
+      const bool far = FOLD && __any(-up > 60.0f);
+      float base = m == -INFINITY ? 0.0f : m, fx = ff;
+      if (__any(fabsf(base) > kSteep)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) sc[s][x] = fmaf(sc[s][x], ff, -base) - rest;
+        base = 0;
+        fx = 1;
+      }
+      const float off = up - base;
       float sum = 0, apart = 0;
       if (far) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) apart += __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, -base));
+          for (int x = 0; x < 16; ++x) apart += __builtin_amdgcn_exp2f(fmaf(sc[s][x], fx, -base));
       }
       if constexpr (!FOLD) {
         float ytop = 0;
@@ -502,7 +514,7 @@ void kv_attention_rows(AttnView a) {
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(sc[s][x], ff, up));
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[s][x], fx, off));
             sum += p;
             const bool seen = sc[s][x] != -INFINITY;  // not seen: whatever scale is there
             sc[s][x] = seen ? p * tile.vs[32 * s + 16 * (x >> 3) + 8 * h + (x & 7)] : 0.0f;
@@ -530,7 +542,7 @@ void kv_attention_rows(AttnView a) {
       auto weigh = [&](int n, int x) __attribute__((always_inline)) {
         float y = sc[n >> 1][8 * (n & 1) + x];
         if constexpr (FOLD) {
-          y = __builtin_amdgcn_exp2f(fmaf(y, ff, up));
+          y = __builtin_amdgcn_exp2f(fmaf(y, fx, off));
           sum += y;
         }
         p1[n & 1][x] = (_Float16)y;
@@ -558,7 +570,7 @@ void kv_attention_rows(AttnView a) {
         }
         in_order();
       });
-      l += !FOLD ? sum * ldexpf(1.0f, ue) : -base - up > 60.0f ? apart : sum * __builtin_amdgcn_exp2f(-base - up);
+      l += !FOLD ? sum * ldexpf(1.0f, ue) : -up > 60.0f ? apart : sum * __builtin_amdgcn_exp2f(-up);
     }
     __syncthreads();
   }
@@ -567,7 +579,7 @@ void kv_attention_rows(AttnView a) {
   if (r >= u.len * share) return;
   if (pos >= room_of(a.c)) l = kNan;               // a position without a column
   // O is held times 2^-(2 back): in two steps, each within fp32
-  const float back = __builtin_amdgcn_exp2f(!FOLD ? 0.5f * e : ref == -INFINITY ? 0.0f : 0.5f * (ref - m - (float)kUp));
+  const float back = __builtin_amdgcn_exp2f(!FOLD ? 0.5f * e : d == -INFINITY ? 0.0f : 0.5f * (d - (float)kUp));
   if (u.chunks == 1) {
     const int tok = r / share, qh = head * share + r % share;
     const float by = l == 0 ? 0.0f : back / l;      // 0 of a row that sees nothing

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import post_quantization_02_amd as kq
-from kv_helpers import DEV, Case, cache_equal, check_attention
+from oracle import kv_oracle as K
+from kv_helpers import DEV, HALF, Case, cache_equal, check_attention, f64
 from test_gpu_kv import TYPES, attend, ids
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +121,38 @@ def test_tables_of_one_column_and_of_none_have_any_stride():
     assert bool(torch.isnan(kq.kronq_kv_read(cache, none, c.rows)[0]).all())
     kq.kronq_kv_append(c.k.to(DEV), c.v.to(DEV), cache, none, rope=rope)
     cache_equal(cache, c.cache)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("new", [2, 90])
+@pytest.mark.parametrize("power", [12, 20, 27, 28, 30, 34, 60, 90])
+def test_scores_of_any_size(dtype, new, power):
+    # scores so large that a unit of them is less than their last place: one key has all the weight
+    c = Case([(200, new), (150, 2)], heads=2, share=2, dim=64, dtype=dtype, seed=power)
+    if dtype == torch.float16:                       # queries do not reach so far; keys do
+        c.cache["k_grid"] += np.uint32(power - 12 << 23)
+    c.q[:] = torch.sign(c.q.float()) * 2.0 ** (12 if dtype == torch.float16 else power)
+    cache, batch, _ = c.dev(kq)
+    out, lse = kq.kronq_kv_attention(c.q.to(DEV), cache, batch, want_lse=True)
+    assert bool(torch.isfinite(out).all() and torch.isfinite(lse).all())
+    # the other tests' bound takes scores' errors to be small; here they are not, and what
+    # is sure is where one score is beyond all others' errors
+    got, glse, sure = f64(out), f64(lse), 0
+    for r, (b, pos) in enumerate(K.rows_of(c.batch, c.rows)):
+        k = np.stack([K.held(c.cache, c.batch, b, j, "k") for j in range(pos + 1)])
+        v = np.stack([K.held(c.cache, c.batch, b, j, "v") for j in range(pos + 1)])
+        for h in range(4):
+            s = 0.125 * k[:, h // 2] @ f64(c.q)[r, h]
+            size = 0.125 * np.abs(k[:, h // 2]) @ np.abs(f64(c.q)[r, h])
+            order = np.argsort(s)
+            # a score is off by 72 half steps of fp32, and 2 2^-11 where keys carry their scales
+            off = size.max() * (72 * 2.0 ** -24 + (2 * 2.0 ** -11 if dtype == torch.bfloat16 else 0))
+            top = s[order[-1]]
+            assert abs(glse[r, h] - top - np.log(np.exp(s - top).sum())) <= off + 2.0 ** -20 * (1 + abs(top)), (r, h)
+            if top - s[order[-2]] > 2 * off + 40:
+                # the value, in bf16 with its scale rounded, and the result's own rounding
+                want = v[order[-1], h // 2]
+                tol = np.abs(want) * (HALF[dtype] + (3 * 2.0 ** -11 if dtype != torch.float32 else 2.0 ** -20)) + 1e-6
+                assert (np.abs(got[r, h] - want) <= tol).all(), (r, h)
+                sure += 1
+    assert sure > c.rows
