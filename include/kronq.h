@@ -602,10 +602,12 @@ kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t d
  * q_heads : a multiple of the cache's heads; at most 2^22 rows and 2^26 rows x
  *           q_heads, at most 2^14 sequences (KRONQ_EUNSUPPORTED otherwise).
  * scale   : > 0 and finite, 1 / sqrt(dim) as a rule.
- * Scores, the running maximum and sum and the outputs are fp32.  Queries and
- * weights enter the matrix cores as fp16 scaled by powers of two: for KRONQ_F32
- * in two parts (22 bits); for KRONQ_F16 queries in two parts, weights in one or
- * two; for KRONQ_BF16 in one.  Codes minus zero points are exact there; for
+ * Scores, the running maximum and sum and the outputs are fp32, sums before their
+ * division too: what rows give that see held values beyond 2^100 is not defined.
+ * Queries and weights enter the matrix cores as fp16 scaled by powers of two: for
+ * KRONQ_F32 in two parts (22 bits); for KRONQ_F16 queries in two parts, weights in
+ * two where sequences have few rows (up to 64 rows x share on average) and in one
+ * else; for KRONQ_BF16 in one.  Codes minus zero points are exact there; for
  * KRONQ_BF16 and many rows they carry the scales, rounded to fp16.
  * ws      : kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim) bytes,
  *           written before it is read; calls that overlap in time need one each.
