@@ -605,10 +605,9 @@ kronq_status kronq_kv_read(const kronq_heads* k, const kronq_heads* v, int32_t d
  * Scores, the running maximum and sum and the outputs are fp32, sums before their
  * division too: what rows give that see held values beyond 2^100 is not defined.
  * Queries and weights enter the matrix cores as fp16 scaled by powers of two: for
- * KRONQ_F32 in two parts (22 bits); for KRONQ_F16 queries in two parts, weights in
- * two where sequences have few rows (up to 64 rows x share on average) and in one
- * else; for KRONQ_BF16 in one.  Codes minus zero points are exact there; for
- * KRONQ_BF16 and many rows they carry the scales, rounded to fp16.
+ * KRONQ_F32 and KRONQ_F16 in two parts (22 bits), for KRONQ_BF16 in one.  Codes
+ * minus zero points are exact there; for KRONQ_BF16 and many rows (beyond 64 rows x
+ * share of a sequence on average) they carry the scales, rounded to fp16.
  * ws      : kronq_kv_attention_ws(rows, seqs, q_heads, heads, dim) bytes,
  *           written before it is read; calls that overlap in time need one each.
  * No host synchronization, no memset, no atomics: may be captured in a HIP

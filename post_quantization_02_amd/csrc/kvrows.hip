@@ -279,12 +279,12 @@ struct Unpacking {
 
 // One stage: the scores of the tile `cur`, and the next tile's codes into `out`.
 // Operands are read a step ahead (further ahead there are no registers).
-template <int DIM, int WAVES, bool FOLD, int QP, bool QLDS>
+template <int DIM, int WAVES, bool FOLD, int PARTS, bool QLDS>
 __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restrict__ cur, Tile<DIM, FOLD>* __restrict__ out,
                                                   const Unpacker& un, const Raw<DIM, WAVES>& t,
                                                   const KeyInfo& info, int wave, uint8_t* __restrict__ mine,
                                                   const half8_t (&q1)[DIM / 16],
-                                                  const half8_t (&q2)[QP > 1 ? DIM / 16 : 1],
+                                                  const half8_t (&q2)[PARTS > 1 ? DIM / 16 : 1],
                                                   const half8_t (*__restrict__ lds_q)[64], f32x16 (&sc)[2]) {
   using S = Split<DIM, WAVES>;
   constexpr int KS = DIM / 16, AHEAD = 1, RING = AHEAD + 1;
@@ -310,8 +310,8 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
     constexpr int k = at / 2, s = at % 2, N = Unpacking<DIM, WAVES, FOLD>::kPieces;
     if constexpr (s == 0 && k + AHEAD < KS) read(k + AHEAD);
     sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], q1[k], sc[s], 0, 0, 0);
-    if constexpr (QP > 1)
-      sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], QLDS ? second[QLDS ? k % RING : 0] : q2[QP > 1 ? k : 0],
+    if constexpr (PARTS > 1)
+      sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv[k % RING][s], QLDS ? second[QLDS ? k % RING : 0] : q2[PARTS > 1 ? k : 0],
                                                      sc[s], 0, 0, 0);
     each<N>([&](auto w) __attribute__((always_inline)) {
       if constexpr (w * 2 * KS / N == at) work.template piece<w>(wave, un, t, out);
@@ -322,18 +322,19 @@ __device__ __forceinline__ void scores_and_unpack(const Tile<DIM, FOLD>* __restr
 
 // Bound by the vector pipes (the exponentials and what surrounds them, and
 // unpacking: by the counters 400 operations a wave and 64 keys at dim 128 in bf16,
-// 540 in fp16) and the matrix cores (32 products of 32 cycles) together, of which two
-// waves on a SIMD overlap little, for one barrier a pass keeps all in one phase; LDS
-// conflicts are 2 % of it.  2047 + 1774 rows x 4 of 8 key heads behind 9001 and 4830
-// keys: 540 us, 700 TFLOP/s, and 570 once the clock has fallen under a run of such
-// launches; fp16 in a window of 2048, queries in two parts: 180 us.  Dim 256 keeps 70
-// registers in scratch in fp32 and fp16.
-template <int DIM, typename T, int QP, int PP, bool FOLD, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && QP > 1 && WAVES == 4) ? 1 : 2)
+// 660 in fp16) and the matrix cores (32 products of 32 cycles, 64 where operands are
+// in two parts) together, of which two waves on a SIMD overlap little, for one
+// barrier a pass keeps all in one phase; LDS conflicts are 2 % of it.  2047 + 1774
+// rows x 4 of 8 key heads behind 9001 and 4830 keys: 540 us, 700 TFLOP/s, and 570 once
+// the clock has fallen under a run of such launches; fp16 in a window of 2048: 200 us
+// (180 with weights in one part, whose error against 64 bits was 0.0003, not 0.0002).
+// Dim 256 keeps 70 registers in scratch in fp32 and fp16.
+template <int DIM, typename T, int PARTS, bool FOLD, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, DIM == 256 || (DIM == 128 && PARTS > 1 && WAVES == 4) ? 1 : 2)
 void kv_attention_rows(AttnView a) {
   using S = Split<DIM, WAVES>;
   constexpr int BM = 32 * WAVES, KS = DIM / 16, VT = DIM / 32;
-  constexpr bool QLDS = QP > 1 && DIM == 128 && WAVES == 8;   // queries' second parts: no registers left
+  constexpr bool QLDS = PARTS > 1 && DIM == 128 && WAVES == 8;   // queries' second parts: no registers left
   __shared__ Tile<DIM, FOLD> lds[2];
   __shared__ half8_t lds_q[QLDS ? WAVES : 1][QLDS ? KS : 1][64];
   __shared__ __align__(16) uint8_t packed[WAVES][256 * S::kWords];
@@ -355,8 +356,8 @@ void kv_attention_rows(AttnView a) {
   const int r0 = u.qtile * BM + 32 * wave, r = r0 + i, pos0 = u.ctx - u.len;
   const int pos = pos0 + min(r / share, u.len - 1);
   const int wave_lo = pos0 + min(r0 / share, u.len - 1), wave_hi = pos0 + min((r0 + 31) / share, u.len - 1);
-  half8_t q1[KS], q2[QP > 1 ? KS : 1];
-  const float f = load_query<T, QP, KS, 2>(a, u, head, r, 8 * h, 16, q1, q2);
+  half8_t q1[KS], q2[PARTS > 1 ? KS : 1];
+  const float f = load_query<T, PARTS, KS, 2>(a, u, head, r, 8 * h, 16, q1, q2);
   if constexpr (QLDS) {
 #pragma unroll
     for (int k = 0; k < KS; ++k) lds_q[wave][k][lane] = q2[k];
@@ -408,7 +409,7 @@ void kv_attention_rows(AttnView a) {
   // the scores of the buffer `from` and the chosen pass into the other; when a tile
   // has gone there the next one's data are asked for
   auto stage = [&](int from) __attribute__((always_inline)) {
-    scores_and_unpack<DIM, WAVES, FOLD, QP, QLDS>(&lds[from], &lds[from ^ 1], un, raw, info, wave, packed[wave], q1, q2,
+    scores_and_unpack<DIM, WAVES, FOLD, PARTS, QLDS>(&lds[from], &lds[from ^ 1], un, raw, info, wave, packed[wave], q1, q2,
                                                   lds_q[QLDS ? wave : 0], sc);
     if (!left) {
       ++at;
@@ -538,7 +539,7 @@ void kv_attention_rows(AttnView a) {
       }
       // Sixteen keys at a time: their products, and between them the next sixteen's
       // weights.
-      half8_t p1[2], p2[PP > 1 ? 2 : 1], vv[2][VT];
+      half8_t p1[2], p2[PARTS > 1 ? 2 : 1], vv[2][VT];
       auto weigh = [&](int n, int x) __attribute__((always_inline)) {
         float y = sc[n >> 1][8 * (n & 1) + x];
         if constexpr (FOLD) {
@@ -546,7 +547,7 @@ void kv_attention_rows(AttnView a) {
           sum += y;
         }
         p1[n & 1][x] = (_Float16)y;
-        if constexpr (PP > 1) p2[n & 1][x] = (_Float16)(y - (float)p1[n & 1][x]);
+        if constexpr (PARTS > 1) p2[n & 1][x] = (_Float16)(y - (float)p1[n & 1][x]);
       };
       auto read = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
@@ -563,7 +564,7 @@ void kv_attention_rows(AttnView a) {
         constexpr int n = at / VT, k = at % VT;
         if constexpr (n < 3 && k == 0) read(n + 1);
         o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[n & 1][k], p1[n & 1], o[k], 0, 0, 0);
-        if constexpr (PP > 1) o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[n & 1][k], p2[PP > 1 ? n & 1 : 0], o[k], 0, 0, 0);
+        if constexpr (PARTS > 1) o[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[n & 1][k], p2[PARTS > 1 ? n & 1 : 0], o[k], 0, 0, 0);
         if constexpr (n < 3) {
 #pragma unroll
           for (int x = 8 * k / VT; x < 8 * (k + 1) / VT; ++x) weigh(n + 1, x);
@@ -617,15 +618,11 @@ template <int DIM, int WAVES>
 void rows_waves(const AttnView& a, int32_t dtype, hipStream_t s) {
   const dim3 grid((unsigned)(a.c.heads * a.cut.units)), block(64 * WAVES);
   if (dtype == KRONQ_F32)
-    hipLaunchKernelGGL((kv_attention_rows<DIM, float, 2, 2, false, WAVES>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, float, 2, false, WAVES>), grid, block, 0, s, a);
   else if (dtype == KRONQ_BF16)
-    hipLaunchKernelGGL((kv_attention_rows<DIM, bf16_t, 1, 1, true, WAVES>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, bf16_t, 1, true, WAVES>), grid, block, 0, s, a);
   else
-    // weights in one part, 2^-11 as the result itself: in two, as the kernel of few rows
-    // holds them, a prompt of 2047 rows x 4 takes 623 us, not 559, one in a window of
-    // 2048 210, not 189; the latter's error against 64 bits is 0.00029 with one, 0.00021
-    // of it the result's own rounding
-    hipLaunchKernelGGL((kv_attention_rows<DIM, _Float16, 2, 1, false, WAVES>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((kv_attention_rows<DIM, _Float16, 2, false, WAVES>), grid, block, 0, s, a);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
-"""Attention of few rows over the 4-bit cache, held to what its kernel promises: a
-second part of queries or weights that were lost, or scales rounded into the
-operands (as those of many rows in bf16 are), would be outside these bounds."""
+"""Attention over the 4-bit cache, held to what its kernels promise: a second part
+of queries or weights that were lost, or scales rounded into the operands (as those
+of many rows in bf16 are), would be outside these bounds."""
 import numpy as np
 import pytest
 import torch
@@ -48,6 +48,21 @@ def test_few_rows_keep_their_precision(dtype, dim, new, keys, qscale):
     want, wlse, size = K.attention(c.cache, c.batch, f64(c.q), dim ** -0.5)
     for r in range(c.rows):
         far, lfar = bounds(size[r], want[r], wlse[r], dtype, dim, 24)
+        assert (np.abs(f64(out)[r] - want[r]) <= far).all(), r
+        assert (np.abs(f64(lse)[r] - wlse[r]) <= lfar).all(), r
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16], ids=["float32", "float16"])
+@pytest.mark.parametrize("dim,new", [(64, 30), (64, 90), (128, 30), (128, 90), (256, 30)])
+def test_many_rows_keep_their_precision(dtype, dim, new):
+    # tiles of 128 and 256 rows x share: as precise as few rows are
+    c = Case([(new + 6, new)], share=4, dim=dim, dtype=dtype, qscale=0.05, seed=dim + new)
+    cache, batch, _ = c.dev(kq)
+    out, lse = kq.kronq_kv_attention(c.q.to(DEV), cache, batch, want_lse=True)
+    want, wlse, size = K.attention(c.cache, c.batch, f64(c.q), dim ** -0.5)
+    for r in range(c.rows):
+        far, lfar = bounds(size[r], want[r], wlse[r], dtype, dim, new + 6)
         assert (np.abs(f64(out)[r] - want[r]) <= far).all(), r
         assert (np.abs(f64(lse)[r] - wlse[r]) <= lfar).all(), r
 
