@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256) void kv_attention_cut(KvView c, CutAsked first
 // share: 32, 40, 44 us by the kernel of few, 70, 75, 77 by both; 24 sequences of up to
 // 96, 128, 192: 105, 130, 181 and 129, 134, 158.  One prompt among 40 single tokens x
 // 4, bf16: of 60, 250, 500 rows 78, 168, 228 by the kernel of few, 94, 156, 223 by
-// both; among 140 of 500 and 2000 rows 342 and 653, 381 and 608 (fp16: 809 and 1182).
+// both; among 140 of 500 and 2000 rows 342 and 653, 381 and 608 (fp16: 809 and over 1182).
 // What the average gives up: dim 256 (250 rows among 40: 384 and 305; 2000 among 140:
 // 1836 and 1202), and a batch padded to 256 sequences (one of 4000 rows: 795 and 629).
 
