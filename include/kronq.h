@@ -621,6 +621,101 @@ kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t row
                                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A calibration pass (hyper.ai summary, Method: H_X = E[x x^T] and H_G = E[g g^T]
+ * need the sublayers' inputs and the gradients of their outputs).  The gradients
+ * of the q, k and v projections' outputs are those of the attention, turned back
+ * by the position rotation; those of the output head are those of the tokens' log
+ * probabilities: what kronq_gram takes as G.  The calls below are these three
+ * operators, in both directions, for whole prompts packed one behind the other.
+ *
+ * Rotary positions.
+ * kronq_rope_tables: cos and sin (device, `positions` rows of dim / 2 floats,
+ *   leading dimension ld >= dim / 2) of the angles p f_i for p = first .. first +
+ *   positions - 1, both times `magnitude`, computed in fp64 and rounded once.  With
+ *   w_i = base^(-2 i / dim), s = factor, f_i is
+ *     KRONQ_ROPE_PLAIN   w_i
+ *     KRONQ_ROPE_LINEAR  w_i / s
+ *     KRONQ_ROPE_PARTS   keep w_i + (1 - keep) w_i / s, keep = (r - low) / (high -
+ *                        low) held to 0 .. 1, r = original w_i / (2 pi): the turns
+ *                        that the pair makes over the original positions
+ *     KRONQ_ROPE_INDEX   the same with keep = 1 - (i - a) / (b - a) held to 0 .. 1,
+ *                        between the pairs that make `high` and `low` turns: with
+ *                        at(r) = dim log(original / (2 pi r)) / (2 log base),
+ *                        a = max(floor(at(high)), 0), b = min(ceil(at(low)), dim - 1)
+ *                        (b - a at least 0.001)
+ *   dim: even, 2 .. 512; first >= 0, first + positions <= 2^31; base > 1, factor > 0,
+ *   original > 0 and 0 < low < high where they are used, all finite (KRONQ_EINVAL
+ *   otherwise).  kronq_rope takes the tables (dim a multiple of 16).
+ * kronq_rotate: q and k (NULL with k_heads 0: none) turned as kronq_rope describes,
+ *   by the angles of pos (device int32[rows]); with `back` by the transpose, a' =
+ *   a cos + b sin, b' = b cos - a sin: the gradient of the rotation.  Values of a head
+ *   behind the rotated ones are copied.  q_out (k_out) may be q (k) itself with the
+ *   same strides, else they must not overlap.  A row with pos < 0 belongs to no
+ *   sequence: its outputs are left as they were.  One whose position has no row in
+ *   the tables gives NaN.  dim (a head's): a multiple of 16 up to 512
+ *   (KRONQ_EUNSUPPORTED otherwise).  Rows, heads, types and strides as for
+ *   kronq_kv_append.  Arithmetic is fp32, rounded once to dtype.
+ * One launch each, no host synchronization, no memset: may be captured in a HIP
+ * graph (the tables' frequencies are the captured call's, pos is read anew).
+ * ------------------------------------------------------------------------- */
+#define KRONQ_ROPE_PLAIN 0
+#define KRONQ_ROPE_LINEAR 1
+#define KRONQ_ROPE_PARTS 2
+#define KRONQ_ROPE_INDEX 3
+
+typedef struct {
+  double base, factor, original, low, high, magnitude;
+  int32_t scaling;               /* KRONQ_ROPE_* */
+} kronq_rope_scaling;
+
+kronq_status kronq_rope_tables(float* cos, float* sin, int64_t ld, int64_t first, int64_t positions,
+                               int32_t dim, const kronq_rope_scaling* scaling, void* stream);
+kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_heads* k, int32_t k_heads,
+                          int32_t dtype, int64_t rows, int32_t dim, const int32_t* pos,
+                          const kronq_rope* rope, int32_t back, const kronq_heads* q_out,
+                          const kronq_heads* k_out, void* stream);
+
+/* Log probabilities of given tokens.  logits: rows x vocab device, dtype KRONQ_F32,
+ * KRONQ_BF16 or KRONQ_F16, leading dimension ld >= vocab, aligned to an element.
+ * kronq_token_logprobs, for each row l with lse = log sum_v exp(l_v):
+ *   lse     : fp32[rows] (NULL: not wanted)
+ *   logp    : fp32[rows], l_t - lse for t = targets[row] (device int32[rows]).
+ *             A target below 0 is none: logp = 0.  One of at least vocab gives NaN.
+ *             (targets and logp are both NULL or neither.)
+ *   entropy : fp32[rows], -sum_v p_v log p_v (NULL: not wanted)
+ *   top_logp, top_ids : rows x top, fp32 and int32: the `top` (0 .. 64) largest
+ *             l_v - lse in descending order, equal ones by ascending index.
+ *   Logits of minus infinity have probability 0 and no part in the entropy.  A row of
+ *   nothing else gives lse = -inf, logp and top_logp = -inf, entropy 0.  A row with a
+ *   NaN or plus infinity gives NaN, and top_ids -1.
+ *   ws: kronq_token_logprobs_ws(rows, vocab, top) bytes (may be 0), written before it
+ *   is read; calls that overlap in time need one each.
+ * kronq_token_logprobs_grad: from lse as above, and entropy where d_entropy is given,
+ *     out_v = g ([v = t] - p_v) - h p_v (log p_v + entropy)
+ *             + sum_k e_k ([v = top_ids_k] - p_v)
+ *   with g = d_logp, h = d_entropy, e = d_top (rows x top) the gradients of logp,
+ *   entropy and top_logp, fp32 device, each NULL for none (d_logp comes with targets,
+ *   d_entropy with entropy, d_top with top_ids).  Rows without a target have g = 0;
+ *   alternatives below 0 or of at least vocab are none; the same index twice counts
+ *   twice.  A row of lse = -inf gives 0; a target of at least vocab NaN.  out: rows x
+ *   vocab of dtype, leading dimension ld_out; it may be logits itself with ld_out = ld,
+ *   else they must not overlap.  Nothing behind a row's vocab values is written.
+ * Sums are fp32 relative to the row's maximum.  rows at most 2^22, vocab at most 2^24
+ * (KRONQ_EUNSUPPORTED otherwise).  At most two launches, no host synchronization, no
+ * memset: may be captured in a HIP graph; equal calls give equal bits.
+ */
+size_t kronq_token_logprobs_ws(int64_t rows, int64_t vocab, int32_t top);
+kronq_status kronq_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int32_t* targets, float* logp, float* lse, float* entropy,
+                                  int32_t top, float* top_logp, int32_t* top_ids, void* ws,
+                                  size_t ws_bytes, void* stream);
+kronq_status kronq_token_logprobs_grad(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                       int64_t ld, const int32_t* targets, const float* lse,
+                                       const float* entropy, const float* d_logp, const float* d_entropy,
+                                       int32_t top, const int32_t* top_ids, const float* d_top, void* out,
+                                       int64_t ld_out, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Sensitivity (hyper.ai summary, Method, Eq. 14: s = tr(H_G) tr(H_X) computed
  * after BiIP).  out3 (device, 3 doubles) = { tr(HX), tr(HG), tr(HX) * tr(HG) },
  * diagonals summed in fp64.  HX is n x n, HG is m x m (fp32 device).

@@ -38,7 +38,8 @@ EXPORTS = ("kronq_status_string", "kronq_last_error", "kronq_version", "kronq_gr
            "kronq_gptaq_correction", "kronq_gptaq_ws", "kronq_gptaq_quantize", "kronq_biip_sx_ws",
            "kronq_biip_rotate_sx", "kronq_biip_unrotate_sx_ws", "kronq_biip_unrotate_sx",
            "kronq_incoherence_ws", "kronq_incoherence", "kronq_kv_append", "kronq_kv_read",
-           "kronq_kv_attention_ws", "kronq_kv_attention")
+           "kronq_kv_attention_ws", "kronq_kv_attention", "kronq_rope_tables", "kronq_rotate",
+           "kronq_token_logprobs_ws", "kronq_token_logprobs", "kronq_token_logprobs_grad")
 
 
 class KronqError(RuntimeError):
@@ -70,6 +71,11 @@ class _Batch(ctypes.Structure):
 class _Rope(ctypes.Structure):
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("ld", ctypes.c_int64),
                 ("positions", ctypes.c_int64), ("dim", ctypes.c_int32), ("neighbours", ctypes.c_int32)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "original", "low", "high", "magnitude")] + \
+               [("scaling", ctypes.c_int32)]
 
 
 class _Heads(ctypes.Structure):
@@ -192,6 +198,16 @@ def load(path: str = LIB_PATH):
     lib.kronq_kv_attention_ws.restype = sz
     lib.kronq_kv_attention.argtypes = [kvh, i32, i64, i32, kvc, kvb, kvr, f32, i64, i64, kvh, vp, vp, sz, vp]
     lib.kronq_kv_attention.restype = i32
+    lib.kronq_rope_tables.argtypes = [vp, vp, i64, i64, i64, i32, ctypes.POINTER(_RopeScaling), vp]
+    lib.kronq_rope_tables.restype = i32
+    lib.kronq_rotate.argtypes = [kvh, i32, kvh, i32, i32, i64, i32, vp, kvr, i32, kvh, kvh, vp]
+    lib.kronq_rotate.restype = i32
+    lib.kronq_token_logprobs_ws.argtypes = [i64, i64, i32]
+    lib.kronq_token_logprobs_ws.restype = sz
+    lib.kronq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.kronq_token_logprobs.restype = i32
+    lib.kronq_token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, i64, vp]
+    lib.kronq_token_logprobs_grad.restype = i32
     _lib = lib
     return lib
 
@@ -934,3 +950,176 @@ def kronq_kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: f
                                          cache.dim ** -0.5 if scale is None else scale, window, sinks, oh,
                                          _ptr(lse), _ptr(ws), need, st), "kronq_kv_attention")
     return out if lse is None else (out, lse)
+
+
+# ------------------------------------------- calibration pass
+
+ROPE_SCALINGS = ("plain", "linear", "parts", "index")
+
+
+def kronq_rope_tables(positions: int, dim: int, base: float = 10000.0, scaling: str = "plain",
+                      factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 4.0,
+                      magnitude: float = 1.0, neighbours: bool = False, first: int = 0, device=None,
+                      stream=None) -> Rope:
+    """The Rope of positions first .. first + positions - 1 for `dim` rotated
+    values of a head: plain, or scaled for longer contexts (include/kronq.h has
+    the formulas)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("unknown scaling %r" % (scaling,))
+    device = _cuda_device(device)
+    c = _RopeScaling(base, factor, original, low, high, magnitude, ROPE_SCALINGS.index(scaling))
+    st, here = _on_stream(device, stream)
+    with here:
+        if positions < 0 or dim < 2:
+            raise ValueError("positions must be at least 0 and dim at least 2")
+        cos, sin = torch.empty((2, positions, dim // 2), dtype=torch.float32, device=device)
+        _check(load().kronq_rope_tables(cos.data_ptr(), sin.data_ptr(), dim // 2, first, positions, dim,
+                                        ctypes.byref(c), st), "kronq_rope_tables")
+    return Rope(cos, sin, neighbours)
+
+
+def _cuda_device(device):
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("device must be a GPU")
+    return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _ints(t: torch.Tensor, name: str, n: int, device):
+    if t.dtype != torch.int32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d entries on %s" % (name, n, device))
+
+
+def _floats(t: torch.Tensor, name: str, shape, device):
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of shape %s on %s" % (name, tuple(shape), device))
+
+
+def kronq_rotate(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, rope: Rope, back: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """(q, k) turned by the angles of pos (int32, one a row): q (rows, q_heads,
+    dim), k (rows, k_heads, dim) or None.  `back`: by the transpose, which is the
+    gradient.  q_out may be q itself (k_out k); they are made where not given.
+    Rows of pos < 0 are left as they were (undefined when made here)."""
+    dtype, device = q.dtype, q.device
+    if dtype not in _KV_DTYPES:
+        raise ValueError("q must be float32, bfloat16 or float16")
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be (rows, heads, dim) on a GPU")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    rows, qh, dim = q.shape
+    kh = 0
+    qs, ks, ko = _heads3(q, "q", rows, qh, dim, dtype, device), None, None
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be (rows, heads, dim)")
+        kh = k.shape[1]
+        ks = _heads3(k, "k", rows, kh, dim, dtype, device)
+        if k_out is not None:
+            ko = _heads3(k_out, "k_out", rows, kh, dim, dtype, device)
+    qo = None if q_out is None else _heads3(q_out, "q_out", rows, qh, dim, dtype, device)
+    _ints(pos, "pos", rows, device)
+    _same_device(device, rope)
+    st, here = _on_stream(device, stream)
+    with here:
+        if qo is None:
+            q_out, qo = _new_heads3((rows, qh, dim), dtype, device)
+        if k is not None and ko is None:
+            k_out, ko = _new_heads3((rows, kh, dim), dtype, device)
+        _check(load().kronq_rotate(qs, qh, ks, kh, _KV_DTYPES[dtype], rows, dim, pos.data_ptr(), rope._c,
+                                   1 if back else 0, qo, ko, st), "kronq_rotate")
+    return q_out, k_out
+
+
+def _logits(t: torch.Tensor, name: str):
+    """(rows, vocab, leading dimension)"""
+    if t.dtype not in _KV_DTYPES:
+        raise ValueError("%s must be float32, bfloat16 or float16" % name)
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s must be (rows, vocab) on a GPU" % name)
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit stride in its last dimension" % name)
+    return rows, vocab, t.stride(0) if rows > 1 else vocab
+
+
+@functools.lru_cache(maxsize=1024)
+def _token_logprobs_ws(rows: int, vocab: int, top: int) -> int:
+    return load().kronq_token_logprobs_ws(rows, vocab, top)
+
+
+def kronq_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top: int = 0,
+                         want_entropy: bool = False, stream=None, ws: torch.Tensor | None = None) -> dict:
+    """Of each row of logits (rows, vocab): lse, logp of its target (int32, below
+    0: none), entropy when asked for, and with `top` the top_logp and top_ids of
+    its largest (rows, top), equal ones by ascending index.  `ws`: device memory
+    that calls that may run at the same time do not share."""
+    rows, vocab, ld = _logits(logits, "logits")
+    device = logits.device
+    if targets is not None:
+        _ints(targets, "targets", rows, device)
+    need = _token_logprobs_ws(rows, vocab, top)
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device):
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
+    st, here = _on_stream(device, stream)
+    with here:
+        new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
+        got = dict(lse=new(rows))
+        if targets is not None:
+            got["logp"] = new(rows)
+        if want_entropy:
+            got["entropy"] = new(rows)
+        if top > 0:
+            got["top_logp"] = new(rows, top)
+            got["top_ids"] = torch.empty((rows, top), dtype=torch.int32, device=device)
+        if need and (ws is None or ws.numel() < need):
+            ws = _ws(need, device)
+        _check(load().kronq_token_logprobs(logits.data_ptr(), _KV_DTYPES[logits.dtype], rows, vocab, ld,
+                                           _ptr(targets), _ptr(got.get("logp")), got["lse"].data_ptr(),
+                                           _ptr(got.get("entropy")), top, _ptr(got.get("top_logp")),
+                                           _ptr(got.get("top_ids")), _ptr(ws), need, st),
+               "kronq_token_logprobs")
+    return got
+
+
+def kronq_token_logprobs_grad(logits: torch.Tensor, targets: torch.Tensor | None, lse: torch.Tensor,
+                              d_logp: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                              d_entropy: torch.Tensor | None = None, top_ids: torch.Tensor | None = None,
+                              d_top: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """The gradient with respect to logits, in their type, of what
+    kronq_token_logprobs gave: d_logp, d_entropy (rows) and d_top (rows, top) are
+    the gradients of logp, entropy and top_logp, each None for none.  `out` may be
+    logits itself."""
+    rows, vocab, ld = _logits(logits, "logits")
+    device = logits.device
+    if targets is not None:
+        _ints(targets, "targets", rows, device)
+    for t, nm in ((lse, "lse"), (d_logp, "d_logp"), (entropy, "entropy"), (d_entropy, "d_entropy")):
+        if t is not None:
+            _floats(t, nm, (rows,), device)
+    top = 0
+    if d_top is not None:
+        if top_ids is None or top_ids.dim() != 2:
+            raise ValueError("d_top needs top_ids (rows, top)")
+        top = top_ids.shape[1]
+        _floats(d_top, "d_top", (rows, top), device)
+        if top_ids.dtype != torch.int32 or top_ids.shape != (rows, top) or top_ids.device != device or \
+                not top_ids.is_contiguous():
+            raise ValueError("top_ids must be a contiguous int32 tensor of shape (%d, %d) on %s" % (rows, top, device))
+    ld_out = vocab
+    if out is not None:
+        if out.dtype != logits.dtype or out.device != device or out.shape != logits.shape:
+            raise ValueError("out must have the type, shape and device of logits")
+        ld_out = _logits(out, "out")[2]
+    st, here = _on_stream(device, stream)
+    with here:
+        if out is None:
+            out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        _check(load().kronq_token_logprobs_grad(logits.data_ptr(), _KV_DTYPES[logits.dtype], rows, vocab, ld,
+                                                _ptr(targets), lse.data_ptr(), _ptr(entropy), _ptr(d_logp),
+                                                _ptr(d_entropy), top, _ptr(top_ids) if top else None,
+                                                _ptr(d_top) if top else None, out.data_ptr(), ld_out, st),
+               "kronq_token_logprobs_grad")
+    return out

@@ -9,6 +9,8 @@
 
 #include "kronq_internal.h"
 #include "kv.h"
+#include "logprobs.h"
+#include "rope.h"
 
 namespace kronq {
 
@@ -678,6 +680,112 @@ kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t row
   const int64_t room = room_of(c);      // a window of all positions is none
   return kv_attention_launch(c, cache->dim, dtype, qv, q_heads, r, scale, window < room ? (int)window : 0,
                              (int)std::min(sinks, room), ov, lse, ws, (hipStream_t)stream);
+}
+
+kronq_status kronq_rope_tables(float* cos, float* sin, int64_t ld, int64_t first, int64_t positions, int32_t dim,
+                               const kronq_rope_scaling* scaling, void* stream) {
+  const char* fn = "kronq_rope_tables";
+  if (!scaling) return fail(KRONQ_EINVAL, "%s: NULL pointer", fn);
+  const kronq_rope_scaling& c = *scaling;
+  if (dim < 2 || dim % 2 || dim > 2 * kRopePairs || ld < dim / 2)
+    return fail(KRONQ_EINVAL, "%s: dim %d (even, 2..%d) or ld", fn, (int)dim, 2 * kRopePairs);
+  if (first < 0 || positions < 0 || first > (int64_t(1) << 31) || positions > (int64_t(1) << 31) - first)
+    return fail(KRONQ_EINVAL, "%s: bad positions", fn);
+  if (c.scaling < KRONQ_ROPE_PLAIN || c.scaling > KRONQ_ROPE_INDEX)
+    return fail(KRONQ_EINVAL, "%s: scaling %d", fn, (int)c.scaling);
+  if (!(c.base > 1) || !std::isfinite(c.base) || !std::isfinite(c.magnitude) || !(c.factor > 0) ||
+      !std::isfinite(c.factor))
+    return fail(KRONQ_EINVAL, "%s: base, factor or magnitude", fn);
+  if (c.scaling >= KRONQ_ROPE_PARTS &&
+      (!(c.original > 0) || !std::isfinite(c.original) || !(c.low > 0) || !(c.high > c.low) || !std::isfinite(c.high)))
+    return fail(KRONQ_EINVAL, "%s: original must be > 0 and 0 < low < high", fn);
+  if (positions == 0) return KRONQ_OK;
+  if (!cos || !sin) return fail(KRONQ_EINVAL, "%s: NULL pointer", fn);
+  return rope_tables_launch(cos, sin, ld, first, positions, dim, c, (hipStream_t)stream);
+}
+
+kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_heads* k, int32_t k_heads,
+                          int32_t dtype, int64_t rows, int32_t dim, const int32_t* pos, const kronq_rope* rope,
+                          int32_t back, const kronq_heads* q_out, const kronq_heads* k_out, void* stream) {
+  const char* fn = "kronq_rotate";
+  if (q_heads < 1 || k_heads < 0) return fail(KRONQ_EINVAL, "%s: %d and %d heads", fn, (int)q_heads, (int)k_heads);
+  kronq_status st = kv_rows(fn, dtype, rows, (int64_t)q_heads + k_heads);
+  if (st) return st;
+  if (dim < 1) return fail(KRONQ_EINVAL, "%s: dim %d", fn, (int)dim);
+  if (dim % 16 || dim > 2 * kRopePairs)
+    return fail(KRONQ_EUNSUPPORTED, "%s: dim %d is not a multiple of 16 up to %d", fn, (int)dim, 2 * kRopePairs);
+  RopeView r;
+  if (!rope) return fail(KRONQ_EINVAL, "%s: rope is NULL", fn);
+  if ((st = kv_rope(fn, rope, dim, &r))) return st;
+  if (rows == 0) return KRONQ_OK;
+  if (!pos) return fail(KRONQ_EINVAL, "%s: pos is NULL", fn);
+  HeadsView in[2] = {}, out[2] = {};
+  const int heads[2] = {q_heads, k_heads};
+  const char* names[4] = {"q", "k", "q_out", "k_out"};
+  for (int w = 0; w < (k_heads ? 2 : 1); ++w) {
+    if ((st = kv_heads(fn, names[w], w ? k : q, dtype, dim, &in[w]))) return st;
+    if ((st = kv_heads(fn, names[2 + w], w ? k_out : q_out, dtype, dim, &out[w]))) return st;
+    if (in[w].data == out[w].data && (in[w].row != out[w].row || in[w].head != out[w].head))
+      return fail(KRONQ_EINVAL, "%s: %s is %s with other strides", fn, names[2 + w], names[w]);
+  }
+  return rotate_launch(in, out, heads, dtype, rows, dim, pos, r, back, (hipStream_t)stream);
+}
+
+static kronq_status logits_check(const char* fn, const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                 int64_t ld, int32_t top) {
+  if (dtype != KRONQ_F32 && dtype != KRONQ_BF16 && dtype != KRONQ_F16)
+    return fail(KRONQ_EINVAL, "%s: dtype %d", fn, (int)dtype);
+  if (rows < 0 || vocab < 1 || ld < vocab) return fail(KRONQ_EINVAL, "%s: bad shape", fn);
+  if (top < 0 || top > vocab) return fail(KRONQ_EINVAL, "%s: top %d of %lld", fn, (int)top, (long long)vocab);
+  if (rows > (int64_t(1) << 22) || vocab > (int64_t(1) << 24) || top > kTopMost)
+    return fail(KRONQ_EUNSUPPORTED, "%s: at most 2^22 rows, 2^24 values a row and %d alternatives", fn, kTopMost);
+  if (rows > 0 && (!logits || !aligned(logits, (size_t)kv_elem(dtype))))
+    return fail(KRONQ_EINVAL, "%s: logits is NULL or not aligned to an element", fn);
+  return KRONQ_OK;
+}
+
+size_t kronq_token_logprobs_ws(int64_t rows, int64_t vocab, int32_t top) {
+  if (rows < 1 || vocab < 1 || rows > (int64_t(1) << 22) || vocab > (int64_t(1) << 24) || top < 0 || top > kTopMost)
+    return 0;
+  return logprobs_ws_bytes(rows, vocab, top);
+}
+
+kronq_status kronq_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int32_t* targets, float* logp, float* lse, float* entropy, int32_t top,
+                                  float* top_logp, int32_t* top_ids, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "kronq_token_logprobs";
+  kronq_status st = logits_check(fn, logits, dtype, rows, vocab, ld, top);
+  if (st) return st;
+  if (rows == 0) return KRONQ_OK;
+  if (!targets != !logp) return fail(KRONQ_EINVAL, "%s: targets without logp, or the reverse", fn);
+  if (top > 0 && (!top_logp || !top_ids)) return fail(KRONQ_EINVAL, "%s: top_logp or top_ids is NULL", fn);
+  const size_t need = logprobs_ws_bytes(rows, vocab, top);
+  if ((st = check_ws(fn, ws, ws_bytes, need, need > 0))) return st;
+  const LogprobsArgs a{logits, ld, targets, rows, (int)vocab, top, logp, lse, entropy, top_logp, top_ids};
+  return logprobs_launch(a, dtype, ws, (hipStream_t)stream);
+}
+
+kronq_status kronq_token_logprobs_grad(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                       const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* d_logp, const float* d_entropy, int32_t top,
+                                       const int32_t* top_ids, const float* d_top, void* out, int64_t ld_out,
+                                       void* stream) {
+  const char* fn = "kronq_token_logprobs_grad";
+  kronq_status st = logits_check(fn, logits, dtype, rows, vocab, ld, top);
+  if (st) return st;
+  if (ld_out < vocab) return fail(KRONQ_EINVAL, "%s: ld_out below vocab", fn);
+  if (rows == 0) return KRONQ_OK;
+  if (!lse || !out || !aligned(out, (size_t)kv_elem(dtype)))
+    return fail(KRONQ_EINVAL, "%s: lse or out is NULL, or out not aligned to an element", fn);
+  if (out == logits && ld_out != ld) return fail(KRONQ_EINVAL, "%s: out is logits with another ld", fn);
+  if (d_logp && !targets) return fail(KRONQ_EINVAL, "%s: d_logp without targets", fn);
+  if (d_entropy && !entropy) return fail(KRONQ_EINVAL, "%s: d_entropy without entropy", fn);
+  if (top > 0 && d_top && !top_ids) return fail(KRONQ_EINVAL, "%s: d_top without top_ids", fn);
+  if (logprobs_grad_grid(rows, vocab) > INT32_MAX)
+    return fail(KRONQ_EUNSUPPORTED, "%s: %lld rows of %lld values", fn, (long long)rows, (long long)vocab);
+  const LogprobsGradArgs a{logits, ld, targets, rows, (int)vocab, d_top ? top : 0, lse, entropy, d_logp, d_entropy,
+                           top > 0 ? d_top : nullptr, top_ids, out, ld_out};
+  return logprobs_grad_launch(a, dtype, (hipStream_t)stream);
 }
 
 kronq_status kronq_sensitivity(const float* HX, int64_t n, int64_t ldhx, const float* HG,
