@@ -675,6 +675,53 @@ kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_hea
                           const kronq_rope* rope, int32_t back, const kronq_heads* q_out,
                           const kronq_heads* k_out, void* stream);
 
+/* Causal attention over whole prompts, packed one behind the other.
+ *   cu (device int32[seqs + 1], not decreasing): rows cu[i] .. cu[i + 1] - 1 of q, k, v
+ *   and the outputs are sequence i's, its positions 0 and up.  Row i sees row j of its
+ *   sequence when j <= i and (window == 0 or j > i - window).  Query head h reads key
+ *   head h / (q_heads / heads).
+ * kronq_prompt_attention:
+ *     out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j - max)
+ *     lse = max + log(sum_j w_j)   (natural logarithm, rows x q_heads fp32, contiguous;
+ *                                   NULL: not wanted)
+ * kronq_prompt_attention_grad: from dout, the gradient of out, and out and lse as the
+ *   call above gave them: with p = exp(scale q . k_j - lse), delta = dout . out
+ *     dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i)
+ *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ *   where the sums of dv and dk go over all query heads of a key head.
+ * q, out, dout, dq: rows x q_heads heads of dtype (KRONQ_F32, KRONQ_BF16, KRONQ_F16);
+ *   k, v, dk, dv: rows x heads.  Outputs must not overlap each other or what is read.
+ *   Row strides at most 2^22 elements.
+ * dim: a multiple of 8 up to 256 (64, 128 and 256 as they are, others in the next larger
+ *   of these); q_heads a multiple of heads; at most 2^22 rows, 2^26 rows x heads, 2^14
+ *   sequences (KRONQ_EUNSUPPORTED otherwise).
+ * scale: > 0 and finite; scores, and lse / scale, have to be numbers that fp32 holds.
+ * A row of no sequence is not read, and its outputs are left as they were.  Nothing
+ * outside the caller's buffers is touched whatever cu holds.  What k, v (grad: q and
+ * dout too) hold in rows that a row does not see has no part in its outputs, be it a NaN
+ * or an infinity; what it sees of these reaches it as in the formula (in dq and dk as a
+ * NaN).
+ * Products of KRONQ_F32 are fp32's own; of the others the matrix cores', with weights
+ * and ds rounded to dtype (for KRONQ_F16 held times a power of two that follows the
+ * largest of a row's or a key's, so that small gradients keep their precision).  Scores,
+ * statistics and sums are fp32.
+ * ws: kronq_prompt_attention_grad_ws(rows, q_heads) bytes, written before it is read;
+ * calls that overlap in time need one each.
+ * One launch (grad: three), no host synchronization, no memset, no atomics: may be
+ * captured in a HIP graph, replays read cu anew, and equal calls give equal bits.
+ */
+kronq_status kronq_prompt_attention(const kronq_heads* q, const kronq_heads* k, const kronq_heads* v,
+                                    int32_t dtype, int64_t rows, int32_t q_heads, int32_t heads, int32_t dim,
+                                    const int32_t* cu, int32_t seqs, float scale, int64_t window,
+                                    const kronq_heads* out, float* lse, void* stream);
+size_t kronq_prompt_attention_grad_ws(int64_t rows, int32_t q_heads);
+kronq_status kronq_prompt_attention_grad(const kronq_heads* dout, const kronq_heads* q, const kronq_heads* k,
+                                         const kronq_heads* v, const kronq_heads* out, const float* lse,
+                                         int32_t dtype, int64_t rows, int32_t q_heads, int32_t heads,
+                                         int32_t dim, const int32_t* cu, int32_t seqs, float scale,
+                                         int64_t window, const kronq_heads* dq, const kronq_heads* dk,
+                                         const kronq_heads* dv, void* ws, size_t ws_bytes, void* stream);
+
 /* Log probabilities of given tokens.  logits: rows x vocab device, dtype KRONQ_F32,
  * KRONQ_BF16 or KRONQ_F16, leading dimension ld >= vocab, aligned to an element.
  * kronq_token_logprobs, for each row l with lse = log sum_v exp(l_v):

@@ -39,7 +39,8 @@ EXPORTS = ("kronq_status_string", "kronq_last_error", "kronq_version", "kronq_gr
            "kronq_biip_rotate_sx", "kronq_biip_unrotate_sx_ws", "kronq_biip_unrotate_sx",
            "kronq_incoherence_ws", "kronq_incoherence", "kronq_kv_append", "kronq_kv_read",
            "kronq_kv_attention_ws", "kronq_kv_attention", "kronq_rope_tables", "kronq_rotate",
-           "kronq_token_logprobs_ws", "kronq_token_logprobs", "kronq_token_logprobs_grad")
+           "kronq_token_logprobs_ws", "kronq_token_logprobs", "kronq_token_logprobs_grad",
+           "kronq_prompt_attention", "kronq_prompt_attention_grad_ws", "kronq_prompt_attention_grad")
 
 
 class KronqError(RuntimeError):
@@ -208,6 +209,13 @@ def load(path: str = LIB_PATH):
     lib.kronq_token_logprobs.restype = i32
     lib.kronq_token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, i64, vp]
     lib.kronq_token_logprobs_grad.restype = i32
+    lib.kronq_prompt_attention.argtypes = [kvh, kvh, kvh, i32, i64, i32, i32, i32, vp, i32, f32, i64, kvh, vp, vp]
+    lib.kronq_prompt_attention.restype = i32
+    lib.kronq_prompt_attention_grad_ws.argtypes = [i64, i32]
+    lib.kronq_prompt_attention_grad_ws.restype = sz
+    lib.kronq_prompt_attention_grad.argtypes = [kvh, kvh, kvh, kvh, kvh, vp, i32, i64, i32, i32, i32, vp, i32, f32,
+                                                i64, kvh, kvh, kvh, vp, sz, vp]
+    lib.kronq_prompt_attention_grad.restype = i32
     _lib = lib
     return lib
 
@@ -1030,6 +1038,80 @@ def kronq_rotate(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, rop
         _check(load().kronq_rotate(qs, qh, ks, kh, _KV_DTYPES[dtype], rows, dim, pos.data_ptr(), rope._c,
                                    1 if back else 0, qo, ko, st), "kronq_rotate")
     return q_out, k_out
+
+
+def _prompt_shapes(q: torch.Tensor, k: torch.Tensor, cu: torch.Tensor):
+    """(rows, q_heads, heads, dim, seqs)"""
+    if q.dtype not in _KV_DTYPES:
+        raise ValueError("q must be float32, bfloat16 or float16")
+    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
+        raise ValueError("q and k must be (rows, heads, dim) on a GPU")
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("cu must have seqs + 1 entries")
+    _ints(cu, "cu", cu.shape[0], q.device)
+    return *q.shape[:2], k.shape[1], q.shape[2], cu.shape[0] - 1
+
+
+def kronq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
+                           scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                           want_lse: bool = False, lse: torch.Tensor | None = None, stream=None):
+    """Causal attention over packed prompts: rows cu[i] .. cu[i + 1] - 1 (cu int32)
+    of q (rows, q_heads, dim), k and v (rows, heads, dim) are sequence i's.  out in
+    q's dtype, or (out, lse) when lse is asked for.  Rows of no sequence are left as
+    they were (undefined when made here)."""
+    rows, qheads, heads, dim, seqs = _prompt_shapes(q, k, cu)
+    dtype, device = q.dtype, q.device
+    qh = _heads3(q, "q", rows, qheads, dim, dtype, device)
+    kh, vh = _heads3(k, "k", rows, heads, dim, dtype, device), _heads3(v, "v", rows, heads, dim, dtype, device)
+    oh = None if out is None else _heads3(out, "out", rows, qheads, dim, dtype, device)
+    if lse is not None:
+        _floats(lse, "lse", (rows, qheads), device)
+    st, here = _on_stream(device, stream)
+    with here:
+        if oh is None:
+            out, oh = _new_heads3((rows, qheads, dim), dtype, device)
+        if lse is None and want_lse:
+            lse = torch.empty((rows, qheads), dtype=torch.float32, device=device)
+        _check(load().kronq_prompt_attention(qh, kh, vh, _KV_DTYPES[dtype], rows, qheads, heads, dim, cu.data_ptr(),
+                                             seqs, dim ** -0.5 if scale is None else scale, window, oh, _ptr(lse),
+                                             st), "kronq_prompt_attention")
+    return out if lse is None else (out, lse)
+
+
+def kronq_prompt_attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                out: torch.Tensor, lse: torch.Tensor, cu: torch.Tensor,
+                                scale: float | None = None, window: int = 0, dq: torch.Tensor | None = None,
+                                dk: torch.Tensor | None = None, dv: torch.Tensor | None = None, stream=None,
+                                ws: torch.Tensor | None = None):
+    """(dq, dk, dv) from dout, the gradient of out, and what kronq_prompt_attention
+    was given and gave.  Rows of no sequence are left as they were (undefined when
+    made here).  `ws`: device memory that calls that may run at the same time do not
+    share."""
+    rows, qheads, heads, dim, seqs = _prompt_shapes(q, k, cu)
+    dtype, device = q.dtype, q.device
+    wide, narrow = (rows, qheads, dim), (rows, heads, dim)
+    h = [_heads3(t, nm, *shape, dtype, device)
+         for t, nm, shape in ((dout, "dout", wide), (q, "q", wide), (k, "k", narrow), (v, "v", narrow), (out, "out", wide))]
+    g = [None if t is None else _heads3(t, nm, *shape, dtype, device)
+         for t, nm, shape in ((dq, "dq", wide), (dk, "dk", narrow), (dv, "dv", narrow))]
+    _floats(lse, "lse", (rows, qheads), device)
+    need = load().kronq_prompt_attention_grad_ws(rows, qheads)
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device):
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
+    st, here = _on_stream(device, stream)
+    with here:
+        if dq is None:
+            dq, g[0] = _new_heads3(wide, dtype, device)
+        if dk is None:
+            dk, g[1] = _new_heads3(narrow, dtype, device)
+        if dv is None:
+            dv, g[2] = _new_heads3(narrow, dtype, device)
+        if need and (ws is None or ws.numel() < need):
+            ws = _ws(need, device)
+        _check(load().kronq_prompt_attention_grad(*h, lse.data_ptr(), _KV_DTYPES[dtype], rows, qheads, heads, dim,
+                                                  cu.data_ptr(), seqs, dim ** -0.5 if scale is None else scale, window,
+                                                  *g, _ptr(ws), need, st), "kronq_prompt_attention_grad")
+    return dq, dk, dv
 
 
 def _logits(t: torch.Tensor, name: str):

@@ -10,6 +10,7 @@
 #include "kronq_internal.h"
 #include "kv.h"
 #include "logprobs.h"
+#include "prompt.h"
 #include "rope.h"
 
 namespace kronq {
@@ -729,6 +730,91 @@ kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_hea
       return fail(KRONQ_EINVAL, "%s: %s is %s with other strides", fn, names[2 + w], names[w]);
   }
   return rotate_launch(in, out, heads, dtype, rows, dim, pos, r, back, (hipStream_t)stream);
+}
+
+// What both directions of prompt attention check; the views of the operands named.
+static kronq_status prompt_view(const char* fn, int32_t dtype, int64_t rows, int32_t q_heads, int32_t heads,
+                                int32_t dim, const int32_t* cu, int32_t seqs, float scale, int64_t window,
+                                PromptArgs* a) {
+  if (heads < 1 || q_heads < 1 || q_heads % heads)
+    return fail(KRONQ_EINVAL, "%s: %d query heads on %d key heads", fn, (int)q_heads, (int)heads);
+  kronq_status st = kv_rows(fn, dtype, rows, q_heads);
+  if (st) return st;
+  if (dim < 1 || seqs < 0 || window < 0) return fail(KRONQ_EINVAL, "%s: dim, seqs or window", fn);
+  if (dim % 8 || dim > 256) return fail(KRONQ_EUNSUPPORTED, "%s: dim %d is not a multiple of 8 up to 256", fn, (int)dim);
+  if (seqs > kAttnSeqs) return fail(KRONQ_EUNSUPPORTED, "%s: %d sequences (at most 2^14)", fn, (int)seqs);
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(KRONQ_EINVAL, "%s: scale must be finite and > 0", fn);
+  if (rows > 0 && seqs > 0 && !cu) return fail(KRONQ_EINVAL, "%s: cu is NULL", fn);
+  // tiles of 128 rows, one a sequence more: the launch's workgroups
+  if ((rows / 128 + seqs) * q_heads > INT32_MAX)
+    return fail(KRONQ_EUNSUPPORTED, "%s: %d sequences of %d heads", fn, (int)seqs, (int)q_heads);
+  *a = PromptArgs{};
+  a->cu = cu;
+  a->seqs = seqs;
+  a->rows = (int)rows;
+  a->heads = heads;
+  a->share = q_heads / heads;
+  a->dim = dim;
+  a->scale = scale;
+  a->window = window < rows ? (int)window : 0;   // a window of all rows is none
+  return KRONQ_OK;
+}
+
+static kronq_status prompt_heads(const char* fn, const char* what, const kronq_heads* h, int32_t dtype, int32_t dim,
+                                 HeadsView* out) {
+  const kronq_status st = kv_heads(fn, what, h, dtype, dim, out);
+  if (st) return st;
+  if (h->row_stride > (int64_t(1) << 22))
+    return fail(KRONQ_EUNSUPPORTED, "%s: row stride %lld of %s (at most 2^22)", fn, (long long)h->row_stride, what);
+  return KRONQ_OK;
+}
+
+kronq_status kronq_prompt_attention(const kronq_heads* q, const kronq_heads* k, const kronq_heads* v, int32_t dtype,
+                                    int64_t rows, int32_t q_heads, int32_t heads, int32_t dim, const int32_t* cu,
+                                    int32_t seqs, float scale, int64_t window, const kronq_heads* out, float* lse,
+                                    void* stream) {
+  const char* fn = "kronq_prompt_attention";
+  PromptArgs a;
+  kronq_status st = prompt_view(fn, dtype, rows, q_heads, heads, dim, cu, seqs, scale, window, &a);
+  if (st) return st;
+  if (rows == 0 || seqs == 0) return KRONQ_OK;
+  if ((st = prompt_heads(fn, "q", q, dtype, dim, &a.q))) return st;
+  if ((st = prompt_heads(fn, "k", k, dtype, dim, &a.k))) return st;
+  if ((st = prompt_heads(fn, "v", v, dtype, dim, &a.v))) return st;
+  if ((st = prompt_heads(fn, "out", out, dtype, dim, &a.out))) return st;
+  a.lse = lse;
+  return prompt_attention_launch(a, dtype, (hipStream_t)stream);
+}
+
+size_t kronq_prompt_attention_grad_ws(int64_t rows, int32_t q_heads) {
+  if (rows < 1 || q_heads < 1 || q_heads > 65535 || rows > (int64_t(1) << 22) || rows * q_heads > (int64_t(1) << 26))
+    return 0;
+  return prompt_grad_ws_bytes(rows, q_heads);
+}
+
+kronq_status kronq_prompt_attention_grad(const kronq_heads* dout, const kronq_heads* q, const kronq_heads* k,
+                                         const kronq_heads* v, const kronq_heads* out, const float* lse,
+                                         int32_t dtype, int64_t rows, int32_t q_heads, int32_t heads, int32_t dim,
+                                         const int32_t* cu, int32_t seqs, float scale, int64_t window,
+                                         const kronq_heads* dq, const kronq_heads* dk, const kronq_heads* dv,
+                                         void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "kronq_prompt_attention_grad";
+  PromptArgs a;
+  kronq_status st = prompt_view(fn, dtype, rows, q_heads, heads, dim, cu, seqs, scale, window, &a);
+  if (st) return st;
+  if (rows == 0 || seqs == 0) return KRONQ_OK;
+  if (!lse) return fail(KRONQ_EINVAL, "%s: lse is NULL", fn);
+  const struct { const char* name; const kronq_heads* h; HeadsView* to; } all[] = {
+      {"dout", dout, &a.dout}, {"q", q, &a.q}, {"k", k, &a.k}, {"v", v, &a.v}, {"out", out, &a.out},
+      {"dq", dq, &a.dq}, {"dk", dk, &a.dk}, {"dv", dv, &a.dv}};
+  for (const auto& x : all)
+    if ((st = prompt_heads(fn, x.name, x.h, dtype, dim, x.to))) return st;
+  const size_t need = prompt_grad_ws_bytes(rows, q_heads);
+  if ((st = check_ws(fn, ws, ws_bytes, need, true))) return st;
+  a.lse = const_cast<float*>(lse);
+  a.neg_lse = static_cast<float*>(ws);
+  a.neg_delta = a.neg_lse + rows * q_heads;
+  return prompt_grad_launch(a, dtype, (hipStream_t)stream);
 }
 
 static kronq_status logits_check(const char* fn, const void* logits, int32_t dtype, int64_t rows, int64_t vocab,

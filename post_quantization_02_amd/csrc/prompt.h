@@ -1,0 +1,413 @@
+// What the kernels of attention over whole packed prompts share: where a workgroup
+// works, matrix operands of each type, tiles in LDS.
+//
+// All products are laid out so that a lane's column is its own: a 32 x 32 block of
+// weights W^T has, in lane (c, h) (c = lane % 32, h = lane / 32), column c and rows
+//   row(x, h) = x % 4 + 8 (x / 4) + 4 h,  x = 0 .. 15,
+// and that is what the next product wants as its second operand, as long as its
+// first operand's k slots are given the same order: weights never leave their
+// registers, and statistics of a column are a lane's own.
+#pragma once
+
+#include <cfloat>
+#include <type_traits>
+#include <utility>
+
+#include "kv.h"
+
+namespace kronq {
+
+struct PromptArgs {
+  HeadsView q, k, v, out, dout, dq, dk, dv;
+  float* lse;               // rows x q_heads (forwards: NULL if not wanted)
+  float *neg_lse, *neg_delta;   // backwards, workspace: q_heads x rows, -lse / scale and -sum dO O
+  const int32_t* cu;
+  int seqs, rows, heads, share, dim;
+  float scale;              // > 0
+  int window;               // 0: none
+};
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kPromptLog2e = 1.44269504088896340736f, kPromptLn2 = 0.69314718055994530942f;
+
+// ---------------------------------------------------------------- where a workgroup works
+
+// Rows of sequence b that there are: cu may hold anything.
+struct Prompt { int start, n; };
+
+__device__ __forceinline__ Prompt prompt_of(const PromptArgs& a, int b) {
+  const int lo = min(max(a.cu[b], 0), a.rows), hi = min(a.cu[b + 1], a.rows);
+  return {lo, max(hi - lo, 0)};
+}
+
+// Tile number `unit` of all sequences' tiles of bm rows: its sequence, and which of
+// its tiles, counted from the last one (late rows see most: they come first).
+// False: there are fewer.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit, Prompt& p, int& tile) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+    Prompt mine{0, 0};
+    if (b0 + lane < a.seqs) mine = prompt_of(a, b0 + lane);
+    const int tiles = (mine.n + bm - 1) / bm;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(upto, o);
+      upto += lane >= o ? y : 0;
+    }
+    const uint64_t past = __ballot(before + upto > unit);
+    if (past) {
+      const int at = __ffsll((unsigned long long)past) - 1;
+      p.start = __builtin_amdgcn_readlane(mine.start, at);
+      p.n = __builtin_amdgcn_readlane(mine.n, at);
+      tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - unit;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------- operands
+
+// EPL: values of a lane in one product (16 bytes); STEP: k of a product.
+template <typename T>
+struct Op;
+
+template <>
+struct Op<bf16_t> {
+  typedef s16x8 frag;
+  static constexpr int EPL = 8, STEP = 16;
+  __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  __device__ static frag pack(const float* w) {
+    bf16x8 f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (__bf16)w[i];
+    return __builtin_bit_cast(frag, f);
+  }
+  // any exponent of all ones
+  __device__ static bool odd(u32x4 w) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7F80u) == 0x7F80u) | ((w[i] & 0x7F800000u) == 0x7F800000u);
+    return bad;
+  }
+};
+
+template <>
+struct Op<_Float16> {
+  typedef s16x8 frag;
+  static constexpr int EPL = 8, STEP = 16;
+  __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  }
+  __device__ static frag pack(const float* w) {
+    half8_t f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (_Float16)w[i];
+    return __builtin_bit_cast(frag, f);
+  }
+  __device__ static bool odd(u32x4 w) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7C00u) == 0x7C00u) | ((w[i] & 0x7C000000u) == 0x7C000000u);
+    return bad;
+  }
+};
+
+// fp32 as it is: four products of k 2 a step
+template <>
+struct Op<float> {
+  typedef f32x4 frag;
+  static constexpr int EPL = 4, STEP = 8;
+  __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static frag pack(const float* w) { return frag{w[0], w[1], w[2], w[3]}; }
+  __device__ static bool odd(u32x4 w) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
+    return bad;
+  }
+};
+
+// Row of a 32 x 32 block that register x holds.
+__device__ constexpr int block_row(int x, int h) { return (x & 3) + 8 * (x >> 2) + 4 * h; }
+
+// f(0), .., f(N - 1), each with a constant.
+template <typename F, int... I>
+__device__ __forceinline__ void prompt_each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void prompt_each(F f) {
+  prompt_each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Largest of a column: both halves hold some of its rows.
+__device__ __forceinline__ float both_max(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
+__device__ __forceinline__ float both_sum(float x) { return x + __shfl_xor(x, 32); }
+
+// ---------------------------------------------------------------- tiles in LDS
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// A tile's place in LDS.
+template <typename Tile>
+__device__ __forceinline__ uint32_t lds_at(const Tile& t) { return (uint32_t)(uintptr_t)(lds_u8*)&t; }
+
+// Hides where a value comes from, so that what is added to it in a loop is added
+// there: kept in a register each, those sums would leave none for the work.
+__device__ __forceinline__ uint32_t hidden(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at) {
+  return *(const __attribute__((address_space(3))) V*)(uintptr_t)at;
+}
+
+// ROWS rows of D values (D a power of two; what a head has fewer is 0), in 16-byte
+// pieces that are exchanged within a row, piece c of a row at c ^ turn(row), so that
+//   sixteen neighbouring rows' same pieces, and
+//   four neighbouring pieces of rows 4 i .. 4 i + 3 (transposing reads)
+// each lie in all 64 banks.  A lane's places are then one number, with a constant
+// exclusive-or'd and a constant added for each read: tiles start at whole KiB.
+template <typename T, int D, int ROWS>
+struct LdsTile {
+  static constexpr int PIECES = D * (int)sizeof(T) / 16, BYTES = D * (int)sizeof(T);
+  alignas(1024) uint8_t b[ROWS * BYTES];
+
+  __device__ static constexpr int turn(int row) {
+    if (PIECES == 8) {                    // two rows in the banks
+      const int m = (row >> 1) & 7;
+      return (m & 1) << 2 | m >> 1;
+    }
+    return (row & 3) << 2 | ((row >> 2) & 3);
+  }
+
+  // This lane's number for rows_by_d: row c, piece h.
+  __device__ static __forceinline__ uint32_t rows_lane() {
+    const int lane = threadIdx.x & 63, row = lane & 31;
+    return (uint32_t)(row * BYTES + (((lane >> 5) ^ turn(row)) << 4));
+  }
+  // First operand, rows r0 .. r0 + 31 by D, step s (of 2 pieces)
+  __device__ static __forceinline__ typename Op<T>::frag rows_by_d(uint32_t at, int r0, int s) {
+    return lds_read<typename Op<T>::frag>((at ^ (uint32_t)(2 * s) << 4) + (uint32_t)(r0 * BYTES));
+  }
+
+  // This lane's number for d_by_rows.
+  __device__ static __forceinline__ uint32_t d_lane() {
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {       // rows 4 h .. 4 h + 3, a 16-lane group's two pieces
+      const int row = 4 * h + ((lane >> 2) & 3), c = ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+      return (uint32_t)(row * BYTES + ((c ^ turn(row)) << 4) + (lane & 1) * 8);
+    } else {                              // row 4 h, value c
+      return (uint32_t)(4 * h * BYTES + ((((lane & 31) >> 2) ^ turn(4 * h)) << 4) + (lane & 3) * 4);
+    }
+  }
+  // First operand, values 32 dt .. 32 dt + 31 by rows r0 .. r0 + 31 (transposed), step s;
+  // its k slots in the order that a block of weights has
+  __device__ static __forceinline__ typename Op<T>::frag d_by_rows(uint32_t at, int r0, int dt, int s) {
+    if constexpr (sizeof(T) == 2) {
+      // rows 8 further turn by 2 more
+      const uint32_t lo_at = (at ^ (uint32_t)(4 * dt) << 4) + (uint32_t)((r0 + 16 * s) * BYTES);
+      const uint32_t hi_at = (at ^ (uint32_t)(4 * dt ^ 2) << 4) + (uint32_t)((r0 + 16 * s + 8) * BYTES);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)lo_at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)hi_at);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      f32x4 f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = lds_read<float>((at ^ (uint32_t)(8 * dt ^ turn(8 * s + i)) << 4) + (uint32_t)((r0 + 8 * s + i) * BYTES));
+      return f;
+    }
+  }
+};
+
+// A tile on its way from memory to LDS: a workgroup of NT threads, 16 bytes a thread
+// and load.
+template <typename T, int D, int ROWS, int NT>
+struct Staged {
+  typedef LdsTile<T, D, ROWS> Tile;
+  static constexpr int EACH = ROWS * Tile::PIECES / NT, APART = NT / Tile::PIECES;
+  static_assert(EACH * NT == ROWS * Tile::PIECES && APART * EACH == ROWS, "whole rows");
+  static_assert((APART & (APART - 1)) == 0 && APART >= 4, "turns of rows APART further are a constant's");
+  u32x4 w[EACH];
+
+  // rows `row` .. of a head's n (row < n); `dim` of D values
+  __device__ __forceinline__ void load(const HeadsView& x, int64_t first, int head, int row, int n, int dim) {
+    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x / Tile::PIECES;
+    const char* base = static_cast<const char*>(x.data) + ((first + row) * x.row + head * x.head) * (int64_t)sizeof(T);
+    const uint32_t stride = (uint32_t)x.row * (uint32_t)sizeof(T), mine = (uint32_t)r * stride + (uint32_t)c * 16;
+    if (row + ROWS <= n && dim == D) {
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) w[i] = *reinterpret_cast<const u32x4*>(base + (uint64_t)i * APART * stride + mine);
+    } else {
+      const bool in = c * Op<T>::EPL < dim;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const bool ok = in && row + r + i * APART < n;
+        const u32x4 y = *reinterpret_cast<const u32x4*>(base + (ok ? (uint32_t)(i * APART) * stride + mine : 0u));
+        w[i] = ok ? y : u32x4{0, 0, 0, 0};
+      }
+    }
+  }
+  // This thread's number for store.
+  __device__ static __forceinline__ uint32_t lane() {
+    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x / Tile::PIECES;
+    return (uint32_t)(r * Tile::BYTES + ((c ^ Tile::turn(r)) << 4));
+  }
+  __device__ __forceinline__ void store(uint32_t at) const {
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+      *(__attribute__((address_space(3))) u32x4*)(uintptr_t)((at ^ (uint32_t)Tile::turn(i * APART) << 4) +
+                                                             (uint32_t)(i * APART * Tile::BYTES)) = w[i];
+  }
+  __device__ __forceinline__ bool odd() const {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) bad |= Op<T>::odd(w[i]);
+    return bad;
+  }
+};
+
+// Second operand, D by a lane's column: row `row` of a head (0 where row >= n).
+template <typename T, int D>
+__device__ __forceinline__ void load_column(const HeadsView& x, int64_t first, int head, int row, int n, int dim,
+                                            typename Op<T>::frag (&f)[D / Op<T>::STEP]) {
+  typedef typename Op<T>::frag frag;
+  const int h = (threadIdx.x & 63) >> 5;
+  const T* p = static_cast<const T*>(x.data) + (first + min(row, n - 1)) * x.row + head * x.head;
+#pragma unroll
+  for (int s = 0; s < D / Op<T>::STEP; ++s) {
+    const int d = s * Op<T>::STEP + h * Op<T>::EPL;
+    const bool ok = row < n && d < dim;
+    const frag y = *reinterpret_cast<const frag*>(p + (ok ? d : 0));
+    f[s] = ok ? y : frag{};
+  }
+}
+
+// A block of scores: rows r0 .. r0 + 31 of a tile (at: its place and rows_lane)
+// against the lanes' columns.
+template <typename T, int D>
+__device__ __forceinline__ f32x16 scores(uint32_t at, int r0, const typename Op<T>::frag (&col)[D / Op<T>::STEP], f32x16 acc) {
+#pragma unroll
+  for (int s = 0; s < D / Op<T>::STEP; ++s) acc = Op<T>::mul(LdsTile<T, D, 32>::rows_by_d(at, r0, s), col[s], acc);
+  return acc;
+}
+
+// acc^T += tile^T w: rows r0 .. r0 + 31 of a tile (at: its place and d_lane) by the
+// lanes' columns of weights, values 32 D0 ..
+template <typename T, int D, int D0, int DN>
+__device__ __forceinline__ void contract(uint32_t at, int r0, const float (&w)[16], f32x16 (&acc)[DN]) {
+#pragma unroll
+  for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
+    const typename Op<T>::frag b = Op<T>::pack(w + s * Op<T>::EPL);
+#pragma unroll
+    for (int dt = 0; dt < DN; ++dt) acc[dt] = Op<T>::mul(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), b, acc[dt]);
+  }
+}
+
+// A frag's values in three: the finite ones, and ones for what is plus (minus)
+// infinity or not a number.
+template <typename T>
+__device__ __forceinline__ void sort_out(typename Op<T>::frag f, typename Op<T>::frag& fine, typename Op<T>::frag& plus,
+                                         typename Op<T>::frag& minus) {
+  typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type bits;
+  constexpr bits kSign = (bits)1 << (8 * sizeof(T) - 1);
+  constexpr bits kInf = sizeof(T) == 4 ? (bits)0x7F800000u : std::is_same<T, bf16_t>::value ? 0x7F80 : 0x7C00;
+  constexpr bits kOne = sizeof(T) == 4 ? (bits)0x3F800000u : std::is_same<T, bf16_t>::value ? 0x3F80 : 0x3C00;
+  typedef bits vec __attribute__((ext_vector_type(Op<T>::EPL)));
+  const vec x = __builtin_bit_cast(vec, f);
+  vec y, p, m;
+#pragma unroll
+  for (int i = 0; i < Op<T>::EPL; ++i) {
+    const bits size = x[i] & (bits)~kSign;
+    const bool odd = size >= kInf, nan = size > kInf, below = (x[i] & kSign) != 0;
+    y[i] = odd ? (bits)0 : x[i];
+    p[i] = odd && (nan || !below) ? kOne : (bits)0;
+    m[i] = odd && (nan || below) ? kOne : (bits)0;
+  }
+  fine = __builtin_bit_cast(typename Op<T>::frag, y);
+  plus = __builtin_bit_cast(typename Op<T>::frag, p);
+  minus = __builtin_bit_cast(typename Op<T>::frag, m);
+}
+
+// The same where rows hold what is not finite and some columns do not see them, for
+// which 0 times that is not 0: the finite values as usual, and infinity where a
+// column sees one (plus and minus, or a NaN: NaN).  SIGNED weights: NaN for all.
+template <typename T, int D, int D0, int DN, bool SIGNED, typename Seen>
+__device__ __forceinline__ void contract_seen(uint32_t at, int r0, const float (&w)[16], f32x16 (&acc)[DN],
+                                              Seen seen) {
+  typedef typename Op<T>::frag frag;
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
+    const frag b = Op<T>::pack(w + s * Op<T>::EPL);
+    float see[Op<T>::EPL];
+#pragma unroll
+    for (int i = 0; i < Op<T>::EPL; ++i) see[i] = seen(block_row(s * Op<T>::EPL + i, h)) ? 1.0f : 0.0f;
+    const frag v = Op<T>::pack(see);
+#pragma unroll
+    for (int dt = 0; dt < DN; ++dt) {
+      frag fine, plus, minus;
+      sort_out<T>(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), fine, plus, minus);
+      f32x16 n;
+      acc[dt] = Op<T>::mul(fine, b, acc[dt]);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) n[x] = 0;
+      n = Op<T>::mul(plus, v, n);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        acc[dt][x] += n[x] > 0 ? INFINITY : 0.0f;
+        if (SIGNED) acc[dt][x] -= n[x] > 0 ? INFINITY : 0.0f;
+        n[x] = 0;
+      }
+      n = Op<T>::mul(minus, v, n);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        acc[dt][x] -= n[x] > 0 ? INFINITY : 0.0f;
+        if (SIGNED) acc[dt][x] += n[x] > 0 ? INFINITY : 0.0f;
+      }
+      __builtin_amdgcn_sched_barrier(0);   // no more registers than one block's
+    }
+  }
+}
+
+// Four neighbouring values of a lane's row of results.
+template <typename T, int DN>
+__device__ __forceinline__ void store_column(const HeadsView& x, int64_t first, int head, int row, int dim, int d0,
+                                             const f32x16 (&acc)[DN], float by) {
+  const int h = (threadIdx.x & 63) >> 5;
+  T* p = static_cast<T*>(x.data) + (first + row) * x.row + head * x.head;
+#pragma unroll
+  for (int dt = 0; dt < DN; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = d0 + 32 * dt + 8 * i + 4 * h;
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = acc[dt][4 * i + j] * by;
+      if (d < dim) store4(p + d, y);
+    }
+}
+
+kronq_status prompt_attention_launch(const PromptArgs& a, int32_t dtype, hipStream_t s);
+size_t prompt_grad_ws_bytes(int64_t rows, int q_heads);
+kronq_status prompt_grad_launch(const PromptArgs& a, int32_t dtype, hipStream_t s);
+
+}  // namespace kronq

@@ -88,3 +88,117 @@ def check_logprobs_grad(got, x, dtype, targets, lse, **kw):
     e = np.minimum(3 * logp, 400) * U + 4 * U + 72 * U
     tol = 1.05 * (size * e + np.abs(np.nan_to_num(want)) * HALF[dtype]) + 2 * TINY[dtype] + 1e-37
     near(got, want, tol, "grad")
+
+
+# ---------------------------------------------------------------- prompts
+
+def prompt_case(lengths, qh, kh, dim, dtype, seed, before=0, behind=0, loud=1.0):
+    """q, k, v, dout (host, typed) of rows of sequences, with rows of none around."""
+    rng = np.random.default_rng(seed)
+    rows = before + sum(lengths) + behind
+    cu = (before + np.concatenate([[0], np.cumsum(lengths)])).astype(np.int32)
+    q = typed(rng.normal(size=(rows, qh, dim)) * loud, dtype)
+    k, v = (typed(rng.normal(size=(rows, kh, dim)), dtype) for _ in "kv")
+    return q, k, v, typed(rng.normal(size=(rows, qh, dim)), dtype), cu
+
+
+def _weight_error(b, s, dim, lse):
+    """Relative error of a weight exp(S - m): products are summed in fp32 (dim additions),
+    scaled (2 roundings), taken from the maximum or started from -lse / scale, lse itself
+    rounded (4 |lse| U in all); exp2 4 U."""
+    return U * (b * (dim + 2) + np.abs(s) * 4 + 4 * np.abs(lse) + 4 + 2 * np.abs(s - lse))
+
+
+def prompt_reference(q, k, v, cu, scale, window, dtype):
+    """64-bit (out, lse) and their bounds; rows of no sequence are NaN.  Dense, for finite
+    inputs.
+
+    A weight is off by a factor 1 + e: 2 e in out.  Weights are rounded to the type of v
+    (half a step; fp16: no finer than 2^-25 beside a largest of at least 1); sums of up to
+    `keys` terms and their turns to new maxima are fp32."""
+    out, lse = np.full(q.shape, np.nan), np.full(q.shape[:2], np.nan)
+    tol, ltol = np.zeros(q.shape), np.zeros(q.shape[:2])
+    share, dim = q.shape[1] // k.shape[1], q.shape[2]
+    for b in range(len(cu) - 1):
+        here, n = slice(cu[b], cu[b + 1]), cu[b + 1] - cu[b]
+        if n == 0:
+            continue
+        mask = C.seen(n, window)
+        for h in range(q.shape[1]):
+            g = h // share
+            s = scale * q[here, h] @ k[here, g].T
+            big = scale * np.abs(q[here, h]) @ np.abs(k[here, g]).T
+            m = np.where(mask, s, -np.inf).max(-1, keepdims=True)
+            w = np.where(mask, np.exp(np.minimum(s - m, 0)), 0)
+            total = w.sum(-1, keepdims=True)
+            p = w / total
+            l = m + np.log(total)
+            e = np.where(mask, _weight_error(big, s, dim, l), 0)
+            out[here, h], lse[here, h] = p @ v[here, g], l[:, 0]
+            av = np.abs(v[here, g])
+            up = HALF[dtype] if dtype != torch.float32 else 0
+            t = p @ av * (up + (1.5 * n + 64) * U) + (p * e) @ av + (p * e).sum(-1, keepdims=True) * (p @ av)
+            if dtype == torch.float16:
+                t = t + mask.sum(-1, keepdims=True) * 2.0 ** -25 * av.max() / total
+            tol[here, h] = 1.05 * (t + np.abs(out[here, h]) * HALF[dtype]) + TINY[dtype]
+            ltol[here, h] = 1.05 * ((p * e).sum(-1) + (n + 8) * U + 4 * U * np.abs(l[:, 0]))
+    return out, lse, tol, ltol
+
+
+def prompt_grad_reference(dout, q, k, v, out, lse, cu, scale, window, dtype):
+    """64-bit (dq, dk, dv) and their bounds.  out and lse are what the call is given:
+    delta is off by what they are off by.
+
+    ds = p (dP - delta) is off by p's error e times its size, and by p times the errors of
+    dP (dim additions) and delta; it and p are rounded to the type (fp16: no finer than
+    2^-36 of a column's largest); sums are fp32."""
+    want = [np.full(x.shape, np.nan) for x in (q, k, v)]
+    tol = [np.zeros(x.shape) for x in (q, k, v)]
+    share, dim = q.shape[1] // k.shape[1], q.shape[2]
+    up = HALF[dtype] if dtype != torch.float32 else 0
+    for b in range(len(cu) - 1):
+        here, n = slice(cu[b], cu[b + 1]), cu[b + 1] - cu[b]
+        if n == 0:
+            continue
+        for x in (1, 2):
+            want[x][here] = 0
+        mask = C.seen(n, window)
+        for h in range(q.shape[1]):
+            g = h // share
+            qh, kg, vg, do = q[here, h], k[here, g], v[here, g], dout[here, h]
+            s = scale * qh @ kg.T
+            big = scale * np.abs(qh) @ np.abs(kg).T
+            ms = np.where(mask, s, -np.inf)
+            m = ms.max(-1, keepdims=True)
+            p = np.exp(ms - m)
+            p /= p.sum(-1, keepdims=True)
+            l = lse[here, h][:, None]
+            e = np.where(mask, _weight_error(big, s, dim, l), 0)
+            dp, adp = do @ vg.T, np.abs(do) @ np.abs(vg).T
+            delta = (p * dp).sum(-1, keepdims=True)
+            given = (do * out[here, h]).sum(-1, keepdims=True)
+            agiven = (np.abs(do) * np.abs(out[here, h])).sum(-1, keepdims=True)
+            ds = p * (dp - delta)
+            ed = p * (np.abs(dp - delta) * e + adp * (dim + 2) * U + np.abs(given - delta) + agiven * (dim + 4) * U)
+            es, ep = ed + np.abs(ds) * (up + 2 * U), p * (e + up)
+            if dtype == torch.float16:
+                es = es + mask * (2.0 ** -36 * np.maximum(np.abs(ds).max(0, keepdims=True), np.abs(ds).max(-1, keepdims=True)))
+                ep = ep + mask * (2.0 ** -36 * p.max(0, keepdims=True))
+            acc = (n * share + 64) * U
+            want[0][here, h] = scale * ds @ kg
+            want[1][here, g] += scale * ds.T @ qh
+            want[2][here, g] += p.T @ do
+            tol[0][here, h] = scale * (es + np.abs(ds) * acc) @ np.abs(kg)
+            tol[1][here, g] += scale * (es + np.abs(ds) * acc).T @ np.abs(qh)
+            tol[2][here, g] += (ep + p * acc).T @ np.abs(do)
+    tol = [1.05 * (t + np.abs(np.nan_to_num(w)) * HALF[dtype]) + TINY[dtype] for t, w in zip(tol, want)]
+    return want, tol
+
+
+def sequences_equal(got, want, tol, cu, before, what):
+    """Rows of sequences are near, the others are as they were."""
+    inside = np.zeros(got.shape[0], dtype=bool)
+    for b in range(len(cu) - 1):
+        inside[cu[b]:cu[b + 1]] = True
+    assert (got[~inside] == before).all(), "%s: a row of no sequence was written" % what
+    near(got[inside], want[inside], tol[inside], what)
