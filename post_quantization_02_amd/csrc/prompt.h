@@ -20,7 +20,7 @@ namespace kronq {
 struct PromptArgs {
   HeadsView q, k, v, out, dout, dq, dk, dv;
   float* lse;               // rows x q_heads (forwards: NULL if not wanted)
-  float *neg_lse, *neg_delta;   // backwards, workspace: q_heads x rows, -lse / scale and -sum dO O
+  float *neg_lse, *neg_delta;   // backwards, workspace: q_heads x rows, -lse log2 e and -delta
   const int32_t* cu;
   int seqs, rows, heads, share, dim;
   float scale;              // > 0
@@ -87,6 +87,7 @@ struct Op<bf16_t> {
   __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
+  __device__ static float value(frag f, int i) { return __uint_as_float((uint32_t)(uint16_t)f[i] << 16); }
   __device__ static frag pack(const float* w) {
     bf16x8 f;
 #pragma unroll
@@ -109,6 +110,7 @@ struct Op<_Float16> {
   __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
   }
+  __device__ static float value(frag f, int i) { return (float)__builtin_bit_cast(half8_t, f)[i]; }
   __device__ static frag pack(const float* w) {
     half8_t f;
 #pragma unroll
@@ -133,6 +135,7 @@ struct Op<float> {
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
     return c;
   }
+  __device__ static float value(frag f, int i) { return f[i]; }
   __device__ static frag pack(const float* w) { return frag{w[0], w[1], w[2], w[3]}; }
   __device__ static bool odd(u32x4 w) {
     bool bad = false;
@@ -301,6 +304,23 @@ __device__ __forceinline__ void load_column(const HeadsView& x, int64_t first, i
   }
 }
 
+// A lane's column into a tile of its wave's own, to be read as rows_by_d of row r0.
+template <typename T, int D>
+__device__ __forceinline__ void put_column(uint32_t at, const typename Op<T>::frag (&f)[D / Op<T>::STEP]) {
+#pragma unroll
+  for (int s = 0; s < D / Op<T>::STEP; ++s)
+    *(__attribute__((address_space(3))) typename Op<T>::frag*)(uintptr_t)(at ^ (uint32_t)(2 * s) << 4) = f[s];
+}
+
+// A block of scores whose columns are such a tile's (at their place and rows_lane).
+template <typename T, int D>
+__device__ __forceinline__ f32x16 scores(uint32_t at, uint32_t col_at, f32x16 acc) {
+#pragma unroll
+  for (int s = 0; s < D / Op<T>::STEP; ++s)
+    acc = Op<T>::mul(LdsTile<T, D, 32>::rows_by_d(at, 0, s), LdsTile<T, D, 32>::rows_by_d(col_at, 0, s), acc);
+  return acc;
+}
+
 // A block of scores: rows r0 .. r0 + 31 of a tile (at: its place and rows_lane)
 // against the lanes' columns.
 template <typename T, int D>
@@ -319,6 +339,22 @@ __device__ __forceinline__ void contract(uint32_t at, int r0, const float (&w)[1
     const typename Op<T>::frag b = Op<T>::pack(w + s * Op<T>::EPL);
 #pragma unroll
     for (int dt = 0; dt < DN; ++dt) acc[dt] = Op<T>::mul(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), b, acc[dt]);
+  }
+}
+
+// Two columns of weights by the same rows.
+template <typename T, int D>
+__device__ __forceinline__ void contract_two(uint32_t at, const float (&w)[16], f32x16 (&acc)[D / 32], const float (&w2)[16],
+                                             f32x16 (&acc2)[D / 32]) {
+#pragma unroll
+  for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
+    const typename Op<T>::frag b = Op<T>::pack(w + s * Op<T>::EPL), b2 = Op<T>::pack(w2 + s * Op<T>::EPL);
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) {
+      const typename Op<T>::frag f = LdsTile<T, D, 32>::d_by_rows(at, 0, dt, s);
+      acc[dt] = Op<T>::mul(f, b, acc[dt]);
+      acc2[dt] = Op<T>::mul(f, b2, acc2[dt]);
+    }
   }
 }
 
@@ -351,17 +387,21 @@ __device__ __forceinline__ void sort_out(typename Op<T>::frag f, typename Op<T>:
 // which 0 times that is not 0: the finite values as usual, and infinity where a
 // column sees one (plus and minus, or a NaN: NaN).  SIGNED weights: NaN for all.
 template <typename T, int D, int D0, int DN, bool SIGNED, typename Seen>
-__device__ __forceinline__ void contract_seen(uint32_t at, int r0, const float (&w)[16], f32x16 (&acc)[DN],
-                                              Seen seen) {
+__device__ __forceinline__ void contract_seen(uint32_t at, int r0, const float (&weights)[16], f32x16 (&acc)[DN], Seen seen) {
   typedef typename Op<T>::frag frag;
   const int h = (threadIdx.x & 63) >> 5;
+  float w[16];
 #pragma unroll
+  for (int x = 0; x < 16; ++x) w[x] = weights[x];
+#pragma clang loop unroll(disable)
   for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
-    const frag b = Op<T>::pack(w + s * Op<T>::EPL);
+    const frag b = Op<T>::pack(w);
     float see[Op<T>::EPL];
 #pragma unroll
     for (int i = 0; i < Op<T>::EPL; ++i) see[i] = seen(block_row(s * Op<T>::EPL + i, h)) ? 1.0f : 0.0f;
     const frag v = Op<T>::pack(see);
+#pragma unroll
+    for (int i = 0; i < 16 - Op<T>::EPL; ++i) w[i] = w[i + Op<T>::EPL];
 #pragma unroll
     for (int dt = 0; dt < DN; ++dt) {
       frag fine, plus, minus;

@@ -26,17 +26,23 @@ struct Shape {
 constexpr float kLazy = 8;
 
 template <typename T, int D>
-__global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(PromptArgs a) {
+struct AttentionLds {
+  LdsTile<T, D, Shape<T, D>::KT> k[2], v[2];
+  int odd[2];                             // the tile (its number + 1) whose values are not all finite
+};
+
+// A workgroup's work.  False, with nothing written, where a tile that some row does not
+// see all of holds values that are not finite, unless CAREFUL.
+template <typename T, int D, bool CAREFUL>
+__device__ __forceinline__ bool attend(const PromptArgs& a, AttentionLds<T, D>& lds) {
   constexpr int KT = Shape<T, D>::KT, SUB = KT / 32, DT = D / 32;
   typedef LdsTile<T, D, KT> Tile;
-  __shared__ Tile lk[2], lv[2];
-  __shared__ int odd[2];                  // the tile (its number + 1) whose values are not all finite
   // key heads are the fastest index: an XCD's workgroups read few heads
   const int g = blockIdx.x % a.heads, hs = blockIdx.x / a.heads % a.share, unit = blockIdx.x / (a.heads * a.share);
   const int head = g * a.share + hs;
   Prompt p;
   int tile;
-  if (!find_tile(a, BM, unit, p, tile)) return;
+  if (!find_tile(a, BM, unit, p, tile)) return true;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r0 = tile * BM, w0 = r0 + 32 * wave, row = w0 + (lane & 31);
 
@@ -51,7 +57,7 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
   float m = -FLT_MAX, l = 0;              // of c S; this lane's share of the sum
 
   const int t0 = a.window && r0 >= a.window ? (r0 - a.window + 1) / KT : 0, t1 = min(r0 + BM - 1, p.n - 1) / KT;
-  if (tid < 2) odd[tid] = 0;
+  if (tid < 2) lds.odd[tid] = 0;
   Staged<T, D, KT, NT> sk, sv;
   // whether some row of the workgroup does not see all of tile t
   auto cut = [&](int t) {
@@ -63,9 +69,9 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
   };
   const uint32_t to_lane = Staged<T, D, KT, NT>::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
   auto put = [&](int t, int to) __attribute__((always_inline)) {
-    sk.store(hidden(lds_at(lk[to]) + to_lane));
-    sv.store(hidden(lds_at(lv[to]) + to_lane));
-    if (cut(t) && sv.odd()) odd[to] = t + 1;
+    sk.store(hidden(lds_at(lds.k[to]) + to_lane));
+    sv.store(hidden(lds_at(lds.v[to]) + to_lane));
+    if (cut(t) && sv.odd()) lds.odd[to] = t + 1;
   };
   fetch(t0);
   __syncthreads();
@@ -73,12 +79,13 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
   for (int t = t0; t <= t1; ++t) {
     const int from = t & 1;
     __syncthreads();
+    if (!CAREFUL && cut(t) && lds.odd[from] == t + 1) return false;
     if (t < t1) fetch(t + 1);
     const int k0 = t * KT;
     const bool none = k0 > w0 + 31 || (a.window && k0 + KT - 1 <= w0 - a.window);
     if (!none) {
       const bool part = k0 + KT - 1 > w0 || (a.window && k0 <= w0 + 31 - a.window);
-      const uint32_t k_at = hidden(lds_at(lk[from]) + rows_lane), v_at = hidden(lds_at(lv[from]) + d_lane);
+      const uint32_t k_at = hidden(lds_at(lds.k[from]) + rows_lane), v_at = hidden(lds_at(lds.v[from]) + d_lane);
       f32x16 s[SUB];
 #pragma unroll
       for (int b = 0; b < SUB; ++b) {
@@ -111,7 +118,6 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
 #pragma unroll
           for (int x = 0; x < 16; ++x) o[dt][x] *= f;
       }
-      const bool careful = part && odd[from] == t + 1;
 #pragma unroll
       for (int b = 0; b < SUB; ++b) {
         float w[16];
@@ -120,8 +126,8 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
           w[x] = __builtin_amdgcn_exp2f(fmaf(s[b][x], c, -m));
           l += w[x];
         }
-        if (!careful) contract<T, D, 0, DT>(v_at, 32 * b, w, o);
-        else contract_seen<T, D, 0, DT, false>(v_at, 32 * b, w, o, [&](int r) { return seen(b, r); });
+        if (CAREFUL && part) contract_seen<T, D, 0, DT, false>(v_at, 32 * b, w, o, [&](int r) { return seen(b, r); });
+        else contract<T, D, 0, DT>(v_at, 32 * b, w, o);
       }
     }
     if (t < t1) put(t + 1, from ^ 1);
@@ -132,6 +138,20 @@ __global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(
     if (a.lse && h == 0)
       a.lse[(int64_t)(p.start + row) * (a.heads * a.share) + head] = l == 0 ? -INFINITY : (m + __log2f(l)) * kPromptLn2;
   }
+  return true;
+}
+
+// Called rather than a part of the kernel, so that it costs the usual way no registers.
+template <typename T, int D>
+__device__ __attribute__((noinline)) void attend_carefully(PromptArgs a, AttentionLds<T, D>* lds) {
+  __syncthreads();
+  attend<T, D, true>(a, *lds);
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(NT, (Shape<T, D>::PER_SIMD)) void prompt_attention(PromptArgs a) {
+  __shared__ AttentionLds<T, D> lds;
+  if (!attend<T, D, false>(a, lds)) attend_carefully<T, D>(a, &lds);
 }
 
 template <typename T>
