@@ -76,14 +76,15 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit,
 
 // ---------------------------------------------------------------- operands
 
-// EPL: values of a lane in one product (16 bytes); STEP: k of a product.
+// EPL: values of a lane in one step (16 bytes); STEP: k of a step; MULS: its products;
+// TURNED: reads of a transposed operand.
 template <typename T>
 struct Op;
 
 template <>
 struct Op<bf16_t> {
   typedef s16x8 frag;
-  static constexpr int EPL = 8, STEP = 16;
+  static constexpr int EPL = 8, STEP = 16, MULS = 1, TURNED = 2;
   __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
@@ -106,7 +107,7 @@ struct Op<bf16_t> {
 template <>
 struct Op<_Float16> {
   typedef s16x8 frag;
-  static constexpr int EPL = 8, STEP = 16;
+  static constexpr int EPL = 8, STEP = 16, MULS = 1, TURNED = 2;
   __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
   }
@@ -129,7 +130,7 @@ struct Op<_Float16> {
 template <>
 struct Op<float> {
   typedef f32x4 frag;
-  static constexpr int EPL = 4, STEP = 8;
+  static constexpr int EPL = 4, STEP = 8, MULS = 4, TURNED = 4;
   __device__ static f32x16 mul(frag a, frag b, f32x16 c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
@@ -159,8 +160,32 @@ __device__ __forceinline__ void prompt_each(F f) {
 }
 
 // Largest of a column: both halves hold some of its rows.
-__device__ __forceinline__ float both_max(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
-__device__ __forceinline__ float both_sum(float x) { return x + __shfl_xor(x, 32); }
+__device__ __forceinline__ float both_max(float x) {
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+__device__ __forceinline__ float both_sum(float x) {
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+}
+
+// N groups of `muls` products with READS operand reads each from LDS, which run AHEAD
+// groups before their products: left alone, the compiler has each product wait for a
+// read just issued.
+template <int N, int MULS, int READS, int AHEAD>
+__device__ __forceinline__ void in_turn() {
+  constexpr int kMul = 0x008, kRead = 0x100, kAhead = AHEAD < N ? AHEAD : N;
+  __builtin_amdgcn_sched_group_barrier(kRead, kAhead * READS, 0);
+#pragma unroll
+  for (int i = 0; i < N - kAhead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMul, MULS, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, READS, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(kMul, kAhead * MULS, 0);
+}
+
+// Keeps what follows a branch of its own: as selects it would cost every tile what few need.
+__device__ __forceinline__ void rarely() { asm volatile(""); }
 
 // ---------------------------------------------------------------- tiles in LDS
 
@@ -251,23 +276,19 @@ struct Staged {
   static_assert((APART & (APART - 1)) == 0 && APART >= 4, "turns of rows APART further are a constant's");
   u32x4 w[EACH];
 
-  // rows `row` .. of a head's n (row < n); `dim` of D values
+  // rows `row` .. of a head's n (row < n); `dim` of D values.  What lies behind the last
+  // row's values is out of the buffer's range, and a load of it gives 0; so are a short
+  // head's missing pieces, whose places are past any range.
   __device__ __forceinline__ void load(const HeadsView& x, int64_t first, int head, int row, int n, int dim) {
     const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x / Tile::PIECES;
-    const char* base = static_cast<const char*>(x.data) + ((first + row) * x.row + head * x.head) * (int64_t)sizeof(T);
-    const uint32_t stride = (uint32_t)x.row * (uint32_t)sizeof(T), mine = (uint32_t)r * stride + (uint32_t)c * 16;
-    if (row + ROWS <= n && dim == D) {
+    const uint32_t stride = (uint32_t)x.row * (uint32_t)sizeof(T);
+    T* base = static_cast<T*>(x.data) + ((first + row) * x.row + head * x.head);
+    const uint32_t range = (uint32_t)(min(n - row, ROWS) - 1) * stride + (uint32_t)dim * (uint32_t)sizeof(T);
+    const auto rows = __builtin_amdgcn_make_buffer_rsrc(base, 0, range, 0x27000);
+    const uint32_t mine = c * Op<T>::EPL < dim ? (uint32_t)r * stride + (uint32_t)c * 16 : 0x80000000u;
 #pragma unroll
-      for (int i = 0; i < EACH; ++i) w[i] = *reinterpret_cast<const u32x4*>(base + (uint64_t)i * APART * stride + mine);
-    } else {
-      const bool in = c * Op<T>::EPL < dim;
-#pragma unroll
-      for (int i = 0; i < EACH; ++i) {
-        const bool ok = in && row + r + i * APART < n;
-        const u32x4 y = *reinterpret_cast<const u32x4*>(base + (ok ? (uint32_t)(i * APART) * stride + mine : 0u));
-        w[i] = ok ? y : u32x4{0, 0, 0, 0};
-      }
-    }
+    for (int i = 0; i < EACH; ++i)
+      w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, mine + (uint32_t)(i * APART) * stride, 0, 0));
   }
   // This thread's number for store.
   __device__ static __forceinline__ uint32_t lane() {
@@ -318,6 +339,7 @@ __device__ __forceinline__ f32x16 scores(uint32_t at, uint32_t col_at, f32x16 ac
 #pragma unroll
   for (int s = 0; s < D / Op<T>::STEP; ++s)
     acc = Op<T>::mul(LdsTile<T, D, 32>::rows_by_d(at, 0, s), LdsTile<T, D, 32>::rows_by_d(col_at, 0, s), acc);
+  in_turn<D / Op<T>::STEP, Op<T>::MULS, 2, 3>();
   return acc;
 }
 
@@ -327,6 +349,7 @@ template <typename T, int D>
 __device__ __forceinline__ f32x16 scores(uint32_t at, int r0, const typename Op<T>::frag (&col)[D / Op<T>::STEP], f32x16 acc) {
 #pragma unroll
   for (int s = 0; s < D / Op<T>::STEP; ++s) acc = Op<T>::mul(LdsTile<T, D, 32>::rows_by_d(at, r0, s), col[s], acc);
+  in_turn<D / Op<T>::STEP, Op<T>::MULS, 1, 4>();
   return acc;
 }
 
@@ -340,6 +363,7 @@ __device__ __forceinline__ void contract(uint32_t at, int r0, const float (&w)[1
 #pragma unroll
     for (int dt = 0; dt < DN; ++dt) acc[dt] = Op<T>::mul(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), b, acc[dt]);
   }
+  in_turn<32 / Op<T>::STEP * DN, Op<T>::MULS, Op<T>::TURNED, 3>();
 }
 
 // Two columns of weights by the same rows.
@@ -356,6 +380,7 @@ __device__ __forceinline__ void contract_two(uint32_t at, const float (&w)[16], 
       acc2[dt] = Op<T>::mul(f, b2, acc2[dt]);
     }
   }
+  in_turn<32 / Op<T>::STEP * (D / 32), 2 * Op<T>::MULS, Op<T>::TURNED, 2>();
 }
 
 // A frag's values in three: the finite ones, and ones for what is plus (minus)

@@ -19,7 +19,7 @@ constexpr int NT = 256, BM = 128;
 template <typename T, int D>
 struct Shape {
   static constexpr int KT = sizeof(T) == 2 && D <= 128 ? 64 : 32;
-  static constexpr int PER_SIMD = D <= 128 ? 2 : 1;
+  static constexpr int PER_SIMD = D == 64 && sizeof(T) == 2 ? 4 : D <= 128 ? 2 : 1;
 };
 
 // The maximum is raised when a tile's exceeds it by 2^kLazy: weights stay below that.
@@ -71,7 +71,10 @@ __device__ __forceinline__ bool attend(const PromptArgs& a, AttentionLds<T, D>& 
   auto put = [&](int t, int to) __attribute__((always_inline)) {
     sk.store(hidden(lds_at(lds.k[to]) + to_lane));
     sv.store(hidden(lds_at(lds.v[to]) + to_lane));
-    if (cut(t) && sv.odd()) lds.odd[to] = t + 1;
+    if (cut(t)) {
+      rarely();
+      if (sv.odd()) lds.odd[to] = t + 1;
+    }
   };
   fetch(t0);
   __syncthreads();
@@ -98,6 +101,7 @@ __device__ __forceinline__ bool attend(const PromptArgs& a, AttentionLds<T, D>& 
         return j <= row && (!a.window || j > row - a.window);
       };
       if (part) {
+        rarely();
 #pragma unroll
         for (int b = 0; b < SUB; ++b)
 #pragma unroll
@@ -110,6 +114,7 @@ __device__ __forceinline__ bool attend(const PromptArgs& a, AttentionLds<T, D>& 
         for (int x = 0; x < 16; ++x) top = fmaxf(top, s[b][x]);
       top = both_max(top) * c;
       if (__any(top > m + kLazy)) {
+        rarely();
         const float up = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - up);
         m = up;
         l *= f;

@@ -43,6 +43,7 @@ struct Fit<_Float16> {
     for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(w[x]));
     top = both_max(top);
     if (__any(top * by >= 0x1p15f)) {
+      rarely();
       // 2^(13 - e) for a largest of 2^e and up
       const int e = (int)(__float_as_uint(top) >> 23);
       const float to = fminf(by, __uint_as_float((uint32_t)min(max(267 - e, 1), 254) << 23));
@@ -124,7 +125,10 @@ __device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& ld
   auto put = [&](int t, int to) __attribute__((always_inline)) {
     sk.store(hidden(lds_at(lds.k[to]) + to_lane));
     sv.store(hidden(lds_at(lds.v[to]) + to_lane));
-    if (cut(t) && sk.odd()) lds.odd[to] = t + 1;
+    if (cut(t)) {
+      rarely();
+      if (sk.odd()) lds.odd[to] = t + 1;
+    }
   };
   {
 #pragma unroll
@@ -164,6 +168,7 @@ __device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& ld
           u[x] = w[x] * d[x];
         }
         if (part) {
+        rarely();
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const bool in = seen(block_row(x, h));
@@ -287,7 +292,10 @@ __device__ __forceinline__ bool keys_grad(const PromptArgs& a, KeysLds<T, D>& ld
     sq.store(hidden(lds_at(lds.q[to]) + to_lane));
     so.store(hidden(lds_at(lds.o[to]) + to_lane));
     if (tid < 64) lds.row[to][tid >> 5][tid & 31] = srow;
-    if (cut(next_row) && (sq.odd() || so.odd())) lds.odd[to] = it + 1;
+    if (cut(next_row)) {
+      rarely();
+      if (sq.odd() || so.odd()) lds.odd[to] = it + 1;
+    }
   };
   {
 #pragma unroll
@@ -339,6 +347,7 @@ __device__ __forceinline__ bool keys_grad(const PromptArgs& a, KeysLds<T, D>& ld
           }
         }
         if (part) {
+        rarely();
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const bool in = seen(block_row(x, h));
