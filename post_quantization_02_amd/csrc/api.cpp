@@ -756,7 +756,7 @@ static kronq_status prompt_view(const char* fn, int32_t dtype, int64_t rows, int
   a->share = q_heads / heads;
   a->dim = dim;
   a->scale = scale;
-  a->window = window < rows ? (int)window : 0;   // a window of all rows is none
+  a->window = window > 0 && window < rows ? (int)window : 1 << 30;
   return KRONQ_OK;
 }
 

@@ -14,6 +14,7 @@
 #include <utility>
 
 #include "kv.h"
+#include "prompt_index.h"
 
 namespace kronq {
 
@@ -24,7 +25,7 @@ struct PromptArgs {
   const int32_t* cu;
   int seqs, rows, heads, share, dim;
   float scale;              // > 0
-  int window;               // 0: none
+  int window;               // of rows; more than there are: none
 };
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -37,14 +38,6 @@ constexpr float kPromptLog2e = 1.44269504088896340736f, kPromptLn2 = 0.693147180
 
 // ---------------------------------------------------------------- where a workgroup works
 
-// Rows of sequence b that there are: cu may hold anything.
-struct Prompt { int start, n; };
-
-__device__ __forceinline__ Prompt prompt_of(const PromptArgs& a, int b) {
-  const int lo = min(max(a.cu[b], 0), a.rows), hi = min(a.cu[b + 1], a.rows);
-  return {lo, max(hi - lo, 0)};
-}
-
 // Tile number `unit` of all sequences' tiles of bm rows: its sequence, and which of
 // its tiles, counted from the last one (late rows see most: they come first).
 // False: there are fewer.
@@ -53,7 +46,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit,
   int before = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     Prompt mine{0, 0};
-    if (b0 + lane < a.seqs) mine = prompt_of(a, b0 + lane);
+    if (b0 + lane < a.seqs) mine = prompt_between(a.cu[b0 + lane], a.cu[b0 + lane + 1], a.rows);
     const int tiles = (mine.n + bm - 1) / bm;
     int upto = tiles;
 #pragma unroll
@@ -89,18 +82,16 @@ struct Op<bf16_t> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
   __device__ static float value(frag f, int i) { return __uint_as_float((uint32_t)(uint16_t)f[i] << 16); }
+  __device__ static float value(bf16_t x) { return __uint_as_float((uint32_t)x.bits << 16); }
   __device__ static frag pack(const float* w) {
     bf16x8 f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = (__bf16)w[i];
     return __builtin_bit_cast(frag, f);
   }
-  // any exponent of all ones
-  __device__ static bool odd(u32x4 w) {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7F80u) == 0x7F80u) | ((w[i] & 0x7F800000u) == 0x7F800000u);
-    return bad;
+  // a word of values without what is not finite (an exponent of all ones)
+  __device__ static uint32_t fine(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0 : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0 : w & 0xFFFF0000u);
   }
 };
 
@@ -112,17 +103,15 @@ struct Op<_Float16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
   }
   __device__ static float value(frag f, int i) { return (float)__builtin_bit_cast(half8_t, f)[i]; }
+  __device__ static float value(_Float16 x) { return (float)x; }
   __device__ static frag pack(const float* w) {
     half8_t f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = (_Float16)w[i];
     return __builtin_bit_cast(frag, f);
   }
-  __device__ static bool odd(u32x4 w) {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7C00u) == 0x7C00u) | ((w[i] & 0x7C000000u) == 0x7C000000u);
-    return bad;
+  __device__ static uint32_t fine(uint32_t w) {
+    return ((w & 0x7C00u) == 0x7C00u ? 0 : w & 0xFFFFu) | ((w & 0x7C000000u) == 0x7C000000u ? 0 : w & 0xFFFF0000u);
   }
 };
 
@@ -137,13 +126,9 @@ struct Op<float> {
     return c;
   }
   __device__ static float value(frag f, int i) { return f[i]; }
+  __device__ static float value(float x) { return x; }
   __device__ static frag pack(const float* w) { return frag{w[0], w[1], w[2], w[3]}; }
-  __device__ static bool odd(u32x4 w) {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
-    return bad;
-  }
+  __device__ static uint32_t fine(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u ? 0 : w; }
 };
 
 // Row of a 32 x 32 block that register x holds.
@@ -177,11 +162,10 @@ __device__ __forceinline__ void in_turn() {
   constexpr int kMul = 0x008, kRead = 0x100, kAhead = AHEAD < N ? AHEAD : N;
   __builtin_amdgcn_sched_group_barrier(kRead, kAhead * READS, 0);
 #pragma unroll
-  for (int i = 0; i < N - kAhead; ++i) {
+  for (int i = 0; i < N; ++i) {
     __builtin_amdgcn_sched_group_barrier(kMul, MULS, 0);
-    __builtin_amdgcn_sched_group_barrier(kRead, READS, 0);
+    if (i < N - kAhead) __builtin_amdgcn_sched_group_barrier(kRead, READS, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(kMul, kAhead * MULS, 0);
 }
 
 // Keeps what follows a branch of its own: as selects it would cost every tile what few need.
@@ -266,21 +250,21 @@ struct LdsTile {
   }
 };
 
-// A tile on its way from memory to LDS: a workgroup of NT threads, 16 bytes a thread
-// and load.
+// A tile on its way from memory to LDS by NT threads (a workgroup, or a wave each its
+// own), 16 bytes a thread and load.
 template <typename T, int D, int ROWS, int NT>
 struct Staged {
   typedef LdsTile<T, D, ROWS> Tile;
   static constexpr int EACH = ROWS * Tile::PIECES / NT, APART = NT / Tile::PIECES;
   static_assert(EACH * NT == ROWS * Tile::PIECES && APART * EACH == ROWS, "whole rows");
-  static_assert((APART & (APART - 1)) == 0 && APART >= 4, "turns of rows APART further are a constant's");
+  static_assert((APART & (APART - 1)) == 0, "the turn of a row is that of its multiple of APART and that of the rest");
   u32x4 w[EACH];
 
   // rows `row` .. of a head's n (row < n); `dim` of D values.  What lies behind the last
   // row's values is out of the buffer's range, and a load of it gives 0; so are a short
   // head's missing pieces, whose places are past any range.
   __device__ __forceinline__ void load(const HeadsView& x, int64_t first, int head, int row, int n, int dim) {
-    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x / Tile::PIECES;
+    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x % NT / Tile::PIECES;
     const uint32_t stride = (uint32_t)x.row * (uint32_t)sizeof(T);
     T* base = static_cast<T*>(x.data) + ((first + row) * x.row + head * x.head);
     const uint32_t range = (uint32_t)(min(n - row, ROWS) - 1) * stride + (uint32_t)dim * (uint32_t)sizeof(T);
@@ -292,7 +276,7 @@ struct Staged {
   }
   // This thread's number for store.
   __device__ static __forceinline__ uint32_t lane() {
-    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x / Tile::PIECES;
+    const int c = threadIdx.x % Tile::PIECES, r = threadIdx.x % NT / Tile::PIECES;
     return (uint32_t)(r * Tile::BYTES + ((c ^ Tile::turn(r)) << 4));
   }
   __device__ __forceinline__ void store(uint32_t at) const {
@@ -301,11 +285,23 @@ struct Staged {
       *(__attribute__((address_space(3))) u32x4*)(uintptr_t)((at ^ (uint32_t)Tile::turn(i * APART) << 4) +
                                                              (uint32_t)(i * APART * Tile::BYTES)) = w[i];
   }
-  __device__ __forceinline__ bool odd() const {
-    bool bad = false;
+  // Takes out what is not finite; the rows of the tile (from 0 on, of the first 32) that this
+  // thread found any in.
+  __device__ __forceinline__ uint32_t clean() {
+    const int r = threadIdx.x % NT / Tile::PIECES;
+    uint32_t rows = 0;
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) bad |= Op<T>::odd(w[i]);
-    return bad;
+    for (int i = 0; i < EACH; ++i) {
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t y = Op<T>::fine(w[i][j]);
+        bad |= y != w[i][j];
+        w[i][j] = y;
+      }
+      rows |= bad ? 1u << ((r + i * APART) & 31) : 0;
+    }
+    return rows;
   }
 };
 
@@ -355,7 +351,7 @@ __device__ __forceinline__ f32x16 scores(uint32_t at, int r0, const typename Op<
 
 // acc^T += tile^T w: rows r0 .. r0 + 31 of a tile (at: its place and d_lane) by the
 // lanes' columns of weights, values 32 D0 ..
-template <typename T, int D, int D0, int DN>
+template <typename T, int D, int D0, int DN, int AHEAD>
 __device__ __forceinline__ void contract(uint32_t at, int r0, const float (&w)[16], f32x16 (&acc)[DN]) {
 #pragma unroll
   for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
@@ -363,7 +359,7 @@ __device__ __forceinline__ void contract(uint32_t at, int r0, const float (&w)[1
 #pragma unroll
     for (int dt = 0; dt < DN; ++dt) acc[dt] = Op<T>::mul(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), b, acc[dt]);
   }
-  in_turn<32 / Op<T>::STEP * DN, Op<T>::MULS, Op<T>::TURNED, 3>();
+  in_turn<32 / Op<T>::STEP * DN, Op<T>::MULS, Op<T>::TURNED, AHEAD>();
 }
 
 // Two columns of weights by the same rows.
@@ -383,72 +379,30 @@ __device__ __forceinline__ void contract_two(uint32_t at, const float (&w)[16], 
   in_turn<32 / Op<T>::STEP * (D / 32), 2 * Op<T>::MULS, Op<T>::TURNED, 2>();
 }
 
-// A frag's values in three: the finite ones, and ones for what is plus (minus)
-// infinity or not a number.
-template <typename T>
-__device__ __forceinline__ void sort_out(typename Op<T>::frag f, typename Op<T>::frag& fine, typename Op<T>::frag& plus,
-                                         typename Op<T>::frag& minus) {
-  typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type bits;
-  constexpr bits kSign = (bits)1 << (8 * sizeof(T) - 1);
-  constexpr bits kInf = sizeof(T) == 4 ? (bits)0x7F800000u : std::is_same<T, bf16_t>::value ? 0x7F80 : 0x7C00;
-  constexpr bits kOne = sizeof(T) == 4 ? (bits)0x3F800000u : std::is_same<T, bf16_t>::value ? 0x3F80 : 0x3C00;
-  typedef bits vec __attribute__((ext_vector_type(Op<T>::EPL)));
-  const vec x = __builtin_bit_cast(vec, f);
-  vec y, p, m;
-#pragma unroll
-  for (int i = 0; i < Op<T>::EPL; ++i) {
-    const bits size = x[i] & (bits)~kSign;
-    const bool odd = size >= kInf, nan = size > kInf, below = (x[i] & kSign) != 0;
-    y[i] = odd ? (bits)0 : x[i];
-    p[i] = odd && (nan || !below) ? kOne : (bits)0;
-    m[i] = odd && (nan || below) ? kOne : (bits)0;
-  }
-  fine = __builtin_bit_cast(typename Op<T>::frag, y);
-  plus = __builtin_bit_cast(typename Op<T>::frag, p);
-  minus = __builtin_bit_cast(typename Op<T>::frag, m);
-}
-
-// The same where rows hold what is not finite and some columns do not see them, for
-// which 0 times that is not 0: the finite values as usual, and infinity where a
-// column sees one (plus and minus, or a NaN: NaN).  SIGNED weights: NaN for all.
-template <typename T, int D, int D0, int DN, bool SIGNED, typename Seen>
-__device__ __forceinline__ void contract_seen(uint32_t at, int r0, const float (&weights)[16], f32x16 (&acc)[DN], Seen seen) {
-  typedef typename Op<T>::frag frag;
+// What rows `from` .. `upto` - 1 of x hold that is not finite, for the columns that see them
+// (weights are positive): tiles that not all columns see are held without it, for 0 times
+// that is not 0.  Rare.
+template <typename T, int DN, typename Seen>
+__device__ __forceinline__ void add_odd(const HeadsView& x, int64_t first, int head, int from, int upto, int dim, int d0,
+                                        f32x16 (&acc)[DN], Seen seen) {
   const int h = (threadIdx.x & 63) >> 5;
-  float w[16];
-#pragma unroll
-  for (int x = 0; x < 16; ++x) w[x] = weights[x];
 #pragma clang loop unroll(disable)
-  for (int s = 0; s < 32 / Op<T>::STEP; ++s) {
-    const frag b = Op<T>::pack(w);
-    float see[Op<T>::EPL];
-#pragma unroll
-    for (int i = 0; i < Op<T>::EPL; ++i) see[i] = seen(block_row(s * Op<T>::EPL + i, h)) ? 1.0f : 0.0f;
-    const frag v = Op<T>::pack(see);
-#pragma unroll
-    for (int i = 0; i < 16 - Op<T>::EPL; ++i) w[i] = w[i + Op<T>::EPL];
+  for (int r = from; r < upto; ++r) {
+    if (!seen(r)) continue;
+    const T* p = static_cast<const T*>(x.data) + (first + r) * x.row + head * x.head;
 #pragma unroll
     for (int dt = 0; dt < DN; ++dt) {
-      frag fine, plus, minus;
-      sort_out<T>(LdsTile<T, D, 32>::d_by_rows(at, r0, D0 + dt, s), fine, plus, minus);
-      f32x16 n;
-      acc[dt] = Op<T>::mul(fine, b, acc[dt]);
 #pragma unroll
-      for (int x = 0; x < 16; ++x) n[x] = 0;
-      n = Op<T>::mul(plus, v, n);
+      for (int i = 0; i < 4; ++i) {
+        const int d = d0 + 32 * dt + 8 * i + 4 * h;
+        if (d >= dim) continue;
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        acc[dt][x] += n[x] > 0 ? INFINITY : 0.0f;
-        if (SIGNED) acc[dt][x] -= n[x] > 0 ? INFINITY : 0.0f;
-        n[x] = 0;
+        for (int j = 0; j < 4; ++j) {
+          const float y = Op<T>::value(p[d + j]);
+          acc[dt][4 * i + j] += (__float_as_uint(y) & 0x7F800000u) == 0x7F800000u ? y : 0.0f;
+        }
       }
-      n = Op<T>::mul(minus, v, n);
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        acc[dt][x] -= n[x] > 0 ? INFINITY : 0.0f;
-        if (SIGNED) acc[dt][x] += n[x] > 0 ? INFINITY : 0.0f;
-      }
-      __builtin_amdgcn_sched_barrier(0);   // no more registers than one block's
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -469,6 +423,36 @@ __device__ __forceinline__ void store_column(const HeadsView& x, int64_t first, 
       for (int j = 0; j < 4; ++j) y[j] = acc[dt][4 * i + j] * by;
       if (d < dim) store4(p + d, y);
     }
+}
+
+// Results of four waves that had a part of the same columns' sums each: this wave's
+// into `all`, and after a barrier the sum of all four of the blocks that are its own.
+template <int DN>
+struct JoinLds { f32x4 b[4][DN][4][64]; };
+
+template <int DN>
+__device__ __forceinline__ void put_part(JoinLds<DN>& all, const f32x16 (&acc)[DN], float by) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int dt = 0; dt < DN; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      all.b[wave][dt][i][lane] = f32x4{acc[dt][4 * i] * by, acc[dt][4 * i + 1] * by, acc[dt][4 * i + 2] * by, acc[dt][4 * i + 3] * by};
+}
+
+template <int DN>
+__device__ __forceinline__ f32x16 joined(const JoinLds<DN>& all, int dt) {
+  const int lane = threadIdx.x & 63;
+  f32x16 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f32x4 x = all.b[0][dt][i][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) x += all.b[w][dt][i][lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[4 * i + j] = x[j];
+  }
+  return y;
 }
 
 kronq_status prompt_attention_launch(const PromptArgs& a, int32_t dtype, hipStream_t s);

@@ -5,7 +5,9 @@
 // Two kernels, so that no sum needs atomics or a second pass: one takes 128 rows of a
 // query head and goes through their keys (dQ), one takes 128 keys of a key head and
 // goes through the rows of all its query heads (dK, dV stay in registers).  Both
-// compute S and dP.
+// compute S and dP.  Where there are too few of these for the chip (SPLIT), a workgroup
+// takes 32 rows or keys, its waves every fourth tile each, by themselves, and the four
+// parts are joined in LDS.
 //
 // delta is dO . O, but O has been rounded to its type, and where one key has most of
 // a row's weight dP - delta is small beside that rounding.  The rows of dS sum to 0,
@@ -61,29 +63,40 @@ struct Fit<_Float16> {
 
 // ---------------------------------------------------------------- queries
 
-template <typename T, int D>
+constexpr int KT = 32;
+
+template <typename T, int D, bool SPLIT>
 struct RowsLds {
   static constexpr bool FIX = sizeof(T) == 2;      // delta is put right; dO is held here
-  LdsTile<T, D, 32> k[2], v[2];
-  typename std::conditional<FIX, LdsTile<T, D, 32>, int>::type own[4];
-  int odd[2];
+  union {
+    struct { LdsTile<T, D, KT> k[SPLIT ? 4 : 2], v[SPLIT ? 4 : 2]; } tile;
+    typename std::conditional<SPLIT, JoinLds<D / 32>, int>::type join;
+  };
+  typename std::conditional<FIX, LdsTile<T, D, 32>, int>::type own[SPLIT ? 1 : 4];
+  float off[4][64];
+  // Of a tile that some row does not see all of: keys that are not finite.  Of a tile, the
+  // next, and the one after, which is cleared while the others are in use (SPLIT: a wave's).
+  uint32_t odd[4];
+  __device__ RowsLds() {}
 };
 
-// A workgroup's work.  False, with nothing written, where a tile that some row does not
-// see all of holds keys that are not finite, unless CAREFUL.
-template <typename T, int D, bool CAREFUL>
-__device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& lds) {
-  constexpr int BM = 128, KT = 32, DT = D / 32, STEPS = D / Op<T>::STEP;
-  constexpr bool FIX = RowsLds<T, D>::FIX;
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__(NT, SPLIT || D == 256 || (D == 128 && sizeof(T) == 4) ? 1 : 2) void prompt_rows_grad(PromptArgs a) {
+  constexpr int BM = SPLIT ? 32 : 128, DT = D / 32, STEPS = D / Op<T>::STEP, BY = SPLIT ? 4 : 1;
+  typedef RowsLds<T, D, SPLIT> Lds;
+  constexpr bool FIX = Lds::FIX;
   typedef LdsTile<T, D, KT> Tile;
+  typedef Staged<T, D, KT, SPLIT ? 64 : NT> Stage;
+  __shared__ Lds lds;
   const int g = blockIdx.x % a.heads, hs = blockIdx.x / a.heads % a.share, unit = blockIdx.x / (a.heads * a.share);
   const int head = g * a.share + hs;
   Prompt p;
   int tile;
-  if (!find_tile(a, BM, unit, p, tile)) return true;
+  if (!find_tile(a, BM, unit, p, tile)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r0 = tile * BM, w0 = r0 + 32 * wave, row = w0 + (lane & 31);
-  const uint32_t to_lane = Staged<T, D, KT, NT>::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
+  const int r0 = tile * BM, w0 = SPLIT ? r0 : r0 + 32 * wave, row = w0 + (lane & 31);
+  const uint32_t to_lane = Stage::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
+  auto& own = lds.own[SPLIT ? 0 : wave];           // SPLIT: all waves write the same
 
   typename Op<T>::frag qc[STEPS], oc[FIX ? 1 : STEPS];
   float neg_lse, neg_delta;
@@ -101,7 +114,7 @@ __device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& ld
     // a row of no weight has none
     neg_lse = lse == -INFINITY ? -INFINITY : -lse * kPromptLog2e;
     if constexpr (FIX) {
-      put_column<T, D>(lds_at(lds.own[wave]) + rows_lane, f);
+      put_column<T, D>(lds_at(own) + rows_lane, f);
     } else {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) oc[s] = f[s];
@@ -110,96 +123,100 @@ __device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& ld
   load_column<T, D>(a.q, p.start, head, row, p.n, a.dim, qc);
   const float c = a.scale * kPromptLog2e;
   f32x16 dq[DT], pk[FIX ? DT : 1];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) dq[dt][x] = pk[FIX ? dt : 0][x] = 0;
   Fit<T> fit;
-  float off;                              // what this lane's rows of dS sum to
+  float off = 0;                          // what this lane's rows of dS sum to
 
-  const int t0 = a.window && r0 >= a.window ? (r0 - a.window + 1) / KT : 0, t1 = min(r0 + BM - 1, p.n - 1) / KT;
-  Staged<T, D, KT, NT> sk, sv;
+  const TileSpan span = keys_of_rows(r0, BM, p.n, a.window, KT);
+  const int t0 = span.first, t1 = span.last;
+  Stage sk, sv;
+  // whether some row of the workgroup does not see all of tile t
   auto cut = [&](int t) {
-    return t * KT + KT - 1 > r0 || (a.window && t * KT <= r0 + BM - 1 - a.window);
+    return t * KT + KT - 1 > r0 || t * KT <= r0 + BM - 1 - a.window;
   };
   auto fetch = [&](int t) __attribute__((always_inline)) {
     sk.load(a.k, p.start, g, t * KT, p.n, a.dim);
     sv.load(a.v, p.start, g, t * KT, p.n, a.dim);
   };
-  auto put = [&](int t, int to) __attribute__((always_inline)) {
-    sk.store(hidden(lds_at(lds.k[to]) + to_lane));
-    sv.store(hidden(lds_at(lds.v[to]) + to_lane));
+  auto put = [&](int t, int to, int slot) __attribute__((always_inline)) {
     if (cut(t)) {
       rarely();
-      if (sk.odd()) lds.odd[to] = t + 1;
+      // 0 times them would not be 0.  A row that sees one has no number for a maximum, or
+      // no weight for the key.
+      const uint32_t keys = sk.clean();
+      if (keys) atomicOr(&lds.odd[slot], keys);
     }
+    sk.store(hidden(lds_at(lds.tile.k[to]) + to_lane));
+    sv.store(hidden(lds_at(lds.tile.v[to]) + to_lane));
   };
-  {
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) dq[dt][x] = pk[FIX ? dt : 0][x] = 0;
-    fit = Fit<T>();
-    off = 0;
-    if (tid < 2) lds.odd[tid] = 0;
-    fetch(t0);
-    __syncthreads();
-    put(t0, t0 & 1);
-    for (int t = t0; t <= t1; ++t) {
-      const int from = t & 1;
+  if (tid < 4) lds.odd[tid] = 0;
+  const int first = SPLIT ? t0 + wave : t0;
+  if (first <= t1) fetch(first);
+  __syncthreads();
+  if (!SPLIT) put(first, first & 1, 0);
+  int slot = SPLIT ? wave : 0;
+  for (int t = first; t <= t1; t += BY) {
+    const int from = SPLIT ? wave : t & 1;
+    int next_slot = slot;
+    if (SPLIT) {
+      if (lane == 0) lds.odd[slot] = 0;
+      put(t, from, slot);
+    } else {
       __syncthreads();
-      if (!CAREFUL && cut(t) && lds.odd[from] == t + 1) return false;
-      if (t < t1) fetch(t + 1);
-      const int k0 = t * KT;
-      const bool none = k0 > w0 + 31 || (a.window && k0 + KT - 1 <= w0 - a.window);
-      if (!none) {
-        const bool part = k0 + KT - 1 > w0 || (a.window && k0 <= w0 + 31 - a.window);
-        auto seen = [&](int r) {
-          const int j = k0 + r;
-          return j <= row && (!a.window || j > row - a.window);
-        };
-        f32x16 s, d;
+      next_slot = slot == 2 ? 0 : slot + 1;
+      if (tid == 0) lds.odd[next_slot == 2 ? 0 : next_slot + 1] = 0;
+    }
+    if (t + BY <= t1) fetch(t + BY);
+    const int k0 = t * KT;
+    const bool none = k0 > w0 + 31 || k0 + KT - 1 <= w0 - a.window;
+    if (!none) {
+      f32x16 s, d;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) s[x] = 0, d[x] = neg_delta;
-        const uint32_t k_at = hidden(lds_at(lds.k[from]) + rows_lane), v_at = hidden(lds_at(lds.v[from]) + rows_lane);
-        s = scores<T, D>(k_at, 0, qc, s);
-        if constexpr (FIX) d = scores<T, D>(v_at, hidden(lds_at(lds.own[wave]) + rows_lane), d);
-        else d = scores<T, D>(v_at, 0, oc, d);
-        float w[16], u[16];
+      for (int x = 0; x < 16; ++x) s[x] = 0, d[x] = neg_delta;
+      const uint32_t k_at = hidden(lds_at(lds.tile.k[from]) + rows_lane), v_at = hidden(lds_at(lds.tile.v[from]) + rows_lane);
+      s = scores<T, D>(k_at, 0, qc, s);
+      if constexpr (FIX) d = scores<T, D>(v_at, hidden(lds_at(own) + rows_lane), d);
+      else d = scores<T, D>(v_at, 0, oc, d);
+      float w[16], u[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        w[x] = __builtin_amdgcn_exp2f(fmaf(s[x], c, neg_lse));
+        u[x] = w[x] * d[x];
+      }
+      if (k0 + KT - 1 > w0 || k0 <= w0 + 31 - a.window) {
+        rarely();
+        const int from_key = (int)hidden(row - k0 - 4 * h);
+        const uint32_t fine = hidden(~lds.odd[slot] >> (4 * h));
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          w[x] = __builtin_amdgcn_exp2f(fmaf(s[x], c, neg_lse));
-          u[x] = w[x] * d[x];
-        }
-        if (part) {
-        rarely();
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const bool in = seen(block_row(x, h));
-            w[x] = in ? w[x] : 0.0f;
-            u[x] = in ? u[x] : 0.0f;
-          }
-        }
-        if constexpr (FIX) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) off += u[x];
-        }
-        fit.scale(u, dq);
-        const uint32_t kd_at = hidden(lds_at(lds.k[from]) + d_lane);
-        bool done = false;
-        if constexpr (CAREFUL) {
-          if (part) {
-            contract_seen<T, D, 0, DT, true>(kd_at, 0, u, dq, seen);
-            if constexpr (FIX) contract_seen<T, D, 0, DT, true>(kd_at, 0, w, pk, seen);
-            done = true;
-          }
-        }
-        if (!done) {
-          if constexpr (FIX) contract_two<T, D>(kd_at, u, dq, w, pk);
-          else contract<T, D, 0, DT>(kd_at, 0, u, dq);
+          const int r = block_row(x, 0);
+          const bool in = r <= from_key && r > from_key - a.window && (fine >> r & 1);
+          w[x] = in ? w[x] : 0.0f;
+          u[x] = in ? u[x] : 0.0f;
         }
       }
-      if (t < t1) put(t + 1, from ^ 1);
+      if constexpr (FIX) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) off += u[x];
+      }
+      fit.scale(u, dq);
+      const uint32_t kd_at = hidden(lds_at(lds.tile.k[from]) + d_lane);
+      if constexpr (FIX) contract_two<T, D>(kd_at, u, dq, w, pk);
+      else contract<T, D, 0, DT, 1>(kd_at, 0, u, dq);
     }
+    if (!SPLIT && t < t1) put(t + 1, from ^ 1, next_slot);
+    slot = next_slot;
+  }
+  if constexpr (FIX) off = both_sum(off);
+  if constexpr (SPLIT && FIX) {
+    lds.off[wave][lane] = off;
+    __syncthreads();
+    off = (lds.off[0][lane] + lds.off[1][lane]) + (lds.off[2][lane] + lds.off[3][lane]);
   }
   if constexpr (FIX) {
-    off = both_sum(off);
     neg_delta -= off;
     const float by = off / fit.back();
 #pragma unroll
@@ -207,209 +224,236 @@ __device__ __forceinline__ bool rows_grad(const PromptArgs& a, RowsLds<T, D>& ld
 #pragma unroll
       for (int x = 0; x < 16; ++x) dq[dt][x] -= by * pk[dt][x];
   }
-  if (row < p.n) {
+  if constexpr (SPLIT) {
+    if (!FIX) __syncthreads();
+    put_part(lds.join, dq, fit.back());
+    __syncthreads();
+#pragma unroll
+    for (int dt = 0; dt < DT; dt += 4)
+      if (dt + wave < DT && row < p.n) {
+        const f32x16 y[1] = {joined(lds.join, dt + wave)};
+        store_column<T, 1>(a.dq, p.start, head, row, a.dim, 32 * (dt + wave), y, a.scale);
+      }
+  } else if (row < p.n) {
     store_column<T, DT>(a.dq, p.start, head, row, a.dim, 0, dq, a.scale * fit.back());
-    if (h == 0) {
-      const int64_t at = (int64_t)head * a.rows + p.start + row;
-      a.neg_lse[at] = neg_lse;
-      a.neg_delta[at] = neg_delta;
-    }
   }
-  return true;
-}
-
-// Called rather than a part of the kernel, so that it costs the usual way no registers.
-template <typename T, int D>
-__device__ __attribute__((noinline)) void rows_grad_carefully(PromptArgs a, RowsLds<T, D>* lds) {
-  __syncthreads();
-  rows_grad<T, D, true>(a, *lds);
-}
-
-template <typename T, int D>
-__global__ __launch_bounds__(NT, D == 256 || (D == 128 && sizeof(T) == 4) ? 1 : 2) void prompt_rows_grad(PromptArgs a) {
-  __shared__ RowsLds<T, D> lds;
-  if (!rows_grad<T, D, false>(a, lds)) rows_grad_carefully<T, D>(a, &lds);
+  if (row < p.n && h == 0 && (!SPLIT || wave == 0)) {
+    const int64_t at = (int64_t)head * a.rows + p.start + row;
+    a.neg_lse[at] = neg_lse;
+    a.neg_delta[at] = neg_delta;
+  }
 }
 
 // ---------------------------------------------------------------- keys and values
 
 constexpr int QT = 32;
 
-template <typename T, int D>
+template <typename T, int D, int DN, bool SPLIT>
 struct KeysLds {
   static constexpr bool OWN = sizeof(T) == 2 && D == 128;   // values are held here: no registers left
-  LdsTile<T, D, QT> q[2], o[2];
-  typename std::conditional<OWN, LdsTile<T, D, 32>, int>::type own[4];
-  alignas(16) float row[2][2][QT];        // -lse log2 e, -delta
-  int odd[2];
+  union {
+    struct { LdsTile<T, D, QT> q[SPLIT ? 4 : 2], o[SPLIT ? 4 : 2]; } tile;
+    typename std::conditional<SPLIT, JoinLds<DN>, int>::type join;
+  };
+  typename std::conditional<OWN, LdsTile<T, D, 32>, int>::type own[SPLIT ? 1 : 4];
+  alignas(16) float row[SPLIT ? 4 : 2][2][QT];   // -lse log2 e, -delta
+  int odd;                                // gradients that were taken out of tiles
+  __device__ KeysLds() {}
 };
 
 // Values 32 D0 .. of a head's: a head of 256 is taken in two halves, whose sums would
 // not fit the registers together.
-template <typename T, int D, int D0, int DN, bool CAREFUL>
-__device__ __forceinline__ bool keys_grad(const PromptArgs& a, KeysLds<T, D>& lds) {
-  const int g = blockIdx.x % a.heads, unit = blockIdx.x / a.heads;
-  constexpr int BN = 128, STEPS = D / Op<T>::STEP;
-  constexpr bool OWN = KeysLds<T, D>::OWN;
+template <typename T, int D, int D0, int DN, bool SPLIT>
+__device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN, SPLIT>& lds) {
+  constexpr int BN = SPLIT ? 32 : 128, STEPS = D / Op<T>::STEP, BY = SPLIT ? 4 : 1;
+  constexpr bool OWN = KeysLds<T, D, DN, SPLIT>::OWN;
   typedef LdsTile<T, D, QT> Tile;
+  typedef Staged<T, D, QT, SPLIT ? 64 : NT> Stage;
+  const int g = blockIdx.x % a.heads, unit = blockIdx.x / a.heads;
   Prompt p;
   int tile;
-  if (!find_tile(a, BN, unit, p, tile)) return true;
+  if (!find_tile(a, BN, unit, p, tile)) return;
   tile = (p.n + BN - 1) / BN - 1 - tile;           // early keys are seen most: they come first
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int k0 = tile * BN, w0 = k0 + 32 * wave, key = w0 + (lane & 31);
-  const uint32_t to_lane = Staged<T, D, QT, NT>::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
+  const int k0 = tile * BN, w0 = SPLIT ? k0 : k0 + 32 * wave, key = w0 + (lane & 31);
+  const uint32_t to_lane = Stage::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
+  auto& own = lds.own[SPLIT ? 0 : wave];           // SPLIT: all waves write the same
   typename Op<T>::frag kc[STEPS], vc[OWN ? 1 : STEPS];
   if constexpr (OWN) {
     load_column<T, D>(a.v, p.start, g, key, p.n, a.dim, kc);
-    put_column<T, D>(lds_at(lds.own[wave]) + rows_lane, kc);
+    put_column<T, D>(lds_at(own) + rows_lane, kc);
   } else {
     load_column<T, D>(a.v, p.start, g, key, p.n, a.dim, vc);
   }
   load_column<T, D>(a.k, p.start, g, key, p.n, a.dim, kc);
   const float c = a.scale * kPromptLog2e;
   f32x16 dk[DN], dv[DN];
+#pragma unroll
+  for (int dt = 0; dt < DN; ++dt)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) dk[dt][x] = dv[dt][x] = 0;
   Fit<T> fit_p, fit_s;
 
-  const int t0 = k0 / QT, last = a.window && k0 + BN - 1 < p.n - a.window ? k0 + BN - 1 + a.window : p.n - 1;
-  const int tiles = last / QT - t0 + 1, total = tiles * a.share;
-  Staged<T, D, QT, NT> sq, so;
+  const TileSpan span = rows_of_keys(k0, BN, p.n, a.window, QT);
+  const int t0 = span.first, t1 = span.last, total = (t1 - t0 + 1) * a.share;
+  Stage sq, so;
   float srow = 0;
-  int next_head, next_row;                // the tile on its way: its query head and first row
+  // the tile on its way: its query head and first row
+  int next_head = g * a.share, next_row = t0 * QT;
+  auto onward = [&](int n) __attribute__((always_inline)) {
+    next_row += n * QT;
+    while (next_row > t1 * QT) next_row -= (t1 - t0 + 1) * QT, ++next_head;
+  };
   // whether some key of the workgroup is not seen by all rows of a tile
-  auto cut = [&](int r0) { return r0 < k0 + BN - 1 || (a.window && r0 + QT - 1 - a.window >= k0); };
+  auto cut = [&](int r0) { return r0 < k0 + BN - 1 || r0 + QT - 1 - a.window >= k0; };
   auto fetch = [&]() __attribute__((always_inline)) {
     sq.load(a.q, p.start, next_head, next_row, p.n, a.dim);
     so.load(a.dout, p.start, next_head, next_row, p.n, a.dim);
-    if (tid < 64) {
-      const int row = next_row + (tid & 31);
-      const float* from = (tid < 32 ? a.neg_lse : a.neg_delta) + (int64_t)next_head * a.rows + p.start;
+    if (SPLIT || tid < 64) {
+      const int row = next_row + (lane & 31);
+      const float* from = (lane < 32 ? a.neg_lse : a.neg_delta) + (int64_t)next_head * a.rows + p.start;
       const float y = from[min(row, p.n - 1)];
-      srow = row < p.n ? y : tid < 32 ? -INFINITY : 0.0f;
+      srow = row < p.n ? y : lane < 32 ? -INFINITY : 0.0f;
     }
   };
-  auto put = [&](int it, int to) __attribute__((always_inline)) {
-    sq.store(hidden(lds_at(lds.q[to]) + to_lane));
-    so.store(hidden(lds_at(lds.o[to]) + to_lane));
-    if (tid < 64) lds.row[to][tid >> 5][tid & 31] = srow;
+  auto put = [&](int to) __attribute__((always_inline)) {
     if (cut(next_row)) {
       rarely();
-      if (sq.odd() || so.odd()) lds.odd[to] = it + 1;
+      // 0 times them would not be 0.  A row of such a query has no lse, one of such a
+      // gradient no delta; what of it belongs to dv is added in the end.
+      sq.clean();
+      if (so.clean()) lds.odd = 1;
     }
+    sq.store(hidden(lds_at(lds.tile.q[to]) + to_lane));
+    so.store(hidden(lds_at(lds.tile.o[to]) + to_lane));
+    if (SPLIT || tid < 64) lds.row[to][lane >> 5][lane & 31] = srow;
   };
-  {
-#pragma unroll
-    for (int dt = 0; dt < DN; ++dt)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) dk[dt][x] = dv[dt][x] = 0;
-    fit_p = fit_s = Fit<T>();
-    next_head = g * a.share;
-    next_row = t0 * QT;
-    if (tid < 2) lds.odd[tid] = 0;
-    fetch();
-    __syncthreads();
-    put(0, 0);
-    for (int it = 0; it < total; ++it) {
-      const int from = it & 1, r0 = next_row;
-      __syncthreads();
-      if (!CAREFUL && cut(r0) && lds.odd[from] == it + 1) return false;
-      if (it + 1 < total) {
-        next_row += QT;
-        if (next_row > last) next_row = t0 * QT, ++next_head;
-        fetch();
-      }
-      const bool none = r0 + QT - 1 < w0 || (a.window && r0 - a.window >= w0 + 31);
-      if (!none) {
-        const bool part = r0 < w0 + 31 || (a.window && r0 + QT - 1 - a.window >= w0);
-        auto seen = [&](int r) {
-          const int i = r0 + r;
-          return key <= i && (!a.window || key > i - a.window);
-        };
-        f32x16 s, d;
-        float w[16], u[16];
-#pragma unroll
-        for (int x = 0; x < 16; x += 4) {
-          const f32x4 z = *reinterpret_cast<const f32x4*>(&lds.row[from][1][block_row(x, h)]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[x + i] = 0, d[x + i] = z[i];
-        }
-        s = scores<T, D>(hidden(lds_at(lds.q[from]) + rows_lane), 0, kc, s);
-        const uint32_t do_at = hidden(lds_at(lds.o[from]) + rows_lane);
-        if constexpr (OWN) d = scores<T, D>(do_at, hidden(lds_at(lds.own[wave]) + rows_lane), d);
-        else d = scores<T, D>(do_at, 0, vc, d);
-#pragma unroll
-        for (int x = 0; x < 16; x += 4) {
-          const f32x4 y = *reinterpret_cast<const f32x4*>(&lds.row[from][0][block_row(x, h)]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[x + i] = __builtin_amdgcn_exp2f(fmaf(s[x + i], c, y[i]));
-            u[x + i] = w[x + i] * d[x + i];
-          }
-        }
-        if (part) {
-        rarely();
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const bool in = seen(block_row(x, h));
-            w[x] = in ? w[x] : 0.0f;
-            u[x] = in ? u[x] : 0.0f;
-          }
-        }
-        fit_p.scale(w, dv);
-        fit_s.scale(u, dk);
-        const uint32_t q_at = hidden(lds_at(lds.q[from]) + d_lane), o_at = hidden(lds_at(lds.o[from]) + d_lane);
-        bool done = false;
-        if constexpr (CAREFUL) {
-          if (part) {
-            contract_seen<T, D, D0, DN, false>(o_at, 0, w, dv, seen);
-            contract_seen<T, D, D0, DN, true>(q_at, 0, u, dk, seen);
-            done = true;
-          }
-        }
-        if (!done) {
-          contract<T, D, D0, DN>(o_at, 0, w, dv);
-          contract<T, D, D0, DN>(q_at, 0, u, dk);
-        }
-      }
-      if (it + 1 < total) put(it + 1, from ^ 1);
+  if (tid == 0) lds.odd = 0;
+  const int first = SPLIT ? wave : 0;
+  if (SPLIT) onward(wave);
+  if (first < total) fetch();
+  __syncthreads();
+  if (!SPLIT) put(0);
+  for (int it = first; it < total; it += BY) {
+    const int from = SPLIT ? wave : it & 1, r0 = next_row;
+    if (SPLIT) put(from);
+    else __syncthreads();
+    if (it + BY < total) {
+      onward(BY);
+      fetch();
     }
+    const bool none = r0 + QT - 1 < w0 || r0 - a.window >= w0 + 31;
+    if (!none) {
+      f32x16 s, d;
+      float w[16], u[16];
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(&lds.row[from][1][block_row(x, h)]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x + i] = 0, d[x + i] = z[i];
+      }
+      s = scores<T, D>(hidden(lds_at(lds.tile.q[from]) + rows_lane), 0, kc, s);
+      const uint32_t do_at = hidden(lds_at(lds.tile.o[from]) + rows_lane);
+      if constexpr (OWN) d = scores<T, D>(do_at, hidden(lds_at(own) + rows_lane), d);
+      else d = scores<T, D>(do_at, 0, vc, d);
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&lds.row[from][0][block_row(x, h)]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[x + i] = __builtin_amdgcn_exp2f(fmaf(s[x + i], c, y[i]));
+          u[x + i] = w[x + i] * d[x + i];
+        }
+      }
+      if (r0 < w0 + 31 || r0 + QT - 1 - a.window >= w0) {
+        rarely();
+        const int from_row = (int)hidden(key - r0 - 4 * h);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const bool in = block_row(x, 0) >= from_row && block_row(x, 0) < from_row + a.window;
+          w[x] = in ? w[x] : 0.0f;
+          u[x] = in ? u[x] : 0.0f;
+        }
+      }
+      fit_p.scale(w, dv);
+      fit_s.scale(u, dk);
+      const uint32_t q_at = hidden(lds_at(lds.tile.q[from]) + d_lane), o_at = hidden(lds_at(lds.tile.o[from]) + d_lane);
+      contract<T, D, D0, DN, 1>(o_at, 0, w, dv);
+      contract<T, D, D0, DN, 1>(q_at, 0, u, dk);
+    }
+    if (!SPLIT && it + 1 < total) put(from ^ 1);
   }
-  if (key < p.n) {
+  __syncthreads();
+  if (lds.odd) {
+    rarely();
+    for (int hs = 0; hs < a.share; ++hs)
+      for (int t = t0; t <= t1; ++t)
+        if (cut(t * QT))
+          add_odd<T, DN>(a.dout, p.start, g * a.share + hs, t * QT, min(t * QT + QT, p.n), a.dim, 32 * D0, dv,
+                         [&](int i) { return key <= i && key > i - a.window; });
+  }
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int both = 0; both < 2; ++both) {
+      put_part(lds.join, both ? dv : dk, both ? fit_p.back() : fit_s.back());
+      __syncthreads();
+#pragma unroll
+      for (int dt = 0; dt < DN; dt += 4)
+        if (dt + wave < DN && key < p.n) {
+          const f32x16 y[1] = {joined(lds.join, dt + wave)};
+          store_column<T, 1>(both ? a.dv : a.dk, p.start, g, key, a.dim, 32 * (D0 + dt + wave), y, both ? 1.0f : a.scale);
+        }
+      __syncthreads();
+    }
+  } else if (key < p.n) {
     store_column<T, DN>(a.dk, p.start, g, key, a.dim, 32 * D0, dk, a.scale * fit_s.back());
     store_column<T, DN>(a.dv, p.start, g, key, a.dim, 32 * D0, dv, fit_p.back());
   }
-  return true;
 }
 
-template <typename T, int D, bool CAREFUL>
-__device__ __forceinline__ bool keys_grad_of(const PromptArgs& a, KeysLds<T, D>& lds) {
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__(NT, (!SPLIT && sizeof(T) == 2 && D <= 128) ? 2 : 1) void prompt_keys_grad(PromptArgs a) {
   if constexpr (D == 256) {
-    return blockIdx.y == 0 ? keys_grad<T, D, 0, 4, CAREFUL>(a, lds) : keys_grad<T, D, 4, 4, CAREFUL>(a, lds);
+    __shared__ KeysLds<T, D, 4, SPLIT> lds;
+    if (blockIdx.y == 0) keys_grad<T, D, 0, 4, SPLIT>(a, lds);
+    else keys_grad<T, D, 4, 4, SPLIT>(a, lds);
   } else {
-    return keys_grad<T, D, 0, D / 32, CAREFUL>(a, lds);
+    __shared__ KeysLds<T, D, D / 32, SPLIT> lds;
+    keys_grad<T, D, 0, D / 32, SPLIT>(a, lds);
   }
 }
 
-template <typename T, int D>
-__device__ __attribute__((noinline)) void keys_grad_carefully(PromptArgs a, KeysLds<T, D>* lds) {
-  __syncthreads();
-  keys_grad_of<T, D, true>(a, *lds);
+template <typename T, int D, bool SPLIT>
+kronq_status launch_rows(const PromptArgs& a, hipStream_t s) {
+  const int64_t units = (int64_t)a.rows / (SPLIT ? 32 : 128) + a.seqs;
+  hipLaunchKernelGGL((prompt_rows_grad<T, D, SPLIT>), dim3((unsigned)(units * a.heads * a.share)), dim3(NT), 0, s, a);
+  KQ_LAUNCHED("prompt_rows_grad");
+  return KRONQ_OK;
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(NT, (sizeof(T) == 2 && D <= 128) ? 2 : 1) void prompt_keys_grad(PromptArgs a) {
-  __shared__ KeysLds<T, D> lds;
-  if (!keys_grad_of<T, D, false>(a, lds)) keys_grad_carefully<T, D>(a, &lds);
+template <typename T, int D, bool SPLIT>
+kronq_status launch_keys(const PromptArgs& a, hipStream_t s) {
+  const int64_t units = (int64_t)a.rows / (SPLIT ? 32 : 128) + a.seqs;
+  hipLaunchKernelGGL((prompt_keys_grad<T, D, SPLIT>), dim3((unsigned)(units * a.heads), D == 256 ? 2 : 1), dim3(NT), 0, s, a);
+  KQ_LAUNCHED("prompt_keys_grad");
+  return KRONQ_OK;
 }
+
+// SPLIT below that many workgroups of 128 rows (keys).
+constexpr int64_t kRowsSplitBelow = 512, kKeysSplitBelow = 512;
 
 template <typename T, int D>
 kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)a.rows / 128 + a.seqs;
-  hipLaunchKernelGGL((prompt_rows_grad<T, D>), dim3((unsigned)(units * a.heads * a.share)), dim3(NT), 0, s, a);
-  KQ_LAUNCHED("prompt_rows_grad");
-  hipLaunchKernelGGL((prompt_keys_grad<T, D>), dim3((unsigned)(units * a.heads), D == 256 ? 2 : 1), dim3(NT), 0, s, a);
-  KQ_LAUNCHED("prompt_keys_grad");
-  return KRONQ_OK;
+  kronq_status st;
+  // fp32 heads of 256 have no room for four waves' tiles
+  if constexpr (!(sizeof(T) == 4 && D == 256)) {
+    st = units * a.heads * a.share <= kRowsSplitBelow ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
+    if (st) return st;
+    return units * a.heads <= kKeysSplitBelow ? launch_keys<T, D, true>(a, s) : launch_keys<T, D, false>(a, s);
+  }
+  st = launch_rows<T, D, false>(a, s);
+  return st ? st : launch_keys<T, D, false>(a, s);
 }
 
 template <typename T>
