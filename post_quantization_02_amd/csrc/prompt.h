@@ -38,16 +38,44 @@ constexpr float kPromptLog2e = 1.44269504088896340736f, kPromptLn2 = 0.693147180
 
 // ---------------------------------------------------------------- where a workgroup works
 
-// Tile number `unit` of all sequences' tiles of bm rows: its sequence, and which of
-// its tiles, counted from the last one (late rows see most: they come first).
-// False: there are fewer.
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit, Prompt& p, int& tile) {
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  return __builtin_amdgcn_readfirstlane(x);
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x = max(x, __shfl_xor(x, o));
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
+// Tile number `unit` of all sequences' tiles of bm rows: its sequence, and how many tiles it
+// has to do with (`much`: 1 .. the sequence's), the most first, so that the last
+// workgroups to start are the short ones.  Sequences beyond 64 are taken one behind the
+// other, each from its longest tile on.  False: there are fewer tiles.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit, Prompt& p, int& much) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     Prompt mine{0, 0};
     if (b0 + lane < a.seqs) mine = prompt_between(a.cu[b0 + lane], a.cu[b0 + lane + 1], a.rows);
     const int tiles = (mine.n + bm - 1) / bm;
+    if (a.seqs <= 64) {
+      int lo = 0, hi = wave_max(tiles), upto = 0;  // tiles of more than hi: at most unit, of more than lo: more
+      if (wave_sum(tiles) <= unit) return false;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, n = wave_sum(max(tiles - mid, 0));
+        if (n <= unit) hi = mid, upto = n;
+        else lo = mid;
+      }
+      const uint64_t some = __ballot(tiles >= hi);
+      const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
+      const int at = __ffsll((unsigned long long)__ballot(tiles >= hi && rank == unit - upto)) - 1;
+      p.start = __builtin_amdgcn_readlane(mine.start, at);
+      p.n = __builtin_amdgcn_readlane(mine.n, at);
+      much = hi;
+      return true;
+    }
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -59,7 +87,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int bm, int unit,
       const int at = __ffsll((unsigned long long)past) - 1;
       p.start = __builtin_amdgcn_readlane(mine.start, at);
       p.n = __builtin_amdgcn_readlane(mine.n, at);
-      tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - unit;
+      much = before + __builtin_amdgcn_readlane(upto, at) - unit;
       return true;
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -186,10 +214,21 @@ __device__ __forceinline__ uint32_t hidden(uint32_t x) {
   return x;
 }
 
+// LDS is written in other units than it is read in.
 template <typename V>
 __device__ __forceinline__ V lds_read(uint32_t at) {
-  return *(const __attribute__((address_space(3))) V*)(uintptr_t)at;
+  typedef V __attribute__((may_alias)) Any;
+  return *(const __attribute__((address_space(3))) Any*)(uintptr_t)at;
 }
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, V x) {
+  typedef V __attribute__((may_alias)) Any;
+  *(__attribute__((address_space(3))) Any*)(uintptr_t)at = x;
+}
+
+// Between what a wave writes to its own LDS and what its other lanes read of it: the
+// hardware keeps their order, the compiler has to.
+__device__ __forceinline__ void own_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // ROWS rows of D values (D a power of two; what a head has fewer is 0), in 16-byte
 // pieces that are exchanged within a row, piece c of a row at c ^ turn(row), so that
@@ -282,8 +321,7 @@ struct Staged {
   __device__ __forceinline__ void store(uint32_t at) const {
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
-      *(__attribute__((address_space(3))) u32x4*)(uintptr_t)((at ^ (uint32_t)Tile::turn(i * APART) << 4) +
-                                                             (uint32_t)(i * APART * Tile::BYTES)) = w[i];
+      lds_write((at ^ (uint32_t)Tile::turn(i * APART) << 4) + (uint32_t)(i * APART * Tile::BYTES), w[i]);
   }
   // Takes out what is not finite; the rows of the tile (from 0 on, of the first 32) that this
   // thread found any in.
@@ -325,8 +363,8 @@ __device__ __forceinline__ void load_column(const HeadsView& x, int64_t first, i
 template <typename T, int D>
 __device__ __forceinline__ void put_column(uint32_t at, const typename Op<T>::frag (&f)[D / Op<T>::STEP]) {
 #pragma unroll
-  for (int s = 0; s < D / Op<T>::STEP; ++s)
-    *(__attribute__((address_space(3))) typename Op<T>::frag*)(uintptr_t)(at ^ (uint32_t)(2 * s) << 4) = f[s];
+  for (int s = 0; s < D / Op<T>::STEP; ++s) lds_write(at ^ (uint32_t)(2 * s) << 4, f[s]);
+  own_lds();
 }
 
 // A block of scores whose columns are such a tile's (at their place and rows_lane).

@@ -18,7 +18,14 @@ namespace kronq {
 namespace {
 
 constexpr int NT = 256;
-constexpr int64_t kSplitBelow = 512;   // workgroups of 128 rows
+
+// SPLIT up to that many workgroups of 128 rows.  Split and whole, us: bf16, dim 128, 64
+// workgroups (4000 rows of 2 heads) 34 and 99, 192 21 and 23, 320 36 and 37, 480 47 and 40;
+// dim 64, 256 17 and 20, 480 25 and 24; dim 256, 64 40 and 55, 128 89 and 94, 420 477 and
+// 183; fp32, whose products take longer than a tile's way to LDS, 544 253 and 376, 690 606
+// and 629, 2800 2433 and 1860.
+template <typename T, int D>
+constexpr int64_t kSplitUpTo = sizeof(T) == 4 ? 704 : D == 256 ? 128 : 320;
 
 // KT: keys of a tile.  More waves on a SIMD are worth more than longer tiles: dim 128
 // in bf16 with tiles of 64 keys and two waves a SIMD 830 us, of 32 and three 808.
@@ -52,10 +59,10 @@ __global__ __launch_bounds__(NT, (Shape<T, D, SPLIT>::PER_SIMD)) void prompt_att
   const int g = blockIdx.x % a.heads, hs = blockIdx.x / a.heads % a.share, unit = blockIdx.x / (a.heads * a.share);
   const int head = g * a.share + hs;
   Prompt p;
-  int tile;
-  if (!find_tile(a, BM, unit, p, tile)) return;
+  int much;
+  if (!find_tile(a, BM, unit, p, much)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r0 = tile * BM, w0 = SPLIT ? r0 : r0 + 32 * wave, row = w0 + (lane & 31);
+  const int r0 = (much - 1) * BM, w0 = SPLIT ? r0 : r0 + 32 * wave, row = w0 + (lane & 31);
 
   typename Op<T>::frag q[D / Op<T>::STEP];
   load_column<T, D>(a.q, p.start, head, row, p.n, a.dim, q);
@@ -96,7 +103,7 @@ __global__ __launch_bounds__(NT, (Shape<T, D, SPLIT>::PER_SIMD)) void prompt_att
   if (!SPLIT) put(first, first & 1);
   for (int t = first; t <= t1; t += BY) {
     const int from = SPLIT ? wave : t & 1;
-    if (SPLIT) put(t, from);
+    if (SPLIT) own_lds(), put(t, from), own_lds();
     else __syncthreads();
     if (t + BY <= t1) fetch(t + BY);
     const int k0 = t * KT;
@@ -193,7 +200,7 @@ kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
   const int64_t wide = ((int64_t)a.rows / 128 + a.seqs) * a.heads * a.share;
   // fp32 heads of 256 have no room for four waves' tiles
   if constexpr (!(sizeof(T) == 4 && D == 256)) {
-    if (wide <= kSplitBelow) {
+    if (wide <= kSplitUpTo<T, D>) {
       const int64_t grid = ((int64_t)a.rows / 32 + a.seqs) * a.heads * a.share;
       hipLaunchKernelGGL((prompt_attention<T, D, true>), dim3((unsigned)grid), dim3(NT), 0, s, a);
       KQ_LAUNCHED("prompt_attention");

@@ -91,10 +91,10 @@ __global__ __launch_bounds__(NT, SPLIT || D == 256 || (D == 128 && sizeof(T) == 
   const int g = blockIdx.x % a.heads, hs = blockIdx.x / a.heads % a.share, unit = blockIdx.x / (a.heads * a.share);
   const int head = g * a.share + hs;
   Prompt p;
-  int tile;
-  if (!find_tile(a, BM, unit, p, tile)) return;
+  int much;
+  if (!find_tile(a, BM, unit, p, much)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r0 = tile * BM, w0 = SPLIT ? r0 : r0 + 32 * wave, row = w0 + (lane & 31);
+  const int r0 = (much - 1) * BM, w0 = SPLIT ? r0 : r0 + 32 * wave, row = w0 + (lane & 31);
   const uint32_t to_lane = Stage::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
   auto& own = lds.own[SPLIT ? 0 : wave];           // SPLIT: all waves write the same
 
@@ -162,8 +162,11 @@ __global__ __launch_bounds__(NT, SPLIT || D == 256 || (D == 128 && sizeof(T) == 
     const int from = SPLIT ? wave : t & 1;
     int next_slot = slot;
     if (SPLIT) {
+      own_lds();
       if (lane == 0) lds.odd[slot] = 0;
+      own_lds();
       put(t, from, slot);
+      own_lds();
     } else {
       __syncthreads();
       next_slot = slot == 2 ? 0 : slot + 1;
@@ -271,11 +274,10 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
   typedef Staged<T, D, QT, SPLIT ? 64 : NT> Stage;
   const int g = blockIdx.x % a.heads, unit = blockIdx.x / a.heads;
   Prompt p;
-  int tile;
-  if (!find_tile(a, BN, unit, p, tile)) return;
-  tile = (p.n + BN - 1) / BN - 1 - tile;           // early keys are seen most: they come first
+  int much;
+  if (!find_tile(a, BN, unit, p, much)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int k0 = tile * BN, w0 = SPLIT ? k0 : k0 + 32 * wave, key = w0 + (lane & 31);
+  const int k0 = ((p.n + BN - 1) / BN - much) * BN, w0 = SPLIT ? k0 : k0 + 32 * wave, key = w0 + (lane & 31);
   const uint32_t to_lane = Stage::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
   auto& own = lds.own[SPLIT ? 0 : wave];           // SPLIT: all waves write the same
   typename Op<T>::frag kc[STEPS], vc[OWN ? 1 : STEPS];
@@ -336,7 +338,7 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
   if (!SPLIT) put(0);
   for (int it = first; it < total; it += BY) {
     const int from = SPLIT ? wave : it & 1, r0 = next_row;
-    if (SPLIT) put(from);
+    if (SPLIT) own_lds(), put(from), own_lds();
     else __syncthreads();
     if (it + BY < total) {
       onward(BY);
@@ -439,8 +441,14 @@ kronq_status launch_keys(const PromptArgs& a, hipStream_t s) {
   return KRONQ_OK;
 }
 
-// SPLIT below that many workgroups of 128 rows (keys).
-constexpr int64_t kRowsSplitBelow = 512, kKeysSplitBelow = 512;
+// SPLIT up to that many workgroups of 128 rows (keys).  Both kernels' time, us, with the
+// one's work split and whole: rows, bf16, dim 128, 64 workgroups 273 and 374, 192 197 and
+// 188, 320 344 and 310; dim 256, 64 381 and 442.  Keys, bf16, dim 128, 48 95 and 188, 176
+// 235 and 380, 320 428 and 450; dim 64, 232 183 and 338, 680 495 and 509; dim 256, 116 826
+// and 851; fp32, dim 128, 344 2254 and 2382, 700 8716 and 7999.
+constexpr int64_t kRowsSplitUpTo = 128;
+template <typename T, int D>
+constexpr int64_t kKeysSplitUpTo = sizeof(T) == 2 && D == 64 ? 640 : 384;
 
 template <typename T, int D>
 kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
@@ -448,9 +456,9 @@ kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
   kronq_status st;
   // fp32 heads of 256 have no room for four waves' tiles
   if constexpr (!(sizeof(T) == 4 && D == 256)) {
-    st = units * a.heads * a.share <= kRowsSplitBelow ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
+    st = units * a.heads * a.share <= kRowsSplitUpTo ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
     if (st) return st;
-    return units * a.heads <= kKeysSplitBelow ? launch_keys<T, D, true>(a, s) : launch_keys<T, D, false>(a, s);
+    return units * a.heads <= kKeysSplitUpTo<T, D> ? launch_keys<T, D, true>(a, s) : launch_keys<T, D, false>(a, s);
   }
   st = launch_rows<T, D, false>(a, s);
   return st ? st : launch_keys<T, D, false>(a, s);
