@@ -337,7 +337,7 @@ struct Staged {
         bad |= y != w[i][j];
         w[i][j] = y;
       }
-      rows |= bad ? 1u << ((r + i * APART) & 31) : 0;
+      rows |= bad ? 1u << ((r + i * APART) & 31) : 0u;
     }
     return rows;
   }
@@ -470,7 +470,7 @@ struct JoinLds { f32x4 b[4][DN][4][64]; };
 
 template <int DN>
 __device__ __forceinline__ void put_part(JoinLds<DN>& all, const f32x16 (&acc)[DN], float by) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3;
 #pragma unroll
   for (int dt = 0; dt < DN; ++dt)
 #pragma unroll

@@ -249,14 +249,22 @@ __global__ __launch_bounds__(NT, SPLIT || D == 256 || (D == 128 && sizeof(T) == 
 
 // ---------------------------------------------------------------- keys and values
 
-constexpr int QT = 32;
+// How a workgroup goes through its keys' rows: 128 keys by four waves, 32 keys split
+// (SPLIT), or 128 keys by eight waves, of which the second four take the second half of
+// each tile.  A key tile at a long sequence's start has many rows to go through, and where
+// there are few workgroups a CU the launch is as long as that takes: with eight waves
+// half as long for the same work.
+enum Way { kFour, kSplit, kEight };
 
-template <typename T, int D, int DN, bool SPLIT>
+template <typename T, int D, int DN, Way WAY>
 struct KeysLds {
+  static constexpr bool SPLIT = WAY == kSplit;
+  static constexpr int HALVES = WAY == kEight ? 2 : 1, QT = 32 * HALVES;
+  static constexpr bool JOINED = SPLIT || HALVES == 2;
   static constexpr bool OWN = sizeof(T) == 2 && D == 128;   // values are held here: no registers left
   union {
     struct { LdsTile<T, D, QT> q[SPLIT ? 4 : 2], o[SPLIT ? 4 : 2]; } tile;
-    typename std::conditional<SPLIT, JoinLds<DN>, int>::type join;
+    typename std::conditional<JOINED, JoinLds<DN>, int>::type join;
   };
   typename std::conditional<OWN, LdsTile<T, D, 32>, int>::type own[SPLIT ? 1 : 4];
   alignas(16) float row[SPLIT ? 4 : 2][2][QT];   // -lse log2 e, -delta
@@ -266,20 +274,24 @@ struct KeysLds {
 
 // Values 32 D0 .. of a head's: a head of 256 is taken in two halves, whose sums would
 // not fit the registers together.
-template <typename T, int D, int D0, int DN, bool SPLIT>
-__device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN, SPLIT>& lds) {
+template <typename T, int D, int D0, int DN, Way WAY>
+__device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN, WAY>& lds) {
+  constexpr bool SPLIT = WAY == kSplit;
   constexpr int BN = SPLIT ? 32 : 128, STEPS = D / Op<T>::STEP, BY = SPLIT ? 4 : 1;
-  constexpr bool OWN = KeysLds<T, D, DN, SPLIT>::OWN;
+  typedef KeysLds<T, D, DN, WAY> Lds;
+  constexpr bool OWN = Lds::OWN;
+  constexpr int HALVES = Lds::HALVES, QT = Lds::QT;
   typedef LdsTile<T, D, QT> Tile;
-  typedef Staged<T, D, QT, SPLIT ? 64 : NT> Stage;
+  typedef Staged<T, D, QT, SPLIT ? 64 : NT * HALVES> Stage;
   const int g = blockIdx.x % a.heads, unit = blockIdx.x / a.heads;
   Prompt p;
   int much;
   if (!find_tile(a, BN, unit, p, much)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int k0 = ((p.n + BN - 1) / BN - much) * BN, w0 = SPLIT ? k0 : k0 + 32 * wave, key = w0 + (lane & 31);
+  const int half = wave >> 2;             // of a tile's rows (SPLIT and four waves: 0)
+  const int k0 = ((p.n + BN - 1) / BN - much) * BN, w0 = SPLIT ? k0 : k0 + 32 * (wave & 3), key = w0 + (lane & 31);
   const uint32_t to_lane = Stage::lane(), rows_lane = Tile::rows_lane(), d_lane = Tile::d_lane();
-  auto& own = lds.own[SPLIT ? 0 : wave];           // SPLIT: all waves write the same
+  auto& own = lds.own[SPLIT ? 0 : wave & 3];       // who has the same keys writes the same
   typename Op<T>::frag kc[STEPS], vc[OWN ? 1 : STEPS];
   if constexpr (OWN) {
     load_column<T, D>(a.v, p.start, g, key, p.n, a.dim, kc);
@@ -300,6 +312,7 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
   const int t0 = span.first, t1 = span.last, total = (t1 - t0 + 1) * a.share;
   Stage sq, so;
   float srow = 0;
+  const int at = SPLIT ? lane : tid;      // which of a tile's rows' constants it loads
   // the tile on its way: its query head and first row
   int next_head = g * a.share, next_row = t0 * QT;
   auto onward = [&](int n) __attribute__((always_inline)) {
@@ -311,11 +324,11 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
   auto fetch = [&]() __attribute__((always_inline)) {
     sq.load(a.q, p.start, next_head, next_row, p.n, a.dim);
     so.load(a.dout, p.start, next_head, next_row, p.n, a.dim);
-    if (SPLIT || tid < 64) {
-      const int row = next_row + (lane & 31);
-      const float* from = (lane < 32 ? a.neg_lse : a.neg_delta) + (int64_t)next_head * a.rows + p.start;
+    if (SPLIT || tid < 2 * QT) {
+      const int row = next_row + at % QT;
+      const float* from = (at < QT ? a.neg_lse : a.neg_delta) + (int64_t)next_head * a.rows + p.start;
       const float y = from[min(row, p.n - 1)];
-      srow = row < p.n ? y : lane < 32 ? -INFINITY : 0.0f;
+      srow = row < p.n ? y : at < QT ? -INFINITY : 0.0f;
     }
   };
   auto put = [&](int to) __attribute__((always_inline)) {
@@ -328,7 +341,7 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
     }
     sq.store(hidden(lds_at(lds.tile.q[to]) + to_lane));
     so.store(hidden(lds_at(lds.tile.o[to]) + to_lane));
-    if (SPLIT || tid < 64) lds.row[to][lane >> 5][lane & 31] = srow;
+    if (SPLIT || tid < 2 * QT) lds.row[to][at / QT][at % QT] = srow;
   };
   if (tid == 0) lds.odd = 0;
   const int first = SPLIT ? wave : 0;
@@ -337,37 +350,38 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
   __syncthreads();
   if (!SPLIT) put(0);
   for (int it = first; it < total; it += BY) {
-    const int from = SPLIT ? wave : it & 1, r0 = next_row;
+    const int from = SPLIT ? wave : it & 1, r0 = next_row + 32 * half;
     if (SPLIT) own_lds(), put(from), own_lds();
     else __syncthreads();
     if (it + BY < total) {
       onward(BY);
       fetch();
     }
-    const bool none = r0 + QT - 1 < w0 || r0 - a.window >= w0 + 31;
+    const bool none = r0 + 31 < w0 || r0 - a.window >= w0 + 31;
+    constexpr int HALF = 32 * D * (int)sizeof(T);   // a half tile's bytes
     if (!none) {
       f32x16 s, d;
       float w[16], u[16];
 #pragma unroll
       for (int x = 0; x < 16; x += 4) {
-        const f32x4 z = *reinterpret_cast<const f32x4*>(&lds.row[from][1][block_row(x, h)]);
+        const f32x4 z = *reinterpret_cast<const f32x4*>(&lds.row[from][1][32 * half + block_row(x, h)]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[x + i] = 0, d[x + i] = z[i];
       }
-      s = scores<T, D>(hidden(lds_at(lds.tile.q[from]) + rows_lane), 0, kc, s);
-      const uint32_t do_at = hidden(lds_at(lds.tile.o[from]) + rows_lane);
+      s = scores<T, D>(hidden(lds_at(lds.tile.q[from]) + half * HALF + rows_lane), 0, kc, s);
+      const uint32_t do_at = hidden(lds_at(lds.tile.o[from]) + half * HALF + rows_lane);
       if constexpr (OWN) d = scores<T, D>(do_at, hidden(lds_at(own) + rows_lane), d);
       else d = scores<T, D>(do_at, 0, vc, d);
 #pragma unroll
       for (int x = 0; x < 16; x += 4) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(&lds.row[from][0][block_row(x, h)]);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&lds.row[from][0][32 * half + block_row(x, h)]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           w[x + i] = __builtin_amdgcn_exp2f(fmaf(s[x + i], c, y[i]));
           u[x + i] = w[x + i] * d[x + i];
         }
       }
-      if (r0 < w0 + 31 || r0 + QT - 1 - a.window >= w0) {
+      if (r0 < w0 + 31 || r0 + 31 - a.window >= w0) {
         rarely();
         const int from_row = (int)hidden(key - r0 - 4 * h);
 #pragma unroll
@@ -379,7 +393,8 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
       }
       fit_p.scale(w, dv);
       fit_s.scale(u, dk);
-      const uint32_t q_at = hidden(lds_at(lds.tile.q[from]) + d_lane), o_at = hidden(lds_at(lds.tile.o[from]) + d_lane);
+      const uint32_t q_at = hidden(lds_at(lds.tile.q[from]) + half * HALF + d_lane);
+      const uint32_t o_at = hidden(lds_at(lds.tile.o[from]) + half * HALF + d_lane);
       contract<T, D, D0, DN, 1>(o_at, 0, w, dv);
       contract<T, D, D0, DN, 1>(q_at, 0, u, dk);
     }
@@ -407,21 +422,42 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
         }
       __syncthreads();
     }
+  } else if constexpr (HALVES == 2) {
+#pragma unroll
+    for (int both = 0; both < 2; ++both) {
+      f32x16 (&acc)[DN] = both ? dv : dk;
+      const float by = both ? fit_p.back() : fit_s.back();
+      if (half) put_part(lds.join, acc, by);
+      __syncthreads();
+      if (!half) {
+#pragma unroll
+        for (int dt = 0; dt < DN; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 y = lds.join.b[wave][dt][i][lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[dt][4 * i + j] = acc[dt][4 * i + j] * by + y[j];
+          }
+        if (key < p.n) store_column<T, DN>(both ? a.dv : a.dk, p.start, g, key, a.dim, 32 * D0, acc, both ? 1.0f : a.scale);
+      }
+      __syncthreads();
+    }
   } else if (key < p.n) {
     store_column<T, DN>(a.dk, p.start, g, key, a.dim, 32 * D0, dk, a.scale * fit_s.back());
     store_column<T, DN>(a.dv, p.start, g, key, a.dim, 32 * D0, dv, fit_p.back());
   }
 }
 
-template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(NT, (!SPLIT && sizeof(T) == 2 && D <= 128) ? 2 : 1) void prompt_keys_grad(PromptArgs a) {
+template <typename T, int D, Way WAY>
+__global__ __launch_bounds__((WAY == kEight ? 2 * NT : NT), (WAY != kSplit && sizeof(T) == 2 && D <= 128) ? 2 : 1)
+void prompt_keys_grad(PromptArgs a) {
   if constexpr (D == 256) {
-    __shared__ KeysLds<T, D, 4, SPLIT> lds;
-    if (blockIdx.y == 0) keys_grad<T, D, 0, 4, SPLIT>(a, lds);
-    else keys_grad<T, D, 4, 4, SPLIT>(a, lds);
+    __shared__ KeysLds<T, D, 4, WAY> lds;
+    if (blockIdx.y == 0) keys_grad<T, D, 0, 4, WAY>(a, lds);
+    else keys_grad<T, D, 4, 4, WAY>(a, lds);
   } else {
-    __shared__ KeysLds<T, D, D / 32, SPLIT> lds;
-    keys_grad<T, D, 0, D / 32, SPLIT>(a, lds);
+    __shared__ KeysLds<T, D, D / 32, WAY> lds;
+    keys_grad<T, D, 0, D / 32, WAY>(a, lds);
   }
 }
 
@@ -433,10 +469,11 @@ kronq_status launch_rows(const PromptArgs& a, hipStream_t s) {
   return KRONQ_OK;
 }
 
-template <typename T, int D, bool SPLIT>
+template <typename T, int D, Way WAY>
 kronq_status launch_keys(const PromptArgs& a, hipStream_t s) {
-  const int64_t units = (int64_t)a.rows / (SPLIT ? 32 : 128) + a.seqs;
-  hipLaunchKernelGGL((prompt_keys_grad<T, D, SPLIT>), dim3((unsigned)(units * a.heads), D == 256 ? 2 : 1), dim3(NT), 0, s, a);
+  const int64_t units = (int64_t)a.rows / (WAY == kSplit ? 32 : 128) + a.seqs;
+  hipLaunchKernelGGL((prompt_keys_grad<T, D, WAY>), dim3((unsigned)(units * a.heads), D == 256 ? 2 : 1),
+                     dim3(WAY == kEight ? 2 * NT : NT), 0, s, a);
   KQ_LAUNCHED("prompt_keys_grad");
   return KRONQ_OK;
 }
@@ -449,6 +486,10 @@ kronq_status launch_keys(const PromptArgs& a, hipStream_t s) {
 constexpr int64_t kRowsSplitUpTo = 128;
 template <typename T, int D>
 constexpr int64_t kKeysSplitUpTo = sizeof(T) == 2 && D == 64 ? 640 : 384;
+// Eight waves up to that many (fp32 and heads of 256 have no room for them).  Both kernels'
+// time, us, eight and four: dim 128, 672 workgroups 583 and 719 and (longer sequences) 1374
+// and 1534, 1340 1598 and 1530; dim 64, 680 470 and 506, 1360 923 and 830.
+constexpr int64_t kEightUpTo = 1024;
 
 template <typename T, int D>
 kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
@@ -458,10 +499,14 @@ kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
   if constexpr (!(sizeof(T) == 4 && D == 256)) {
     st = units * a.heads * a.share <= kRowsSplitUpTo ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
     if (st) return st;
-    return units * a.heads <= kKeysSplitUpTo<T, D> ? launch_keys<T, D, true>(a, s) : launch_keys<T, D, false>(a, s);
+    if (units * a.heads <= kKeysSplitUpTo<T, D>) return launch_keys<T, D, kSplit>(a, s);
+    if constexpr (sizeof(T) == 2 && D <= 128)
+      if (units * a.heads <= kEightUpTo) return launch_keys<T, D, kEight>(a, s);
+    return launch_keys<T, D, kFour>(a, s);
+  } else {
+    st = launch_rows<T, D, false>(a, s);
+    return st ? st : launch_keys<T, D, kFour>(a, s);
   }
-  st = launch_rows<T, D, false>(a, s);
-  return st ? st : launch_keys<T, D, false>(a, s);
 }
 
 template <typename T>
