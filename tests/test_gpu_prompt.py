@@ -18,6 +18,14 @@ SHAPES = [
     ([127, 128, 129, 1, 0], 4, 4, 128, 0), ([300], 8, 1, 96, 0), ([257, 31], 3, 3, 256, 0), ([200, 90], 2, 1, 136, 70),
     ([150], 5, 1, 72, 1), ([400, 3], 2, 2, 128, 64), ([500], 2, 1, 64, 200), ([130], 2, 2, 16, 129), ([130], 2, 2, 128, 131),
 ]
+# Enough workgroups of 128 rows for the ways that long calls take: many short sequences beside
+# longer ones, many heads.  (lengths, query heads, key heads, dim, window)
+SHORT = [5, 1, 33, 2] * 9
+BUSY = [
+    ([300, 1, 200, 0] + SHORT, 32, 32, 64, 0), ([300, 1, 200, 0] + SHORT, 32, 16, 128, 90),
+    ([260, 129] + SHORT, 26, 26, 128, 0), ([290] + SHORT, 24, 24, 256, 150), ([260] + SHORT + [7] * 40, 24, 12, 64, 33),
+    ([257] + SHORT, 64, 8, 96, 0),
+]
 IDS = ["%s-%d-%d-%d-%d" % ("+".join(map(str, s[0])), *s[1:]) for s in SHAPES]
 
 
@@ -45,6 +53,22 @@ def test_attention(lengths, qh, kh, dim, window, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", range(len(BUSY)))
+def test_busy_calls(shape, dtype):
+    """Both directions where the chip is full."""
+    lengths, qh, kh, dim, window = BUSY[shape]
+    q, k, v, do, cu = prompt_case(lengths, qh, kh, dim, dtype, shape + 100, before=1, behind=2)
+    args = [t.to(DEV) for t in (q, k, v)]
+    out = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    kq.kronq_prompt_attention(*args, dev(cu), window=window, out=out, lse=lse)
+    check_forward(q, k, v, cu, out, lse, dtype, window)
+    grads = [torch.full(t.shape, 7.0, dtype=dtype, device=DEV) for t in (q, k, v)]
+    kq.kronq_prompt_attention_grad(do.to(DEV), *args, out, lse, dev(cu), window=window, dq=grads[0], dk=grads[1], dv=grads[2])
+    check_backward(q, k, v, do, cu, out, lse, grads, dtype, window, before=7.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_of_large_scores(dtype):
     """Weights that are nearly all one key's, maxima that rise along the row, another scale."""
     q, k, v, _, cu = prompt_case([200, 77], 4, 2, 64, dtype, 5, loud=6.0)
@@ -64,9 +88,10 @@ def test_a_long_prompt(dtype):
         check_backward(q, k, v, do, cu, out, lse, got, dtype, window)
 
 
-def odd_case(dtype, dim=64):
+def odd_case(dtype, dim=64, kh=2):
     """NaN and infinities at late rows, which earlier rows do not see, and in rows of none."""
-    q, k, v, do, cu = prompt_case([150, 70], 4, 2, dim, dtype, 21, before=1, behind=2)
+    lengths = [150, 70] + (SHORT if kh > 2 else [])
+    q, k, v, do, cu = prompt_case(lengths, 2 * kh, kh, dim, dtype, 21, before=1, behind=2)
     nan, inf = float("nan"), float("inf")
     for t in (q, k, v, do):
         t[0], t[-2:] = nan, inf
@@ -79,9 +104,10 @@ def odd_case(dtype, dim=64):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("window", (0, 20))
-@pytest.mark.parametrize("dim", (64, 128, 200))
-def test_what_a_row_does_not_see(dtype, window, dim):
-    q, k, v, _, cu = odd_case(dtype, dim)
+@pytest.mark.parametrize("dim,kh", [(64, 2), (128, 2), (200, 2), (64, 12), (128, 12), (200, 6)])
+def test_what_a_row_does_not_see(dtype, window, dim, kh):
+    """(Few heads, and as many as make a busy call.)"""
+    q, k, v, _, cu = odd_case(dtype, dim, kh)
     out, lse = torch.full(q.shape, 7.0, dtype=dtype, device=DEV), torch.full(q.shape[:2], 7.0, device=DEV)
     kq.kronq_prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), dev(cu), window=window, out=out, lse=lse)
     with np.errstate(invalid="ignore"):
@@ -178,10 +204,10 @@ def test_grad_of_small_and_large_gradients_in_fp16(size):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("dim", (64, 128, 200))
-def test_grad_of_what_a_row_does_not_see(dtype, dim):
+@pytest.mark.parametrize("dim,kh", [(64, 2), (128, 2), (200, 2), (64, 18), (128, 18), (128, 28), (200, 12)])
+def test_grad_of_what_a_row_does_not_see(dtype, dim, kh):
     """A late row's NaN reaches the rows and keys that it has to do with, and no others."""
-    q, k, v, do, cu = prompt_case([150, 70], 4, 2, dim, dtype, 61)
+    q, k, v, do, cu = prompt_case([150, 70] + (SHORT if kh > 2 else []), 2 * kh, kh, dim, dtype, 61)
     args = [t.to(DEV) for t in (q, k, v)]
     clean = kq.kronq_prompt_attention(*args, dev(cu), want_lse=True)
     # row 100: its query; row 130: its gradient; both of query head 1.  Keys behind 130 see neither
@@ -198,14 +224,14 @@ def test_grad_of_what_a_row_does_not_see(dtype, dim):
     rows = bad[0].any(-1)
     want = np.zeros_like(rows)
     want[[100, 130], 1] = True
-    want[140:150, 2:] = True
+    want[140:150, 2:4] = True
     assert np.array_equal(rows, want)
     keys = bad[1].any(-1)
     assert keys[:131, 0].all() and not keys[131:, 0].any()
-    assert keys[:150, 1].all() and not keys[150:].any()
+    assert keys[:150, 1].all() and not keys[150:].any() and not keys[:, 2:].any()
     keys = bad[2].any(-1)
     assert keys[:131, 0].all() and not keys[131:, 0].any()
-    assert not keys[150:].any()
+    assert not keys[150:].any() and not keys[:, 2:].any()
     # dv of keys 101 .. 130 sees only the gradient's one value
     assert not np.delete(bad[2][101:131, 0], 9, axis=-1).any()
     # and what has nothing to do with it is right
