@@ -139,17 +139,19 @@ struct Shared {
 template <typename T, typename F>
 __device__ __forceinline__ void visit(const Row<T>& row, int c0, int c1, bool ends_lo, bool ends_hi, const Shared& sh, F f) {
   constexpr int N = Row<T>::N;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x;
   if (ends_lo && tid < row.head) f(value(row.data[tid]), tid);
   if (ends_hi && tid < row.vocab - row.rest()) f(value(row.data[row.rest() + tid]), row.rest() + tid);
-  for (int w = wave; w < sh.chosen; w += WAVES) {
-    for (int c = c0 + sh.who[w] + NT * lane; c < c1; c += NT * 64) {
-      if (*const_cast<const volatile int*>(&sh.n) > kList) return;
-      float x[N];
-      unpack(row.chunk(c), x, T());
+  // their chunks one behind the other, one a lane
+  const int each = (c1 - c0 + NT - 1) / NT, all = sh.chosen * each;
+  for (int at = tid; at < all; at += NT) {
+    if (*const_cast<const volatile int*>(&sh.n) > kList) return;
+    const int w = at / each, c = c0 + sh.who[w] + NT * (at - w * each);
+    if (c >= c1) continue;
+    float x[N];
+    unpack(row.chunk(c), x, T());
 #pragma unroll
-      for (int i = 0; i < N; ++i) f(x[i], row.index(c) + i);
-    }
+    for (int i = 0; i < N; ++i) f(x[i], row.index(c) + i);
   }
 }
 
@@ -277,7 +279,12 @@ __device__ __forceinline__ void ranked(Shared& sh, int K, F f) {
   for (int i = threadIdx.x; i < n; i += NT) {
     const uint64_t k = sh.list[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += sh.list[j] > k;
+    int j = 0;
+    for (; j + 16 <= n; j += 16) {        // reads in flight together: one behind the other they would be all of the time
+#pragma unroll
+      for (int x = 0; x < 16; ++x) rank += sh.list[j + x] > k;
+    }
+    for (; j < n; ++j) rank += sh.list[j] > k;
     if (rank < K) f(rank, k);
   }
 }
@@ -393,20 +400,23 @@ __global__ __launch_bounds__(NT) void token_logprobs_join(LogprobsArgs a, int se
   if (a.top > 0) {
     if (tid == 0) sh.n = 0;
     __syncthreads();
+    // a segment's last key is reached by `top` of the row's
+    uint64_t least = 1;
+    for (int i = 0; i < segs; ++i) least = max(least, keys[(r * segs + i) * a.top + a.top - 1]);
     for (int i = tid; i < segs * a.top; i += NT) {
       const uint64_t k = keys[r * segs * a.top + i];
-      if (k) sh.list[atomicAdd(&sh.n, 1)] = k;
+      if (k >= least) sh.list[atomicAdd(&sh.n, 1)] = k;
     }
     __syncthreads();
   }
   finish(a, r, row, s, sh);
 }
 
-// Segments of a row: where rows are fewer than the chip's CUs, about two workgroups
-// a CU, of at least 8192 values each; what the join takes fits its list.
+// Segments of a row: where rows are fewer than the chip's CUs, about one workgroup a CU,
+// of at least 8192 values each; what the join takes fits its list.
 int segments(int64_t rows, int64_t vocab) {
   if (rows >= 256) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({kList / kTopMost, (512 + rows - 1) / rows, vocab / 8192}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kList / kTopMost, (256 + rows - 1) / rows, vocab / 8192}));
 }
 
 template <typename T>
@@ -427,7 +437,7 @@ kronq_status logprobs_type(const LogprobsArgs& a, void* ws, hipStream_t s) {
 
 // ---------------------------------------------------------------- gradients
 
-constexpr int kSpan = 16384;              // values of a row that a workgroup takes
+constexpr int kSpan = 4096;               // values of a row that a workgroup takes (6144 x 128256 bf16: 518 us, 16384 620, 2048 589)
 
 // One pass, a read and a write; bound by HBM.  The few places that a target or an
 // alternative names are computed again behind it, all their shares at once.  The
