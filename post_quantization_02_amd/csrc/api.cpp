@@ -192,6 +192,8 @@ static kronq_status kv_view(const char* fn, const kronq_kv_cache* c, const kronq
 // time grows with their square (one head of one token each of up to 60 keys: 1024
 // sequences 33 us, 4096 260 us, 16384 3.2 ms; 2^20 would be minutes for a few heads).
 static constexpr int64_t kAttnSeqs = 1 << 14;
+// workgroups of 256 threads in a launch, whose threads are counted in 32 bits
+static constexpr int64_t kMostGroups = (1 << 24) - 1;
 
 static kronq_status kv_rope(const char* fn, const kronq_rope* r, int32_t dim, RopeView* out) {
   *out = RopeView{};
@@ -702,6 +704,8 @@ kronq_status kronq_rope_tables(float* cos, float* sin, int64_t ld, int64_t first
     return fail(KRONQ_EINVAL, "%s: original must be > 0 and 0 < low < high", fn);
   if (positions == 0) return KRONQ_OK;
   if (!cos || !sin) return fail(KRONQ_EINVAL, "%s: NULL pointer", fn);
+  if (rope_tables_grid(positions, dim) > kMostGroups)
+    return fail(KRONQ_EUNSUPPORTED, "%s: %lld positions of %d pairs", fn, (long long)positions, (int)dim / 2);
   return rope_tables_launch(cos, sin, ld, first, positions, dim, c, (hipStream_t)stream);
 }
 
@@ -729,6 +733,8 @@ kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_hea
     if (in[w].data == out[w].data && (in[w].row != out[w].row || in[w].head != out[w].head))
       return fail(KRONQ_EINVAL, "%s: %s is %s with other strides", fn, names[2 + w], names[w]);
   }
+  if (rotate_grid(rows, (int64_t)q_heads + k_heads, dim, dtype) > kMostGroups)
+    return fail(KRONQ_EUNSUPPORTED, "%s: %lld rows of %d values a head", fn, (long long)rows, (int)dim);
   return rotate_launch(in, out, heads, dtype, rows, dim, pos, r, back, (hipStream_t)stream);
 }
 
@@ -746,7 +752,7 @@ static kronq_status prompt_view(const char* fn, int32_t dtype, int64_t rows, int
   if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(KRONQ_EINVAL, "%s: scale must be finite and > 0", fn);
   if (rows > 0 && seqs > 0 && !cu) return fail(KRONQ_EINVAL, "%s: cu is NULL", fn);
   // tiles of 128 rows, one a sequence more: the launch's workgroups
-  if ((rows / 128 + seqs) * q_heads > INT32_MAX)
+  if ((rows / 128 + seqs) * q_heads > kMostGroups)
     return fail(KRONQ_EUNSUPPORTED, "%s: %d sequences of %d heads", fn, (int)seqs, (int)q_heads);
   *a = PromptArgs{};
   a->cu = cu;
@@ -867,7 +873,7 @@ kronq_status kronq_token_logprobs_grad(const void* logits, int32_t dtype, int64_
   if (d_logp && !targets) return fail(KRONQ_EINVAL, "%s: d_logp without targets", fn);
   if (d_entropy && !entropy) return fail(KRONQ_EINVAL, "%s: d_entropy without entropy", fn);
   if (top > 0 && d_top && !top_ids) return fail(KRONQ_EINVAL, "%s: d_top without top_ids", fn);
-  if (logprobs_grad_grid(rows, vocab) > INT32_MAX)
+  if (logprobs_grad_grid(rows, vocab) > kMostGroups)
     return fail(KRONQ_EUNSUPPORTED, "%s: %lld rows of %lld values", fn, (long long)rows, (long long)vocab);
   const LogprobsGradArgs a{logits, ld, targets, rows, (int)vocab, d_top ? top : 0, lse, entropy, d_logp, d_entropy,
                            top > 0 ? d_top : nullptr, top_ids, out, ld_out};

@@ -11,7 +11,6 @@
 
 #include <cfloat>
 #include <type_traits>
-#include <utility>
 
 #include "kv.h"
 #include "prompt_index.h"
@@ -161,16 +160,6 @@ struct Op<float> {
 
 // Row of a 32 x 32 block that register x holds.
 __device__ constexpr int block_row(int x, int h) { return (x & 3) + 8 * (x >> 2) + 4 * h; }
-
-// f(0), .., f(N - 1), each with a constant.
-template <typename F, int... I>
-__device__ __forceinline__ void prompt_each_of(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void prompt_each(F f) {
-  prompt_each_of(f, std::make_integer_sequence<int, N>{});
-}
 
 // Largest of a column: both halves hold some of its rows.
 __device__ __forceinline__ float both_max(float x) {

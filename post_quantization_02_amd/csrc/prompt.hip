@@ -10,8 +10,6 @@
 // Where there are too few of these for the chip (SPLIT), a workgroup takes 32 rows, and
 // its waves go through every fourth tile each, by themselves; the four parts are joined
 // in LDS.
-#include <utility>
-
 #include "prompt.h"
 
 namespace kronq {

@@ -14,8 +14,6 @@
 // so with a delta that is off the sum is what it is off by, r_i: the first kernel
 // sums it beside B = P K, takes r B off dQ and hands the right delta to the second.
 // (Not for fp32, whose outputs hold it well enough.)
-#include <utility>
-
 #include "prompt.h"
 
 namespace kronq {

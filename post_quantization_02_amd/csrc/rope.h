@@ -13,6 +13,10 @@ constexpr int kRopePairs = 256;           // of a table: they travel as a kernel
 // The dim / 2 frequencies, in fp64 (host).
 void rope_frequencies(const kronq_rope_scaling& c, int dim, double* f);
 
+// Workgroups of a call's launch, for the checks of their number.
+int64_t rope_tables_grid(int64_t positions, int dim);
+int64_t rotate_grid(int64_t rows, int64_t heads, int dim, int32_t dtype);
+
 kronq_status rope_tables_launch(float* cos, float* sin, int64_t ld, int64_t first, int64_t positions, int dim,
                                 const kronq_rope_scaling& c, hipStream_t s);
 

@@ -184,13 +184,20 @@ void rope_frequencies(const kronq_rope_scaling& c, int dim, double* f) {
   }
 }
 
+int64_t rope_tables_grid(int64_t positions, int dim) {
+  return ((positions + kSteps - 1) / kSteps * (dim / 2) + 255) / 256;
+}
+
+int64_t rotate_grid(int64_t rows, int64_t heads, int dim, int32_t dtype) {
+  return (rows * heads * (dim / (dtype == KRONQ_F32 ? 8 : 16)) + 255) / 256;
+}
+
 kronq_status rope_tables_launch(float* cos, float* sin, int64_t ld, int64_t first, int64_t positions, int dim,
                                 const kronq_rope_scaling& c, hipStream_t s) {
   Frequencies fr{};
   rope_frequencies(c, dim, fr.f);
   const int half = dim / 2;
-  const int64_t threads = (positions + kSteps - 1) / kSteps * half;
-  hipLaunchKernelGGL(rope_tables, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, fr, cos, sin, ld, first,
+  hipLaunchKernelGGL(rope_tables, dim3((unsigned)rope_tables_grid(positions, dim)), dim3(256), 0, s, fr, cos, sin, ld, first,
                      positions, half, c.magnitude);
   KQ_LAUNCHED("rope_tables");
   return KRONQ_OK;
@@ -210,8 +217,7 @@ kronq_status rotate_launch(const HeadsView* in, const HeadsView* out, const int*
   a.rows = (int)rows;
   a.dim = dim;
   a.back = back;
-  const int64_t each = dim / (dtype == KRONQ_F32 ? 8 : 16);
-  const int64_t grid = (rows * (heads[0] + heads[1]) * each + 255) / 256;
+  const int64_t grid = rotate_grid(rows, (int64_t)heads[0] + heads[1], dim, dtype);
   switch (dtype) {
     case KRONQ_F32: rotate_type<float>(a, (unsigned)grid, s); break;
     case KRONQ_BF16: rotate_type<bf16_t>(a, (unsigned)grid, s); break;

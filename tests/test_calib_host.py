@@ -121,3 +121,158 @@ def test_log_probabilities_by_hand_and_by_differences():
         step[at] = 1e-6
         assert np.isclose((loss(x + step) - loss(x - step)) / 2e-6, grad[at], rtol=1e-6, atol=1e-8)
     assert (np.abs(grad) <= size + 1e-12).all()
+
+
+# ---------------------------------------------------------------- refusals
+
+OK, EINVAL, EWORKSPACE, EUNSUPPORTED = 0, 1, 4, 5
+P = 0x10000                                              # an aligned address: nothing is launched
+
+
+def heads(data=P, row=512, head=64):
+    return kq._Heads(data, row, head)
+
+
+def rope(cos=P, sin=P, ld=32, positions=10, dim=64, neighbours=0):
+    return kq._Rope(cos, sin, ld, positions, dim, neighbours)
+
+
+def scaling(base=10000.0, factor=1.0, original=100.0, low=1.0, high=4.0, magnitude=1.0, kind=0):
+    return kq._RopeScaling(base, factor, original, low, high, magnitude, kind)
+
+
+@pytest.mark.parametrize("status,change", [
+    (OK, dict(positions=0, cos=None)), (EINVAL, dict(cos=None)), (EINVAL, dict(sin=None)), (EINVAL, dict(dim=3)),
+    (EINVAL, dict(dim=0)), (EINVAL, dict(dim=514)), (EINVAL, dict(ld=31)), (EINVAL, dict(first=-1)),
+    (EINVAL, dict(positions=-1)), (EINVAL, dict(first=2 ** 31, positions=1)), (EINVAL, dict(first=2 ** 62, positions=2 ** 62)),
+    (EINVAL, dict(c=None)), (EINVAL, dict(c=scaling(kind=4))), (EINVAL, dict(c=scaling(kind=-1))),
+    (EINVAL, dict(c=scaling(base=1.0))), (EINVAL, dict(c=scaling(base=math.inf))), (EINVAL, dict(c=scaling(base=math.nan))),
+    (EINVAL, dict(c=scaling(factor=0.0))), (EINVAL, dict(c=scaling(magnitude=math.nan))),
+    (EINVAL, dict(c=scaling(kind=2, low=4.0))), (EINVAL, dict(c=scaling(kind=3, original=0.0))),
+    (EINVAL, dict(c=scaling(kind=3, low=0.0))), (EINVAL, dict(c=scaling(kind=2, high=math.inf))),
+    (EUNSUPPORTED, dict(positions=2 ** 31, dim=512, ld=256)),
+])
+def test_rope_tables_refusals(status, change):
+    a = dict(cos=P, sin=P, ld=32, first=0, positions=5, dim=64, c=scaling())
+    a.update(change)
+    assert kq.load().kronq_rope_tables(a["cos"], a["sin"], a["ld"], a["first"], a["positions"], a["dim"],
+                                       a["c"], None) == status
+
+
+@pytest.mark.parametrize("status,change", [
+    (OK, dict(rows=0, q=None, pos=None)), (EINVAL, dict(qh=0)), (EINVAL, dict(kh=-1)), (EINVAL, dict(dtype=7)),
+    (EINVAL, dict(rows=-1)), (EUNSUPPORTED, dict(rows=2 ** 22 + 1)), (EUNSUPPORTED, dict(rows=2 ** 22, qh=8, kh=9)),
+    (EINVAL, dict(dim=0)), (EUNSUPPORTED, dict(dim=72)), (EUNSUPPORTED, dict(dim=528)), (EINVAL, dict(rope=None)),
+    (EINVAL, dict(rope=rope(cos=None))), (EINVAL, dict(rope=rope(dim=80, ld=40))), (EUNSUPPORTED, dict(rope=rope(dim=24))),
+    (EINVAL, dict(rope=rope(ld=30))), (EINVAL, dict(pos=None)), (EINVAL, dict(q=None)), (EINVAL, dict(q=heads(P + 8))),
+    (EINVAL, dict(q=heads(row=516))), (EINVAL, dict(qo=heads(head=32))), (EINVAL, dict(k=None)), (EINVAL, dict(ko=None)),
+    (EINVAL, dict(qo=heads(row=1024))), (EINVAL, dict(ko=heads(2 * P, row=1024))),
+    (EUNSUPPORTED, dict(rows=2 ** 22, qh=15, kh=1, dtype=0, dim=512, q=heads(row=8192, head=512), k=heads(2 * P, 8192, 512),
+                        qo=heads(row=8192, head=512), ko=heads(2 * P, 8192, 512))),
+])
+def test_rotate_refusals(status, change):
+    a = dict(q=heads(), qh=8, k=heads(2 * P), kh=2, dtype=1, rows=4, dim=64, pos=P, rope=rope(), back=0,
+             qo=heads(), ko=heads(2 * P))
+    a.update(change)
+    assert kq.load().kronq_rotate(a["q"], a["qh"], a["k"], a["kh"], a["dtype"], a["rows"], a["dim"], a["pos"], a["rope"],
+                                  a["back"], a["qo"], a["ko"], None) == status
+
+
+PROMPT = [
+    (OK, dict(rows=0, q=None, cu=None)), (OK, dict(seqs=0, q=None, cu=None)), (EINVAL, dict(dtype=3)), (EINVAL, dict(rows=-1)),
+    (EINVAL, dict(heads=0)), (EINVAL, dict(qh=7)), (EINVAL, dict(qh=0)), (EINVAL, dict(dim=0)), (EUNSUPPORTED, dict(dim=60)),
+    (EUNSUPPORTED, dict(dim=264)), (EINVAL, dict(seqs=-1)), (EUNSUPPORTED, dict(seqs=2 ** 14 + 1)), (EINVAL, dict(cu=None)),
+    (EINVAL, dict(scale=0.0)), (EINVAL, dict(scale=-1.0)), (EINVAL, dict(scale=math.inf)), (EINVAL, dict(scale=math.nan)),
+    (EINVAL, dict(window=-1)), (EUNSUPPORTED, dict(rows=2 ** 22 + 1)), (EUNSUPPORTED, dict(rows=2 ** 22, qh=32)),
+    (EINVAL, dict(q=None)), (EINVAL, dict(k=None)), (EINVAL, dict(v=None)), (EINVAL, dict(out=None)),
+    (EINVAL, dict(q=heads(P + 4))), (EINVAL, dict(v=heads(row=257))), (EINVAL, dict(k=heads(head=56))),
+    (EUNSUPPORTED, dict(q=heads(row=2 ** 22 + 8))), (EUNSUPPORTED, dict(seqs=2 ** 14, qh=1024, heads=1024)),
+]
+
+
+def prompt_args(change):
+    a = dict(q=heads(), k=heads(), v=heads(), out=heads(), dout=heads(), dtype=1, rows=5, qh=8, heads=2, dim=64, cu=P, seqs=2,
+             scale=0.125, window=0, lse=P, dq=heads(), dk=heads(), dv=heads(), ws=P, bytes=1 << 40)
+    a.update(change)
+    return a
+
+
+@pytest.mark.parametrize("status,change", PROMPT)
+def test_prompt_attention_refusals(status, change):
+    a = prompt_args(change)
+    got = kq.load().kronq_prompt_attention(a["q"], a["k"], a["v"], a["dtype"], a["rows"], a["qh"], a["heads"], a["dim"], a["cu"],
+                                           a["seqs"], a["scale"], a["window"], a["out"], a["lse"], None)
+    assert got == status
+
+
+@pytest.mark.parametrize("status,change", PROMPT + [
+    (EINVAL, dict(lse=None)), (EINVAL, dict(dout=None)), (EINVAL, dict(dq=None)), (EINVAL, dict(dk=None)), (EINVAL, dict(dv=None)),
+    (EINVAL, dict(dv=heads(P + 2))), (EWORKSPACE, dict(ws=None)), (EWORKSPACE, dict(bytes=5 * 8 * 8 - 1)), (EINVAL, dict(ws=P + 8)),
+])
+def test_prompt_attention_grad_refusals(status, change):
+    a = prompt_args(change)
+    got = kq.load().kronq_prompt_attention_grad(a["dout"], a["q"], a["k"], a["v"], a["out"], a["lse"], a["dtype"], a["rows"],
+                                                a["qh"], a["heads"], a["dim"], a["cu"], a["seqs"], a["scale"], a["window"],
+                                                a["dq"], a["dk"], a["dv"], a["ws"], a["bytes"], None)
+    assert got == status
+
+
+def test_prompt_attention_grad_ws():
+    ws = kq.load().kronq_prompt_attention_grad_ws
+    assert ws(5, 8) == 5 * 8 * 2 * 4
+    assert [ws(0, 8), ws(5, 0), ws(2 ** 22 + 1, 1), ws(2 ** 22, 17), ws(1, 65536)] == [0] * 5
+
+
+@pytest.mark.parametrize("status,change", [
+    (OK, dict(rows=0, logits=None)), (EINVAL, dict(dtype=3)), (EINVAL, dict(rows=-1)), (EINVAL, dict(vocab=0)), (EINVAL, dict(ld=99)),
+    (EINVAL, dict(top=-1)), (EINVAL, dict(vocab=50, ld=50, top=51)), (EUNSUPPORTED, dict(top=65)), (EUNSUPPORTED, dict(rows=2 ** 22 + 1)),
+    (EUNSUPPORTED, dict(vocab=2 ** 24 + 1, ld=2 ** 25)), (EINVAL, dict(logits=None)), (EINVAL, dict(logits=P + 1)),
+    (EINVAL, dict(targets=None)), (EINVAL, dict(logp=None)), (EINVAL, dict(top_logp=None)), (EINVAL, dict(top_ids=None)),
+    (EWORKSPACE, dict(vocab=128256, ld=128256, ws=None)), (EWORKSPACE, dict(vocab=128256, ld=128256, bytes=100)),
+    (EINVAL, dict(vocab=128256, ld=128256, ws=P + 4)),
+])
+def test_token_logprobs_refusals(status, change):
+    a = dict(logits=P, dtype=1, rows=4, vocab=100, ld=100, targets=P, logp=P, lse=P, entropy=P, top=3, top_logp=P, top_ids=P, ws=P,
+             bytes=1 << 40)
+    a.update(change)
+    assert kq.load().kronq_token_logprobs(a["logits"], a["dtype"], a["rows"], a["vocab"], a["ld"], a["targets"], a["logp"],
+                                          a["lse"], a["entropy"], a["top"], a["top_logp"], a["top_ids"], a["ws"], a["bytes"],
+                                          None) == status
+
+
+@pytest.mark.parametrize("status,change", [
+    (OK, dict(rows=0, logits=None, out=None)), (EINVAL, dict(dtype=-1)), (EINVAL, dict(ld=99)), (EINVAL, dict(ld_out=99)),
+    (EINVAL, dict(lse=None)), (EINVAL, dict(out=None)), (EINVAL, dict(out=2 * P + 1)), (EINVAL, dict(out=P, ld_out=128)),
+    (EINVAL, dict(targets=None)), (EINVAL, dict(entropy=None)), (EINVAL, dict(top_ids=None)), (EUNSUPPORTED, dict(top=65)),
+    (EUNSUPPORTED, dict(rows=2 ** 22, vocab=2 ** 24, ld=2 ** 24, ld_out=2 ** 24)),
+])
+def test_token_logprobs_grad_refusals(status, change):
+    a = dict(logits=P, dtype=1, rows=4, vocab=100, ld=100, targets=P, lse=P, entropy=P, d_logp=P, d_entropy=P, top=3, top_ids=P,
+             d_top=P, out=2 * P, ld_out=100)
+    a.update(change)
+    assert kq.load().kronq_token_logprobs_grad(a["logits"], a["dtype"], a["rows"], a["vocab"], a["ld"], a["targets"], a["lse"],
+                                               a["entropy"], a["d_logp"], a["d_entropy"], a["top"], a["top_ids"], a["d_top"],
+                                               a["out"], a["ld_out"], None) == status
+
+
+def test_the_binding_refuses():
+    x = torch.zeros(3, 2, 64)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        kq.kronq_prompt_attention(x, x, x, cu)           # on the host
+    with pytest.raises(ValueError):
+        kq.kronq_prompt_attention(x.double(), x, x, cu)
+    with pytest.raises(ValueError):
+        kq.kronq_prompt_attention_grad(x, x[0], x, x, x, x, cu)
+    with pytest.raises(ValueError):
+        kq.kronq_token_logprobs(torch.zeros(3, 5))
+    with pytest.raises(ValueError):
+        kq.kronq_token_logprobs(torch.zeros(3, 5, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        kq.kronq_token_logprobs_grad(torch.zeros(3, 5), None, torch.zeros(3))
+    with pytest.raises(ValueError):
+        kq.kronq_rope_tables(4, 64, scaling="more")
+    with pytest.raises(ValueError):
+        kq.kronq_rope_tables(4, 64, device="cpu")
+    with pytest.raises(ValueError):
+        kq.kronq_rotate(x, None, cu, None)
