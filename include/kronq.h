@@ -645,7 +645,8 @@ kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t row
  *                        (b - a at least 0.001)
  *   dim: even, 2 .. 512; first >= 0, first + positions <= 2^31; base > 1, factor > 0,
  *   original > 0 and 0 < low < high where they are used, all finite (KRONQ_EINVAL
- *   otherwise).  kronq_rope takes the tables (dim a multiple of 16).
+ *   otherwise); fewer than 2^37 pairs of a cosine and a sine (KRONQ_EUNSUPPORTED).
+ *   kronq_rope takes the tables (dim a multiple of 16).
  * kronq_rotate: q and k (NULL with k_heads 0: none) turned as kronq_rope describes,
  *   by the angles of pos (device int32[rows]); with `back` by the transpose, a' =
  *   a cos + b sin, b' = b cos - a sin: the gradient of the rotation.  Values of a head
@@ -654,7 +655,8 @@ kronq_status kronq_kv_attention(const kronq_heads* q, int32_t dtype, int64_t row
  *   sequence: its outputs are left as they were.  One whose position has no row in
  *   the tables gives NaN.  dim (a head's): a multiple of 16 up to 512
  *   (KRONQ_EUNSUPPORTED otherwise).  Rows, heads, types and strides as for
- *   kronq_kv_append.  Arithmetic is fp32, rounded once to dtype.
+ *   kronq_kv_append, and fewer than 2^37 bytes of values (KRONQ_EUNSUPPORTED).
+ *   Arithmetic is fp32, rounded once to dtype.
  * One launch each, no host synchronization, no memset: may be captured in a HIP
  * graph (the tables' frequencies are the captured call's, pos is read anew).
  * ------------------------------------------------------------------------- */
@@ -694,20 +696,22 @@ kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_hea
  *   Row strides at most 2^22 elements.
  * dim: a multiple of 8 up to 256 (64, 128 and 256 as they are, others in the next larger
  *   of these); q_heads a multiple of heads; at most 2^22 rows, 2^26 rows x heads, 2^14
- *   sequences (KRONQ_EUNSUPPORTED otherwise).
+ *   sequences, fewer than 2^24 of (rows / 128 + seqs) x q_heads (KRONQ_EUNSUPPORTED
+ *   otherwise).
  * scale: > 0 and finite; scores, and lse / scale, have to be numbers that fp32 holds.
  * A row of no sequence is not read, and its outputs are left as they were.  Nothing
  * outside the caller's buffers is touched whatever cu holds.  What k, v (grad: q and
  * dout too) hold in rows that a row does not see has no part in its outputs, be it a NaN
  * or an infinity; what it sees of these reaches it as in the formula (in dq and dk as a
- * NaN).
+ * NaN), but that an infinity or NaN of v or dout times a weight that fp32 holds as 0 may
+ * come out as itself or as a NaN.
  * Products of KRONQ_F32 are fp32's own; of the others the matrix cores', with weights
  * and ds rounded to dtype (for KRONQ_F16 held times a power of two that follows the
  * largest of a row's or a key's, so that small gradients keep their precision).  Scores,
  * statistics and sums are fp32.
  * ws: kronq_prompt_attention_grad_ws(rows, q_heads) bytes, written before it is read;
  * calls that overlap in time need one each.
- * One launch (grad: three), no host synchronization, no memset, no atomics: may be
+ * One launch (grad: two), no host synchronization, no memset, no atomics: may be
  * captured in a HIP graph, replays read cu anew, and equal calls give equal bits.
  */
 kronq_status kronq_prompt_attention(const kronq_heads* q, const kronq_heads* k, const kronq_heads* v,
@@ -747,8 +751,8 @@ kronq_status kronq_prompt_attention_grad(const kronq_heads* dout, const kronq_he
  *   twice.  A row of lse = -inf gives 0; a target of at least vocab NaN.  out: rows x
  *   vocab of dtype, leading dimension ld_out; it may be logits itself with ld_out = ld,
  *   else they must not overlap.  Nothing behind a row's vocab values is written.
- * Sums are fp32 relative to the row's maximum.  rows at most 2^22, vocab at most 2^24
- * (KRONQ_EUNSUPPORTED otherwise).  At most two launches, no host synchronization, no
+ * Sums are fp32 relative to the row's maximum.  rows at most 2^22, vocab at most 2^24,
+ * of gradients fewer than 2^36 values (KRONQ_EUNSUPPORTED otherwise).  At most two launches, no host synchronization, no
  * memset: may be captured in a HIP graph; equal calls give equal bits.
  */
 size_t kronq_token_logprobs_ws(int64_t rows, int64_t vocab, int32_t top);

@@ -332,7 +332,10 @@ __device__ __forceinline__ void finish(const LogprobsArgs& a, int64_t r, const R
   }
 }
 
-// A workgroup takes a segment of a row, or (segs 1) a row.  Bound by HBM.
+// A workgroup takes a segment of a row, or (segs 1) a row; four pieces a thread are in
+// flight.  Bound by HBM: 4095 x 32000 in fp32 with entropy and five alternatives 98 us,
+// 5.3 TB/s.  Few rows are bound by the steps that follow one another: 40 x 128256 in
+// bf16, 20 alternatives, 12 us and 7 of the join, where the bytes take 2.
 template <typename T, bool ENTROPY>
 __global__ __launch_bounds__(NT) void token_logprobs(LogprobsArgs a, int segs, Part* __restrict__ parts,
                                                      uint64_t* __restrict__ keys) {
@@ -439,7 +442,8 @@ kronq_status logprobs_type(const LogprobsArgs& a, void* ws, hipStream_t s) {
 
 constexpr int kSpan = 4096;               // values of a row that a workgroup takes (6144 x 128256 bf16: 518 us, 16384 620, 2048 589)
 
-// One pass, a read and a write; bound by HBM.  The few places that a target or an
+// One pass, a read and a write; bound by HBM: 6144 x 128256 in bf16 505 us, 6.2 TB/s.
+// An output is rounded to its type once.  The few places that a target or an
 // alternative names are computed again behind it, all their shares at once.  The
 // logits may be where the gradients go: those places are read before the pass.
 template <typename T>

@@ -22,7 +22,8 @@ namespace {
 // and of one step from the library, then one turn a step in fp64, four operations
 // where a sine and a cosine cost above a hundred.  kSteps turns are off by at most
 // kSteps 2^-52, far below the result's 2^-24, relative to a small sine as well (its
-// terms then have one sign).
+// terms then have one sign).  Bound by the writes: 131072 positions of 64 pairs 12.2 us,
+// 5.5 TB/s.
 constexpr int kSteps = 32;
 
 struct Frequencies { double f[kRopePairs]; };
