@@ -698,7 +698,8 @@ kronq_status kronq_rotate(const kronq_heads* q, int32_t q_heads, const kronq_hea
  *   of these); q_heads a multiple of heads; at most 2^22 rows, 2^26 rows x heads, 2^14
  *   sequences, fewer than 2^24 of (rows / 128 + seqs) x q_heads (KRONQ_EUNSUPPORTED
  *   otherwise).
- * scale: > 0 and finite; scores, and lse / scale, have to be numbers that fp32 holds.
+ * scale: > 0 and finite; scores (scale q . k) within 2^30, lse / scale a number that fp32
+ * holds.
  * A row of no sequence is not read, and its outputs are left as they were.  Nothing
  * outside the caller's buffers is touched whatever cu holds.  What k, v (grad: q and
  * dout too) hold in rows that a row does not see has no part in its outputs, be it a NaN
