@@ -505,13 +505,17 @@ kronq_status launch_keys(const PromptArgs& a, hipStream_t s) {
 }
 
 // SPLIT up to that many workgroups of 128 rows (keys).  Both kernels' time, us, with the
-// one's work split and whole: rows, bf16, dim 128, 64 workgroups 273 and 374, 192 197 and
-// 188, 320 344 and 310; dim 256, 64 381 and 442.  Keys, bf16, dim 128, 48 95 and 188, 176
-// 235 and 380, 320 428 and 450; dim 64, 232 183 and 338, 680 495 and 509; dim 256, 116 826
-// and 851; fp32, dim 128, 344 2254 and 2382, 700 8716 and 7999.
-constexpr int64_t kRowsSplitUpTo = 128;
+// one's work split and whole: rows, bf16, dim 128, 128 workgroups 86 and 99, 192 125 and
+// 123, 288 58 and 42; dim 256, 64 285 and 357, 256 1317 and 846; dim 64, 192
+// 60 and 71 or (shorter sequences) 42 and 41, 288 33 and 27; fp32, dim 64, 192 109 and
+// 116, 288 76 and 70; dim 128, 96 271 and 473.  Keys, split and the way that follows,
+// bf16, dim 128, 96 169 and 260, 160 357 and 427, 192 229 and 226, 256 325 and 295; dim 64,
+// 256 174 and 197, 384 295 and 294, 760 825 and 784; dim 256, 116 826 and 851; fp32, dim
+// 128, 344 2254 and 2382, 700 8716 and 7999.
 template <typename T, int D>
-constexpr int64_t kKeysSplitUpTo = sizeof(T) == 2 && D == 64 ? 640 : 384;
+constexpr int64_t kRowsSplitUpTo = D == 256 ? 64 : sizeof(T) == 4 || D == 64 ? 192 : 128;
+template <typename T, int D>
+constexpr int64_t kKeysSplitUpTo = sizeof(T) == 2 && D == 128 ? 192 : 384;
 // Eight waves up to that many (fp32 and heads of 256 have no room for them).  Both kernels'
 // time, us, eight and four: dim 128, 672 workgroups 583 and 719 and (longer sequences) 1374
 // and 1534, 1340 1598 and 1530; dim 64, 680 470 and 506, 1360 923 and 830.
@@ -523,7 +527,7 @@ kronq_status launch_dim(const PromptArgs& a, hipStream_t s) {
   kronq_status st;
   // fp32 heads of 256 have no room for four waves' tiles
   if constexpr (!(sizeof(T) == 4 && D == 256)) {
-    st = units * a.heads * a.share <= kRowsSplitUpTo ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
+    st = units * a.heads * a.share <= kRowsSplitUpTo<T, D> ? launch_rows<T, D, true>(a, s) : launch_rows<T, D, false>(a, s);
     if (st) return st;
     if (units * a.heads <= kKeysSplitUpTo<T, D>) return launch_keys<T, D, kSplit>(a, s);
     if constexpr (sizeof(T) == 2 && D <= 128)

@@ -104,7 +104,7 @@ def odd_case(dtype, dim=64, kh=2):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("window", (0, 20))
-@pytest.mark.parametrize("dim,kh", [(64, 2), (128, 2), (200, 2), (64, 12), (128, 12), (200, 6)])
+@pytest.mark.parametrize("dim,kh", [(64, 2), (128, 2), (200, 2), (64, 12), (128, 12), (200, 6), (64, 36), (128, 36), (200, 12)])
 def test_what_a_row_does_not_see(dtype, window, dim, kh):
     """(Few heads, and as many as make a busy call.)"""
     q, k, v, _, cu = odd_case(dtype, dim, kh)
