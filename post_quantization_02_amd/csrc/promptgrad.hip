@@ -13,7 +13,8 @@
 // a row's weight dP - delta is small beside that rounding.  The rows of dS sum to 0,
 // so with a delta that is off the sum is what it is off by, r_i: the first kernel
 // sums it beside B = P K, takes r B off dQ and hands the right delta to the second.
-// (Not for fp32, whose outputs hold it well enough.)
+// (Not for fp32, whose outputs hold it well enough.)  A row that sees one key has dS = 0,
+// not what two ways to sum dO . V differ by (times 0: what is not a number stays).
 //
 // Bound by the matrix cores and the vector pipes, which overlap little: 9807 rows of 8
 // sequences, 32 heads of 128 on 8, bf16, 304 + 322 us, the matrix cores busy 36 and 32 %
@@ -213,12 +214,13 @@ __global__ __launch_bounds__(NT, SPLIT || D == 256 || (D == 128 && sizeof(T) == 
         rarely();
         const int from_key = (int)hidden(row - k0 - 4 * h);
         const uint32_t fine = hidden(~lds.odd[slot] >> (4 * h));
+        const float alone = row == 0 || a.window == 1 ? 0.0f : 1.0f;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int r = block_row(x, 0);
           const bool in = r <= from_key && r > from_key - a.window && (fine >> r & 1);
           w[x] = in ? w[x] : 0.0f;
-          u[x] = in ? u[x] : 0.0f;
+          u[x] = in ? u[x] * alone : 0.0f;
         }
       }
       if constexpr (FIX) {
@@ -411,8 +413,9 @@ __device__ __forceinline__ void keys_grad(const PromptArgs& a, KeysLds<T, D, DN,
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const bool in = block_row(x, 0) >= from_row && block_row(x, 0) < from_row + a.window;
+          const bool alone = block_row(x, 0) == from_row && (key == 0 || a.window == 1);
           w[x] = in ? w[x] : 0.0f;
-          u[x] = in ? u[x] : 0.0f;
+          u[x] = in ? u[x] * (alone ? 0.0f : 1.0f) : 0.0f;
         }
       }
       fit_p.scale(w, dv);

@@ -369,3 +369,15 @@ def test_calibration_pass(dtype, neighbours):
     assert abs(loss - rloss) < bound * (abs(rloss) + rows)
     for a, b in zip(grams, exact):
         assert np.linalg.norm(f64(a) - b) < bound * np.linalg.norm(b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,dim,window", [([1, 1, 1], 64, 0), ([1] * 70, 128, 0), ([50, 3], 64, 1), ([40], 256, 1)])
+def test_grad_of_rows_that_see_themselves(lengths, dim, window, dtype):
+    """A weight of 1 whatever the scores are: nothing goes back to q and k, all of it to v."""
+    q, k, v, do, cu = prompt_case(lengths, 4, 2, dim, dtype, 91)
+    args = [t.to(DEV) for t in (q, k, v)]
+    out, lse = kq.kronq_prompt_attention(*args, dev(cu), window=window, want_lse=True)
+    dq, dk, dv = kq.kronq_prompt_attention_grad(do.to(DEV), *args, out, lse, dev(cu), window=window)
+    assert not dq.any() and not dk.any()
+    check_backward(q, k, v, do, cu, out, lse, (dq, dk, dv), dtype, window)
