@@ -17,8 +17,8 @@
 // not what two ways to sum dO . V differ by (times 0: what is not a number stays).
 //
 // Bound by the matrix cores and the vector pipes, which overlap little: 9807 rows of 8
-// sequences, 32 heads of 128 on 8, bf16, 304 + 322 us, the matrix cores busy 36 and 32 %
-// of the time.  Of the eight products five are the formulas' (460 TFLOP/s); S and dP
+// sequences, 32 heads of 128 on 8, bf16, 305 + 320 us, the matrix cores busy 37 and 34 %
+// of the time.  Of the eight products five are the formulas' (480 TFLOP/s); S and dP
 // twice and B are what the two kernels and the right delta cost.  P and dS are rounded
 // to the operands' type, half a step of it each, which makes dq and dk up to 1.6 times
 // as far off as a plain form in fp32 on the same inputs that rounds its results only; dS
